@@ -422,6 +422,127 @@ typedef struct {
 moe_status_t expert_cache_timeline(moe_cache_t* cache, int enable, int max_marks);
 moe_status_t expert_cache_timeline_read(moe_cache_t* cache, moe_cache_timeline_t* out);
 
+/* ------------------------------------------------------------ attention half
+ * What stands between two routed layers of a decoder block with latent
+ * attention (colibri summary, "Principales fonctionnalites": q/kv-LoRA,
+ * partial interleaved rotary positions, one compressed key/value vector of
+ * 576 values per token shared by 64 heads, kv_b absorption): the residual
+ * norm, the 8-bit projections, the latent cache and attention over it.
+ *
+ * bf16 tensors are passed as uint16_t bits, 8-bit tensors are E4M3 bytes (no
+ * infinities, largest value 448).  Strides count elements; the innermost
+ * dimension is contiguous unless a stride is given for it.  Sums, norms and
+ * softmax statistics are fp32; every output is rounded once.  Every call is
+ * asynchronous and safe to capture in a graph; device-side metadata (lengths,
+ * page tables, slots, positions) is never read by the host, and entries that
+ * point outside their tensor are skipped as stated, not followed.  Calls of 0
+ * tokens are no-ops. */
+enum { MOE_BF16 = 0, MOE_F32 = 1 };
+
+/* moe_add_rmsnorm: h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight,
+ * for T rows of H <= 32768 columns.  The statistics use h before rounding.
+ * d_residual may be NULL.  d_sum (or NULL) receives h in the residual's type
+ * (x's without one) and may be d_residual itself.  d_y (or NULL) receives y
+ * in bf16.  d_q (or NULL) receives y in 8 bits with one scale per 128
+ * columns, the largest magnitude / 448 (at least 1e-12; NaN for a group that
+ * holds one), at d_scale[t * scale_stride_t + group * scale_stride_g].  With
+ * scale_stride_t = 1 the layout is the one moe_fp8_linear reads fastest.
+ * 16-byte accesses are used when all rows start on 16 bytes and H is a
+ * multiple of 8; any other layout works, more slowly. */
+moe_status_t moe_add_rmsnorm(const void* d_x, int x_type, int64_t x_stride, const void* d_residual,
+                             int residual_type, int64_t residual_stride, const void* d_weight, int weight_type,
+                             int T, int H, float eps, void* d_sum, int64_t sum_stride, uint16_t* d_y,
+                             int64_t y_stride, uint8_t* d_q, int64_t q_stride, float* d_scale,
+                             int64_t scale_stride_t, int64_t scale_stride_g, void* stream);
+
+/* moe_fp8_linear: out[m][n] = sum_b a_scale[m][b] w_scale[n / 128][b]
+ * sum_{k in b} a[m][k] w[n][k] over blocks b of 128 inner columns (the last
+ * may be short): a [M][K], w [N][K], a_scale at m * as_stride_m + b *
+ * as_stride_b, w_scale [ceil(N / 128)][ceil(K / 128)] with row stride
+ * ws_stride, out [M][N] bf16 or fp32 (out_type).  K and the strides of a and
+ * w are multiples of 16, both pointers 16-byte aligned (else
+ * MOE_EUNSUPPORTED).  The products of one block are summed by the matrix
+ * unit (relative error about 1e-5 of a block's sum), the blocks in fp32. */
+moe_status_t moe_fp8_linear(const uint8_t* d_a, int64_t a_stride, const float* d_a_scale, int64_t as_stride_m,
+                            int64_t as_stride_b, const uint8_t* d_w, int64_t w_stride, const float* d_w_scale,
+                            int64_t ws_stride, int M, int N, int K, void* d_out, int out_type, int64_t out_stride,
+                            void* stream);
+
+/* moe_head_linear: out[t][h][n] = sum_k x[t][h][k] w[h][n][k], bf16; w is
+ * contiguous.  The absorbed form of latent attention applies it to the
+ * queries before (w = the key expansion, transposed per head) and to the
+ * outputs after (w = the value expansion).  K a multiple of 8, N of 4, x
+ * strides of 8, out strides of 4; x and w 16-byte aligned, out 8-byte. */
+moe_status_t moe_head_linear(const uint16_t* d_x, int64_t x_stride_t, int64_t x_stride_h, const uint16_t* d_w, int T,
+                             int heads, int K, int N, uint16_t* d_out, int64_t out_stride_t, int64_t out_stride_h,
+                             void* stream);
+
+/* moe_latent_append: the write side of the latent cache.  Token t's row of
+ * d_kv holds rank latent values and rope position values; the latent is
+ * normed (root mean square, weight, eps), the position part rotated (pairs of
+ * neighbouring columns 2i, 2i + 1) by row positions[t] of d_table
+ * [n_positions][rope] (cosines of the rope / 2 pairs, then sines), and both
+ * are written to row slots[t] of d_cache [n_slots][rank + rope].  A slot
+ * outside [0, n_slots) writes no row; a position outside the table rotates to
+ * NaN.  Two tokens must not share a slot.  d_cache may be NULL (d_slots
+ * then unused).  Further outputs, each optional: d_q_rope [T][heads][rope]
+ * rotated into d_q_out (which may be d_q_rope itself); d_lat_q / d_lat_scale:
+ * the normed latent in 8 bits as in moe_add_rmsnorm (input of the key/value
+ * expansion); d_key [T][rope]: a copy of the rotated position part.
+ * rank <= 2048; rank, rope and all bf16 strides multiples of 8, pointers
+ * 16-byte aligned (d_lat_q 8-byte). */
+moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const void* d_weight, int weight_type,
+                               float eps, int rank, int rope, const float* d_table, int n_positions,
+                               const int32_t* d_positions, const int64_t* d_slots, int T, uint16_t* d_cache,
+                               int64_t n_slots, const uint16_t* d_q_rope, int heads, int64_t q_stride_t,
+                               int64_t q_stride_h, uint16_t* d_q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                               uint8_t* d_lat_q, int64_t lat_stride, float* d_lat_scale, int64_t ls_stride_t,
+                               int64_t ls_stride_g, uint16_t* d_key, int64_t key_stride, void* stream);
+
+/* moe_latent_attention: attention over the paged latent cache, absorbed form.
+ * d_q [T][heads][rank + rope] (queries already in the latent space, and their
+ * rotated position part); d_cache [n_pages] pages of page_size rows of rank +
+ * rope values, page_stride elements apart; sequence b has lens[b] rows
+ * (including its new tokens') on pages d_pages[b * pages_stride + i], i <
+ * pages_per_seq.  Its new tokens are rows d_cu_q[b] .. d_cu_q[b + 1] of d_q
+ * (d_cu_q NULL: T / B each) and take its last positions.
+ *   out[t][h] = sum_j softmax_j(scale q[t][h] . c_j) c_j[:rank]
+ * over the rows a token sees: all before the sequence's first new token, and
+ * of the new ones, the i-th and its predecessors for token i, or with d_tree
+ * those whose bit is set in the 64-bit d_tree[t] (bit j = the sequence's j-th
+ * new token; a token's own bit is not implied; tokens past 64 are unseen).
+ * Rows on a page index outside [0, n_pages) or past the table are unseen.  A
+ * token that sees nothing gets zeros; what unseen rows hold (NaN included)
+ * does not matter unless another token of the same sequence sees them.
+ * max_q and max_len bound the new tokens and rows of a sequence (they size
+ * the launch and the workspace only).  rank 512 or 256 with rope 64; scale
+ * positive.  moe_latent_attention_workspace: device bytes needed, 256-byte
+ * aligned; the buffer's contents need not be kept or cleared. */
+size_t moe_latent_attention_workspace(int B, int max_q, int heads, int rank, int max_len);
+moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, int T, int heads,
+                                  int rank, int rope, const uint16_t* d_cache, int n_pages, int page_size,
+                                  int64_t page_stride, const int32_t* d_pages, int64_t pages_stride,
+                                  int pages_per_seq, const int32_t* d_lens, int B, const int32_t* d_cu_q, int max_q,
+                                  int max_len, const int64_t* d_tree, float scale, uint16_t* d_out,
+                                  int64_t out_stride_t, int64_t out_stride_h, void* d_ws, size_t ws_bytes,
+                                  void* stream);
+
+/* moe_prompt_attention: the expanded form, for prompts.  d_q
+ * [Tq][heads][nope + rope], d_k [Tk][heads][nope], d_k_rope [Tk][rope] (shared
+ * by the heads), d_v [Tk][heads][vdim], out [Tq][heads][vdim]; sequence b has
+ * queries d_cu_q[b] .. d_cu_q[b + 1] and keys d_cu_k[b] .. d_cu_k[b + 1].
+ * causal != 0: its i-th query of n sees keys up to i + (keys - n) (the
+ * queries are the last positions); else all.  A query that sees nothing gets
+ * zeros.  (nope, rope, vdim) in {(64, 64, 64), (128, 64, 128),
+ * (192, 64, 256)}; strides multiples of 8 and pointers 16-byte aligned;
+ * scale positive.  max_q bounds the queries of a sequence. */
+moe_status_t moe_prompt_attention(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* d_k,
+                                  int64_t k_stride_t, int64_t k_stride_h, const uint16_t* d_k_rope,
+                                  int64_t kr_stride_t, const uint16_t* d_v, int64_t v_stride_t, int64_t v_stride_h,
+                                  int Tq, int Tk, int heads, int nope, int rope, int vdim, const int32_t* d_cu_q,
+                                  const int32_t* d_cu_k, int B, int max_q, int causal, float scale, uint16_t* d_out,
+                                  int64_t out_stride_t, int64_t out_stride_h, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

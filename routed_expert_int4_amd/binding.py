@@ -20,6 +20,8 @@ MOE_OK, MOE_EINVAL, MOE_ENOSLOT, MOE_EHIP, MOE_EUNSUPPORTED = 0, -1, -2, -3, -4
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_l = ctypes.c_int64
+_f = ctypes.c_float
 
 
 class MoeConfig(ctypes.Structure):
@@ -95,6 +97,16 @@ _SIGNATURES = {
     "expert_cache_replay_prefetch": ([_i, _i, _i, _vp, _vp, _i, _i, _vp, _i, ctypes.POINTER(ctypes.c_uint64)], _i),
     "expert_cache_timeline": ([_vp, _i, _i], _i),
     "expert_cache_timeline_read": ([_vp, ctypes.POINTER(MoeCacheTimeline)], _i),
+    "moe_add_rmsnorm": ([_vp, _i, _l, _vp, _i, _l, _vp, _i, _i, _i, _f, _vp, _l, _vp, _l, _vp, _l, _vp, _l, _l, _vp], _i),
+    "moe_fp8_linear": ([_vp, _l, _vp, _l, _l, _vp, _l, _vp, _l, _i, _i, _i, _vp, _i, _l, _vp], _i),
+    "moe_head_linear": ([_vp, _l, _l, _vp, _i, _i, _i, _i, _vp, _l, _l, _vp], _i),
+    "moe_latent_append": ([_vp, _l, _vp, _i, _f, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _l, _vp, _i, _l, _l, _vp, _l, _l,
+                           _vp, _l, _vp, _l, _l, _vp, _l, _vp], _i),
+    "moe_latent_attention_workspace": ([_i] * 5, _sz),
+    "moe_latent_attention": ([_vp, _l, _l, _i, _i, _i, _i, _vp, _i, _i, _l, _vp, _l, _i, _vp, _i, _vp, _i, _i, _vp, _f,
+                              _vp, _l, _l, _vp, _sz, _vp], _i),
+    "moe_prompt_attention": ([_vp, _l, _l, _vp, _l, _l, _vp, _l, _vp, _l, _l] + [_i] * 6 + [_vp, _vp, _i, _i, _i, _f,
+                              _vp, _l, _l, _vp], _i),
 }
 
 

@@ -1,0 +1,304 @@
+// Product of 8-bit (E4M3) activations and weights with block scales:
+//   out[m][n] = sum_b a_scale[m][b] w_scale[n / 128][b] sum_{k in block b} A[m][k] W[n][k]
+// over blocks b of 128 inner columns.
+//
+// One matrix instruction (16 x 16 x 128) covers one block of 128 exactly, so
+// each one starts from zero and its four results per lane enter the fp32 sums
+// through one fma with the product of the two scales.  The rows of the
+// instruction are n and its columns are tokens: the activation scale is then
+// one value per lane and token tile, the weight scale is uniform, and a lane
+// holds four consecutive n of one token.  The order of the 128 columns inside
+// an instruction does not matter as long as both operands share it.
+#include "moe_block.h"
+#include "moe_block_device.h"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
+    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+__device__ __forceinline__ f32x4 mfma_fp8(i32x8 w, i32x8 a) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+
+// --------------------------------------------------------------- short rows
+// The 8-bit matrix instructions align the products of a sum to the largest
+// and drop what lies some 13 bits below it: measured, at most 2.5e-5 of the
+// sum of magnitudes over 128 terms of one size, but up to 6e-5 over 16.  Rows
+// of up to 64 columns are summed in fp32 instead, one output per lane; they
+// are latency bound either way.
+constexpr int kShort = 64;
+__global__ void __launch_bounds__(256) fp8_short_kernel(Fp8Args a) {
+    const int n = blockIdx.x * 64 + (threadIdx.x & 63);
+    const long t = (long)blockIdx.y * 4 + (threadIdx.x >> 6);
+    if (n >= a.N || t >= a.M) return;
+    float v = 0.0f;
+    for (int k = 0; k < a.K; k += 4) {
+        const int x = *as_global<int>(a.a + t * a.lda + k), w = *as_global<int>(a.w + (long)n * a.ldw + k);
+        v = fmaf(__builtin_amdgcn_cvt_f32_fp8(x, 0), __builtin_amdgcn_cvt_f32_fp8(w, 0), v);
+        v = fmaf(__builtin_amdgcn_cvt_f32_fp8(x, 1), __builtin_amdgcn_cvt_f32_fp8(w, 1), v);
+        v = fmaf(__builtin_amdgcn_cvt_f32_fp8(x, 2), __builtin_amdgcn_cvt_f32_fp8(w, 2), v);
+        v = fmaf(__builtin_amdgcn_cvt_f32_fp8(x, 3), __builtin_amdgcn_cvt_f32_fp8(w, 3), v);
+    }
+    v *= a.a_scale[t * a.as_t] * a.w_scale[(long)(n >> 7) * a.ws_n];
+    if (a.out_f32)
+        static_cast<float*>(a.out)[t * a.ldo + n] = v;
+    else
+        static_cast<uint16_t*>(a.out)[t * a.ldo + n] = round_bf16(v);
+}
+
+// ---------------------------------------------------------------- few tokens
+// Bound by reading the weights once.  A workgroup owns NT x 16 rows of W and
+// TT x 16 tokens; its eight waves take the blocks of the inner dimension in
+// turn, straight from global memory in operand order, and their sums are
+// joined through LDS in wave order.
+template <int NT, int TT>
+__global__ void __launch_bounds__(512) fp8_rows_kernel(Fp8Args a) {
+    constexpr int kWaves = 8, U = NT * TT >= 4 ? 2 : 4;
+    __shared__ float part[kWaves][NT * TT * 256];
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = wave_in_block();
+    const int n0 = blockIdx.x * NT * 16, t0 = blockIdx.y * TT * 16;
+    const uint8_t* w[NT];
+    const uint8_t* x[TT];
+    const float* sx[TT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int n = n0 + i * 16 + col;
+        w[i] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        const int t = t0 + i * 16 + col;
+        const long tc = t < a.M ? t : a.M - 1;
+        x[i] = a.a + tc * a.lda;
+        sx[i] = a.a_scale + tc * a.as_t;
+    }
+    const float* sw = a.w_scale + (long)(n0 >> 7) * a.ws_n;  // 16 NT divides 128
+    const int blocks = (a.K + 127) >> 7;
+    f32x4 acc[NT][TT] = {};
+    for (int b0 = wave; b0 < blocks; b0 += kWaves * U) {
+        u32x4 wf[U][NT][2], xf[U][TT][2];
+        float s[U][TT], sb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u * kWaves;
+            if (b >= blocks) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int k = b * 128 + (quad * 2 + c) * 16;
+                const int kc = k < a.K ? k : 0;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) wf[u][i][c] = load_stream16(w[i] + kc);
+#pragma unroll
+                for (int i = 0; i < TT; ++i) xf[u][i][c] = *as_global<u32x4>(x[i] + kc);
+            }
+            sb[u] = as_global<float>(sw)[b];
+#pragma unroll
+            for (int i = 0; i < TT; ++i) s[u][i] = as_global<float>(sx[i])[(long)b * a.as_k];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u * kWaves;
+            if (b >= blocks) break;
+            if (b * 128 + 128 > a.K) {  // the last block ends early: no weight past the end
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const bool in = b * 128 + (quad * 2 + c) * 16 < a.K;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) wf[u][i][c] = in ? wf[u][i][c] : u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) xf[u][i][c] = in ? xf[u][i][c] : u32x4{0, 0, 0, 0};
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                const float sc = s[u][j] * sb[u];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const f32x4 p = mfma_fp8(join(wf[u][i][0], wf[u][i][1]), join(xf[u][j][0], xf[u][j][1]));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sc, p[e], acc[i][j][e]);
+                }
+            }
+        }
+    }
+    // part[wave][token][n] of the workgroup's tile
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            *reinterpret_cast<f32x4*>(&part[wave][(j * 16 + col) * (NT * 16) + i * 16 + quad * 4]) = acc[i][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < NT * TT * 256; e += 512) {
+        const int t = t0 + e / (NT * 16), n = n0 + e % (NT * 16);
+        if (t >= a.M || n >= a.N) continue;
+        float v = part[0][e];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) v += part[i][e];
+        if (a.out_f32)
+            static_cast<float*>(a.out)[(long)t * a.ldo + n] = v;
+        else
+            static_cast<uint16_t*>(a.out)[(long)t * a.ldo + n] = round_bf16(v);
+    }
+}
+
+// --------------------------------------------------------------- many tokens
+// Bound by the matrix cores.  WN x WT waves, each NT x TT instruction tiles;
+// both operands of one block of 128 columns go through LDS, loaded
+// asynchronously one block ahead into the other of two buffers.  A row of a
+// buffer is 128 bytes; its 16-byte chunk c sits at place c ^ ((row / 2) & 7),
+// so that the 16 rows of an operand read cover all banks.
+template <int WN, int WT, int NT, int TT>
+__global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
+    constexpr int kWaves = WN * WT, BN = WN * NT * 16, BT = WT * TT * 16, kRows = BN + BT;
+    constexpr int kLoads = kRows / 8 / kWaves;  // asynchronous loads per wave and block
+    static_assert(kRows % (8 * kWaves) == 0 && 128 % (NT * 16) == 0 && BN % 8 == 0, "tile shape");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kRows * 128];
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = wave_in_block();
+    const int wn = wave % WN, wt = wave / WN;
+    // Workgroups are dealt to the eight dies in turn: each die gets a
+    // contiguous run of the tile order, in which bands of eight weight tiles
+    // pass over the tokens, so that its L2 serves both operands again.
+    const int tiles_n = (a.N + BN - 1) / BN, tiles_t = (a.M + BT - 1) / BT, total = tiles_n * tiles_t;
+    const int die = blockIdx.x & 7, idx = blockIdx.x >> 3, each = total >> 3, more = total & 7;
+    const int pid = die * each + (die < more ? die : more) + idx;
+    const int band = 8, band_size = band * tiles_t, g = pid / band_size;
+    const int in_band = tiles_n - g * band < band ? tiles_n - g * band : band;
+    const int n0 = (g * band + (pid % band_size) % in_band) * BN, t0 = ((pid % band_size) / in_band) * BT;
+
+    // per-lane source of each load: rows past the end repeat the last one
+    const uint8_t* base[kLoads];
+    int chunk[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int r0 = (i * kWaves + wave) * 8, r = r0 + (lane >> 3);
+        chunk[i] = ((lane & 7) ^ (r >> 1)) & 7;
+        if (r0 < BN) {
+            const int n = n0 + r;
+            base[i] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
+        } else {
+            const int t = t0 + r - BN;
+            base[i] = a.a + (long)(t < a.M ? t : a.M - 1) * a.lda;
+        }
+        base[i] += chunk[i] * 16;
+    }
+    const int blocks = (a.K + 127) >> 7;
+    const unsigned lds0 = lds_address(&lds[0][0]);
+    auto issue = [&](int b) {
+        const unsigned dst = lds0 + (b & 1) * kRows * 128 + wave * 1024;
+        const bool whole = b * 128 + 128 <= a.K;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint8_t* p = base[i] + (long)b * 128;
+            if (!whole) p = b * 128 + chunk[i] * 16 < a.K ? p : kZeros;
+            load_to_lds16(p, dst + i * kWaves * 1024);
+        }
+    };
+    const float* sx[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int t = t0 + (wt * TT + j) * 16 + col;
+        sx[j] = a.a_scale + (long)(t < a.M ? t : a.M - 1) * a.as_t;
+    }
+    int nb = (n0 + wn * NT * 16) >> 7;  // a tile past the last row has no scale of its own
+    const int last_nb = (a.N - 1) >> 7;
+    const float* sw = a.w_scale + (long)(nb < last_nb ? nb : last_nb) * a.ws_n;
+
+    float sc[TT], sb = as_global<float>(sw)[0];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) sc[j] = as_global<float>(sx[j])[0];
+    issue(0);
+    f32x4 acc[NT][TT] = {};
+    for (int b = 0; b < blocks; ++b) {
+        wait_vmem<0>();
+        float s[TT];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            s[j] = sc[j] * sb;
+            asm volatile("" : "+v"(s[j]));  // the scales have landed: no later wait covers the loads below
+        }
+        lds_barrier();  // block b is in LDS, and every wave is done with the other buffer
+        if (b + 1 < blocks) {
+            sb = as_global<float>(sw)[b + 1];
+#pragma unroll
+            for (int j = 0; j < TT; ++j) sc[j] = as_global<float>(sx[j])[(long)(b + 1) * a.as_k];
+            issue(b + 1);
+        }
+        const uint8_t* buf = lds[b & 1];
+        auto operand = [&](int row0) {
+            const int r = row0 + col, sw0 = (r >> 1) & 7;
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(buf + r * 128 + ((quad ^ sw0) * 16));
+            const u32x4 hi = *reinterpret_cast<const u32x4*>(buf + r * 128 + (((quad + 4) ^ sw0) * 16));
+            return join(lo, hi);
+        };
+        i32x8 xf[TT];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) xf[j] = operand(BN + (wt * TT + j) * 16);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const i32x8 wf = operand((wn * NT + i) * 16);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                const f32x4 p = mfma_fp8(wf, xf[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(s[j], p[e], acc[i][j][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int t = t0 + (wt * TT + j) * 16 + col;
+        if (t >= a.M) continue;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int n = n0 + (wn * NT + i) * 16 + quad * 4;
+            const f32x4 v = acc[i][j];
+            if (a.out_f32) {
+                float* o = static_cast<float*>(a.out) + (long)t * a.ldo + n;
+                if (n + 3 < a.N && a.out_vec)
+                    *reinterpret_cast<f32x4*>(o) = v;
+                else
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < a.N) o[e] = v[e];
+            } else {
+                uint16_t* o = static_cast<uint16_t*>(a.out) + (long)t * a.ldo + n;
+                if (n + 3 < a.N && a.out_vec)
+                    *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                else
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < a.N) o[e] = round_bf16(v[e]);
+            }
+        }
+    }
+}
+
+template <int NT, int TT>
+void launch_rows(const Fp8Args& a, hipStream_t s) {
+    const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.M + 16 * TT - 1) / (16 * TT));
+    hipLaunchKernelGGL((fp8_rows_kernel<NT, TT>), grid, dim3(512), 0, s, a);
+}
+
+template <int WN, int WT, int NT, int TT>
+void launch_tiles(const Fp8Args& a, hipStream_t s) {
+    constexpr int BN = WN * NT * 16, BT = WT * TT * 16;
+    const int total = ((a.N + BN - 1) / BN) * ((a.M + BT - 1) / BT);
+    hipLaunchKernelGGL((fp8_tiles_kernel<WN, WT, NT, TT>), dim3(total), dim3(WN * WT * 64), 0, s, a);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t s) {
+    if (a.K <= kShort)
+        hipLaunchKernelGGL(fp8_short_kernel, dim3((a.N + 63) / 64, (a.M + 3) / 4), dim3(256), 0, s, a);
+    else if (a.M <= 16)
+        launch_rows<1, 1>(a, s);
+    else if (a.M <= 64)
+        launch_rows<1, 4>(a, s);
+    else
+        launch_tiles<2, 2, 4, 4>(a, s);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,201 @@
+// Causal attention over keys and values expanded per head (the expanded form
+// of latent attention): ragged sequences packed one after another, the
+// position part of the keys shared by all heads.
+//
+// One pass over the keys with the running maximum and sum of the softmax.  A
+// workgroup owns 128 queries of one head, 32 per wave; tiles of KT keys go
+// through LDS, loaded asynchronously one tile ahead into the other of two
+// buffers.  Bound by the matrix cores: per 64 keys a wave issues 40 matrix
+// instructions of 32 x 32 x 16 (widths 192 and 128) and some 900 cycles of
+// exponentials and statistics, which the second workgroup on the same CU
+// fills in (half of LDS each).
+#include "moe_block.h"
+#include "moe_block_device.h"
+
+namespace moe {
+namespace {
+
+// Key rows are cut into parts of 64 columns, each part of a tile an array of
+// 128-byte rows in LDS.  The chunk c (16 bytes) of row r sits at place
+// c ^ ((r / 2) & 7), so that the 16 rows of an operand read (same chunk)
+// cover all banks; value rows are mixed so that the four rows by 64 bytes of
+// a transposed read do.
+__device__ __forceinline__ int key_place(int c, int r) { return c ^ ((r >> 1) & 7); }
+template <int ROW_BYTES>
+__device__ __forceinline__ int value_place(int c, int r) {
+    return ROW_BYTES % 256 ? c ^ (((r >> 1) & 1) << 2) : c ^ ((r & 3) << 2);
+}
+
+template <int NOPE, int ROPE, int VD, int KT, int PER_CU>
+__global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArgs a) {
+    static_assert(ROPE == 64 && NOPE % 64 == 0, "the position part is one part of 64 columns");
+    constexpr int kSub = KT / 32, kParts = NOPE / 64 + 1, kPartBytes = KT * 128, kOut = VD / 32;
+    constexpr int kTileBytes = kParts * kPartBytes + KT * VD * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kTileBytes];
+    const int lane = threadIdx.x & 63, wave = wave_in_block(), half = lane >> 5, col = lane & 31;
+    const int h = blockIdx.x, b = blockIdx.z;
+    // bounds come from device memory: kept inside the tensors whatever they say
+    auto inside = [](int v, int n) { return v < 0 ? 0 : (v > n ? n : v); };
+    const int q_first = inside(a.cu_q[b], a.Tq), q_count = inside(a.cu_q[b + 1], a.Tq) - q_first;
+    const int k_first = inside(a.cu_k[b], a.Tk), k_count_all = inside(a.cu_k[b + 1], a.Tk) - k_first;
+    const int k_count = k_count_all > 0 ? k_count_all : 0;
+    // the last tiles see the most keys: they go first
+    const int tile = gridDim.y - 1 - blockIdx.y, q0 = tile * 128;
+    if (q0 >= q_count) return;
+    const int past = k_count - q_count;  // keys before the first query's own
+    const int my_q = q0 + wave * 32 + col;
+    const bool row_ok = my_q < q_count;
+    const long q_row = q_first + (row_ok ? my_q : q_count - 1);
+
+    bf16x8 qf[kParts * 4];
+    {
+        const uint16_t* p = a.q + q_row * a.q_stride_t + h * a.q_stride_h + half * 8;
+#pragma unroll
+        for (int k = 0; k < kParts * 4; ++k) qf[k] = __builtin_bit_cast(bf16x8, *as_global<u32x4>(p + k * 16));
+    }
+    // visible keys of this lane's query, and of the workgroup's and wave's last one
+    auto visible = [&](int q) {
+        const int n = a.causal ? past + q + 1 : k_count;
+        return n < 0 ? 0 : (n > k_count ? k_count : n);
+    };
+    const int last_q = q0 + 127 < q_count ? q0 + 127 : q_count - 1;
+    const int wave_last = q0 + wave * 32 + 31 < q_count ? q0 + wave * 32 + 31 : q_count - 1;
+    const int limit = row_ok ? visible(my_q) : 0;
+    const int wave_limit = q0 + wave * 32 < q_count ? visible(wave_last) : 0;
+    const int wave_full = a.causal ? visible(q0 + wave * 32) : k_count;  // keys that all of the wave's rows see
+    const int tiles = (visible(last_q) + KT - 1) / KT;
+
+    // Loads of one tile: an instruction covers whole rows, and the place of a
+    // lane's chunk is the same in all of a kind.
+    constexpr int kValueRows = 1024 / (VD * 2);
+    const int kr = wave * 8 + lane / 8, vr = wave * kValueRows + lane / (VD / 8);
+    const int k_chunk = key_place(lane % 8, kr), v_chunk = value_place<VD * 2>(lane % (VD / 8), vr);
+    const uint16_t* k_base = a.k + (long)k_first * a.k_stride_t + h * a.k_stride_h;
+    const uint16_t* r_base = a.k_rope + (long)k_first * a.kr_stride_t;
+    const uint16_t* v_base = a.v + (long)k_first * a.v_stride_t + h * a.v_stride_h;
+    const unsigned lds0 = lds_address(&lds[0][0]);
+    auto issue_part = [&](const uint16_t* base, long stride, int key0, int row, int chunk, unsigned dst) {
+        // row: this lane's row in the tile
+        if (key0 + KT <= k_count) {
+            load_to_lds16(base + (long)key0 * stride + 0, (unsigned)(row * stride * 2 + chunk * 16), dst);
+        } else {
+            const int key = key0 + row;
+            const uint16_t* p = base + (long)key * stride + chunk * 8;
+            load_to_lds16(key < k_count ? static_cast<const void*>(p) : kZeros, dst);
+        }
+    };
+    auto issue = [&](int t) {
+        const int key0 = t * KT;
+        const unsigned dst = lds0 + (t & 1) * kTileBytes + wave * 1024;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i)
+                issue_part(p < kParts - 1 ? k_base + p * 64 : r_base, p < kParts - 1 ? a.k_stride_t : a.kr_stride_t, key0,
+                           kr + i * 32, k_chunk, dst + p * kPartBytes + i * 4096);
+#pragma unroll
+        for (int i = 0; i < KT / (4 * kValueRows); ++i)
+            issue_part(v_base, a.v_stride_t, key0, vr + i * 4 * kValueRows, v_chunk, dst + kParts * kPartBytes + i * 4096);
+    };
+
+    const float c = a.scale * 1.44269504088896340736f;
+    float m = kNoMax, l = 0.0f;
+    f32x16 o[kOut] = {};
+    if (tiles > 0) issue(0);
+    for (int t = 0; t < tiles; ++t) {
+        wait_vmem<0>();
+        lds_barrier();  // tile t is in LDS, and every wave is done with the other buffer
+        if (t + 1 < tiles) issue(t + 1);
+        const int key0 = t * KT;
+        if (key0 >= wave_limit) continue;
+        const unsigned buf = lds0 + (t & 1) * kTileBytes;
+        f32x16 s[kSub] = {};
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            const int r = u * 32 + col;
+#pragma unroll
+            for (int k = 0; k < kParts * 4; ++k)
+                s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    lds_chunk(buf + (k / 4) * kPartBytes + r * 128 + key_place((k % 4) * 2 + half, r) * 16), qf[k], s[u],
+                    0, 0, 0);
+        }
+        if (key0 + KT > wave_full) {
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (key0 + u * 32 + 8 * (i / 4) + 4 * half + i % 4 >= limit) s[u][i] = -__builtin_inff();
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+        top = half_max(top);
+        if (__any((top - m) * c > kMaxSlack)) {
+            const float nm = fmaxf(m, top), f = __builtin_amdgcn_exp2f((m - nm) * c);
+            m = nm;
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < kOut; ++k)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[k][i] *= f;
+        }
+        const float mc = m * c;
+        bf16x8 p[kSub * 2];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[u][i], c, -mc));
+                l += e;
+                p[u * 2 + i / 8][i % 8] = (__bf16)e;
+            }
+        const unsigned values = buf + kParts * kPartBytes;
+        const int vrow = half * 4 + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+#pragma unroll
+        for (int k = 0; k < kOut; ++k)
+#pragma unroll
+            for (int u = 0; u < kSub * 2; ++u) {
+                const int r = u * 16 + vrow, ch = (k * 32 + vcol) / 8, sub = (vcol & 4) * 2;
+                const unsigned lo = values + r * VD * 2 + value_place<VD * 2>(ch, r) * 16 + sub;
+                const unsigned hi = values + (r + 8) * VD * 2 + value_place<VD * 2>(ch, r + 8) * 16 + sub;
+                o[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_transposed(lo, hi), p[u], o[k], 0, 0, 0);
+            }
+    }
+    if (!row_ok) return;
+    l = half_sum(l);
+    // a row that sees no key gives zero
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    uint16_t* out = a.out + q_row * a.o_stride_t + h * a.o_stride_h + half * 4;
+#pragma unroll
+    for (int k = 0; k < kOut; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x2*>(out + k * 32 + i * 8) =
+                u32x2{pack_bf16(o[k][i * 4] * inv, o[k][i * 4 + 1] * inv), pack_bf16(o[k][i * 4 + 2] * inv, o[k][i * 4 + 3] * inv)};
+}
+
+template <int NOPE, int ROPE, int VD, int KT, int PER_CU>
+void launch_shape(const PromptArgs& a, hipStream_t s) {
+    const dim3 grid(a.heads, (a.max_q + 127) / 128, a.B);
+    hipLaunchKernelGGL((prompt_attention_kernel<NOPE, ROPE, VD, KT, PER_CU>), grid, dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+bool prompt_shape_supported(int nope, int rope, int vdim) {
+    return rope == 64 && ((nope == 64 && vdim == 64) || (nope == 128 && vdim == 128) || (nope == 192 && vdim == 256));
+}
+
+hipError_t launch_prompt_attention(const PromptArgs& a, hipStream_t s) {
+    if (a.nope == 64)
+        launch_shape<64, 64, 64, 64, 2>(a, s);
+    else if (a.nope == 128)
+        launch_shape<128, 64, 128, 64, 2>(a, s);
+    else  // 230 registers of queries and sums: one wave per SIMD
+        launch_shape<192, 64, 256, 64, 1>(a, s);
+    return hipGetLastError();
+}
+
+}  // namespace moe
