@@ -79,6 +79,7 @@ struct LatentArgs {
     uint8_t* ws;            // latent_workspace() bytes
     long q_stride_t, q_stride_h, o_stride_t, o_stride_h, pages_stride, cache_page_stride;
     int T, B, heads, rank, rope, n_pages, page_size, pages_per_seq, max_q, max_len;
+    int group, runs, per_seq;  // how the call is cut, filled in by the launcher
     float scale;
 };
 // Device workspace of a call (partial sums of the split sequences).

@@ -21,11 +21,14 @@
 // two layouts agree lane by lane, 32 bytes each.  A workgroup is one or two
 // such pairs.
 //
-// The tiles of all sequences and row blocks form one list that is cut into
-// equal runs, one per workgroup (lengths are only known on the device, and
-// ragged batches would leave compute units idle).  A run that does not hold
-// the whole of a (sequence, row block) leaves fp32 sums, maximum and total in
-// the workspace, and a second launch joins them in run order.
+// Row blocks of one sequence read the same cache rows, so GS workgroups work
+// as a group: on the same die (one L2), over the same tiles, each on its own
+// row block; a sequence of more blocks takes several passes.  The tiles of all
+// (sequence, pass) units form one list that is cut into equal runs, one per
+// group (lengths are only known on the device, and ragged batches would leave
+// compute units idle).  A run that does not hold the whole of a unit leaves
+// fp32 sums, maximum and total in the workspace, and a second launch joins
+// them in run order.
 #include "moe_block.h"
 #include "moe_block_device.h"
 
@@ -33,11 +36,10 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 64;          // cache rows per tile
-constexpr int kMaxRuns = 256;      // one workgroup per CU
-constexpr int kMinRun = 2;         // tiles a run is worth starting for
+constexpr int kMaxGroup = 8;       // workgroups of a group
+constexpr int kMaxWorkgroups = 256;  // one per CU
 constexpr int kRopeWidth = 64;
 
-// How one call is cut up (the same arithmetic in both launches).
 __device__ __forceinline__ int seq_len(const LatentArgs& a, int b) {
     const int n = a.lens[b];
     const long most = (long)a.pages_per_seq * a.page_size;
@@ -50,53 +52,71 @@ __device__ __forceinline__ void seq_tokens(const LatentArgs& a, int b, int& firs
         count = (v > a.T ? a.T : v) - first;
         if (count < 0) count = 0;
     } else {
-        count = a.T / a.B;
+        count = a.per_seq;
         first = b * count;
     }
 }
-__device__ __forceinline__ int seq_tiles(const LatentArgs& a, int b) {
-    const int n = (seq_len(a, b) + kTile - 1) / kTile;
-    return n > 1 ? n : 1;  // an empty sequence still writes its zeros
-}
+// One sequence's part of the list: tiles of the cache, row blocks, passes.
+struct SeqShape {
+    int len, first, count, tiles, blocks, passes;
+};
 template <int ROWS>
-__device__ __forceinline__ int seq_blocks(const LatentArgs& a, int b) {
-    int first, count;
-    seq_tokens(a, b, first, count);
-    return (count * a.heads + ROWS - 1) / ROWS;
+__device__ __forceinline__ SeqShape seq_shape(const LatentArgs& a, int b) {
+    SeqShape s;
+    s.len = seq_len(a, b);
+    seq_tokens(a, b, s.first, s.count);
+    s.tiles = s.len > kTile ? (s.len + kTile - 1) / kTile : 1;  // an empty sequence still writes its zeros
+    s.blocks = (s.count * a.heads + ROWS - 1) / ROWS;
+    s.passes = (s.blocks + a.group - 1) / a.group;
+    return s;
 }
 
-__device__ __forceinline__ int wave_sum_int(int v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
-}
 // Inclusive sum over the lanes up to this one.
-__device__ __forceinline__ int wave_scan_int(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        if (lane >= d) v += u;
-    }
-    return v;
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int scan_step(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan_int(int v) {
+    v = scan_step<0x111, 0xF>(v);  // within rows of 16: shifts by 1, 2, 4, 8
+    v = scan_step<0x112, 0xF>(v);
+    v = scan_step<0x114, 0xF>(v);
+    v = scan_step<0x118, 0xF>(v);
+    v = scan_step<0x142, 0xA>(v);  // last lane of rows 0 and 2 into rows 1 and 3
+    return scan_step<0x143, 0xC>(v);  // lane 31 into the upper half
 }
 
-// Tiles of the whole call (each wave by itself).
+// The whole list: its length, and the tiles before sequence `upto`.
 template <int ROWS>
-__device__ __forceinline__ int total_tiles(const LatentArgs& a, int lane) {
-    int n = 0;
-    for (int b = lane; b < a.B; b += 64) n += seq_tiles(a, b) * seq_blocks<ROWS>(a, b);
-    return __builtin_amdgcn_readfirstlane(wave_sum_int(n));
+__device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int lane, int& before) {
+    int total = 0;
+    before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        const int b = b0 + lane;
+        int mine = 0;
+        if (b < a.B) {
+            const SeqShape s = seq_shape<ROWS>(a, b);
+            mine = s.tiles * s.passes;
+        }
+        const int scan = wave_scan_int(mine);
+        if (upto > b0) before = total + __builtin_amdgcn_readlane(scan, (upto - b0 < 64 ? upto - b0 : 64) - 1);
+        total += __builtin_amdgcn_readlane(scan, 63);
+    }
+    return total;
 }
 
-// The sequence that holds tile `at` of the list (tiles of a sequence: its row
-// blocks one after another), and the tile its part starts with.
+// The sequence that holds tile `at` of the list (at < its length), and the
+// tile its part starts with.
 template <int ROWS>
 __device__ __forceinline__ void find_tile(const LatentArgs& a, int at, int lane, int& seq, int& start) {
     int before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
         const int b = b0 + lane;
-        const int mine = b < a.B ? seq_tiles(a, b) * seq_blocks<ROWS>(a, b) : 0;
-        const int upto = wave_scan_int(mine, lane) + before;
+        int mine = 0;
+        if (b < a.B) {
+            const SeqShape s = seq_shape<ROWS>(a, b);
+            mine = s.tiles * s.passes;
+        }
+        const int upto = wave_scan_int(mine) + before;
         const unsigned long long hit = __ballot(b < a.B && upto > at);
         if (hit) {
             const int w = __builtin_ctzll(hit);
@@ -106,17 +126,17 @@ __device__ __forceinline__ void find_tile(const LatentArgs& a, int at, int lane,
         }
         before = __builtin_amdgcn_readlane(upto, 63);
     }
-    seq = a.B;
-    start = before;
+    seq = a.B - 1;
+    start = at;
 }
 
-__device__ __forceinline__ int run_count(int total, int most) {
-    const int n = (total + kMinRun - 1) / kMinRun;
-    return n < most ? n : most;
-}
+// Runs the list is cut into, and where run g starts.
+__device__ __forceinline__ int run_count(int total, int most) { return total < most ? total : most; }
 __device__ __forceinline__ int run_start(int total, int runs, int g) { return (int)((long)total * g / runs); }
 
-// Partial sums of one run: [2 per run][ROWS][RANK] fp32, then (maximum, total) pairs.
+// Partial sums of one workgroup: [2][ROWS][RANK] fp32, then (maximum, total)
+// pairs; the second half is for the unit it starts, the first for the one it
+// finds begun.
 template <int ROWS, int RANK>
 __device__ __forceinline__ float* part_sums(const LatentArgs& a, int slot) {
     return reinterpret_cast<float*>(a.ws) + (size_t)slot * ROWS * (RANK + 2);
@@ -127,6 +147,21 @@ __device__ __forceinline__ float* part_sums(const LatentArgs& a, int slot) {
 // an operand read of 16 rows (same chunk) and a transposed read of four rows
 // by four chunks cover all banks.
 __device__ __forceinline__ int place_mix(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+
+// Matrix instructions with the register file of each operand fixed: 144
+// registers of queries lie in the accumulation file, 128 of sums, the scores
+// and the LDS operands in the other (left to itself the compiler moves 240
+// registers between the two per tile).  It does not see hazards of assembly:
+// the leading s_nop covers operands written just before, settle() the states
+// from a matrix instruction to the first other reader of its result (19 at
+// most; instructions that accumulate into the same registers need none).
+__device__ __forceinline__ void mfma_scores(f32x16& s, bf16x8 keys, bf16x8 queries) {
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(keys), "a"(queries));
+}
+__device__ __forceinline__ void mfma_sums(f32x16& o, bf16x8 values, bf16x8 p) {
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(o) : "v"(values), "v"(p));
+}
+__device__ __forceinline__ void settle(f32x16& v) { asm("s_nop 15\n\ts_nop 3" : "+v"(v)); }
 
 // The n lowest bits (none below 0, all from 64 up).
 __device__ __forceinline__ unsigned long long low_bits(int n) {
@@ -145,12 +180,13 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
     __shared__ int shared_raise[2][kWaves];     // a row's maximum has to move (by tile parity)
     const int lane = threadIdx.x & 63, wave = wave_in_block(), half = lane >> 5, col = lane & 31;
     const int rg = wave >> 1, side = wave & 1, other = wave ^ 1;
-    const int total = total_tiles<ROWS>(a, lane), runs = run_count(total, gridDim.x);
-    const int run = blockIdx.x;
+    // workgroups are dealt to the eight dies in turn: group g lies on die g % 8
+    const int turn = blockIdx.x >> 3, run = (blockIdx.x & 7) + 8 * (turn / a.group), member = turn % a.group;
+    int before;
+    const int total = count_tiles<ROWS>(a, 0, lane, before), runs = run_count(total, a.runs);
     if (run >= runs) return;
     const int run_end = run_start(total, runs, run + 1);
     int at = run_start(total, runs, run);
-    if (at >= run_end) return;
     int seq, seq_at;
     find_tile<ROWS>(a, at, lane, seq, seq_at);
 
@@ -179,16 +215,20 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
     }
 
     while (at < run_end) {
-        int first, count;
-        seq_tokens(a, seq, first, count);
-        const int len = seq_len(a, seq), tiles = seq_tiles(a, seq), blocks = seq_blocks<ROWS>(a, seq);
-        if (at >= seq_at + tiles * blocks) {
-            seq_at += tiles * blocks;
+        const SeqShape shape = seq_shape<ROWS>(a, seq);
+        const int len = shape.len, first = shape.first, count = shape.count, tiles = shape.tiles;
+        if (at >= seq_at + tiles * shape.passes) {
+            seq_at += tiles * shape.passes;
             ++seq;
             continue;
         }
-        const int block = (at - seq_at) / tiles, t_first = (at - seq_at) % tiles;
+        const int pass = (at - seq_at) / tiles, t_first = (at - seq_at) % tiles;
         const int t_last = tiles - t_first < run_end - at ? tiles : t_first + run_end - at;
+        const int block = pass * a.group + member;
+        if (block >= shape.blocks) {  // the last pass of this sequence has no block for this member
+            at += t_last - t_first;
+            continue;
+        }
         const int context = len - count;  // keys before the first new token
         const int row = block * ROWS + rg * 32 + col;
         const bool row_ok = row < count * a.heads;
@@ -219,12 +259,11 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             const uint16_t* p = a.cache + (long)page * a.cache_page_stride + (long)off * WIDTH;
             return (unsigned long long)((unsigned)page < (unsigned)a.n_pages ? static_cast<const void*>(p) : kZeros);
         };
-        auto issue = [&](int buf, unsigned long long addr) {
+        constexpr int kLatLoads = kTile / kRowsPerLoad / kWaves, kLoads = kLatLoads + kTile / 8 / kWaves;
+        // Asynchronous load i of this wave's kLoads of a tile.
+        auto issue = [&](int i, int buf, unsigned long long addr, int chunk) {
             const unsigned dst = lds0 + buf * kTileBytes;
-            int chunk = lane;
-            asm volatile("" : "+v"(chunk));  // the mixed places are not worth a register each across the loop
-#pragma unroll
-            for (int i = 0; i < kTile / kRowsPerLoad / kWaves; ++i) {
+            if (i < kLatLoads) {
                 const int r0 = (i * kWaves + wave) * kRowsPerLoad;
                 if constexpr (kRowsPerLoad == 1) {
                     const unsigned lo = __builtin_amdgcn_readlane((unsigned)addr, r0),
@@ -236,10 +275,8 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                     const unsigned long long p = __shfl(addr, r);
                     load_to_lds16((const uint8_t*)p + ((chunk % (RANK / 8)) ^ place_mix(r)) * 16, dst + r0 * RANK * 2);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < kTile / 8 / kWaves; ++i) {
-                const int r0 = (i * kWaves + wave) * 8, r = r0 + (chunk >> 3);
+            } else {
+                const int r0 = ((i - kLatLoads) * kWaves + wave) * 8, r = r0 + (chunk >> 3);
                 const unsigned long long p = __shfl(addr, r);
                 load_to_lds16((const uint8_t*)p + RANK * 2 + (((chunk & 7) ^ (r >> 1)) & 7) * 16,
                               dst + kLatBytes + r0 * kRopeWidth * 2);
@@ -250,7 +287,11 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
         f32x16 o[kOut] = {};
         int off, page = page_of(t_first, off);
         unsigned long long valid = __ballot((unsigned)page < (unsigned)a.n_pages);
-        issue(0, address(page, off));
+        {
+            const unsigned long long addr = address(page, off);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) issue(i, 0, addr, lane);
+        }
         page = page_of(t_first + 1, off);
         for (int t = t_first; t < t_last; ++t) {
             const int buf = (t - t_first) & 1;
@@ -258,12 +299,12 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             asm volatile("" : "+v"(page));  // the next tile's pages have landed: no later wait covers its loads
             lds_barrier();                  // tile t is in LDS, and every wave is done with the other buffer
             const unsigned long long now = valid;
-            if (t + 1 < t_last) {
-                valid = __ballot((unsigned)page < (unsigned)a.n_pages);
-                const unsigned long long next = address(page, off);
-                page = page_of(t + 2, off);
-                issue(buf ^ 1, next);
-            }
+            valid = __ballot((unsigned)page < (unsigned)a.n_pages);
+            const unsigned long long next = address(page, off);
+            const bool more = t + 1 < t_last;
+            page = page_of(t + 2, off);
+            int chunk = lane;
+            asm volatile("" : "+v"(chunk));  // the mixed places are not worth a register each across the loop
             const unsigned tile = lds0 + buf * kTileBytes;
             f32x16 s = {};
             {
@@ -272,17 +313,29 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 // at once
                 constexpr int kAhead = 6;
                 bf16x8 x[kAhead];
+                unsigned key_base[8], rope_base[kRope];  // plus immediate offsets
+#pragma unroll
+                for (int k = 0; k < 8; ++k) key_base[k] = key_at[k] + tile;
+#pragma unroll
+                for (int k = 0; k < kRope; ++k) rope_base[k] = rope_at[k] + tile;
                 auto key_chunk = [&](int k) {
-                    return lds_chunk(k < kLat ? key_at[k & 7] + tile + (k >> 3) * 256 : rope_at[k - kLat] + tile);
+                    return lds_chunk(k < kLat ? key_base[k & 7] + (k >> 3) * 256 : rope_base[k - kLat]);
                 };
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) x[k] = key_chunk(k);
 #pragma unroll
                 for (int k = 0; k < kLat + kRope; ++k) {
-                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[k % kAhead], qf[k], s, 0, 0, 0);
+                    mfma_scores(s, x[k % kAhead], qf[k]);
                     if (k + kAhead < kLat + kRope) x[k % kAhead] = key_chunk(k + kAhead);
+                    // the next tile's loads, spread over the instructions (a
+                    // wave that issues them in one go stalls in the queue)
+                    constexpr int kSteps = kLat + kRope;
+#pragma unroll
+                    for (int i = k * kLoads / kSteps; i < (k + 1) * kLoads / kSteps; ++i)
+                        if (more) issue(i, buf ^ 1, next, chunk);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                settle(s);
             }
             if (now != ~0ull || (t + 1) * kTile > context + (a.tree ? 0 : 1)) {
                 // visible keys of this tile, a bit each; this lane's registers
@@ -304,6 +357,21 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 for (int i = 0; i < 16; ++i)
                     s[i] = word >> (8 * (i / 4) + i % 4) & 1 ? s[i] : -__builtin_inff();
             }
+            // the first values are read before the exchange
+            constexpr int kAhead = 6;
+            bf16x8 x[kAhead];
+            unsigned lo[4], hi[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                lo[k] = value_lo[k] + tile;
+                hi[k] = value_hi[k] + tile;
+            }
+            auto value_chunk = [&](int j) {
+                const int k = j >> 2, at_key = (j & 3) * 16 * RANK * 2 + (k >> 2) * 256;
+                return values_transposed(lo[k & 3] + at_key, hi[k & 3] + at_key);
+            };
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) x[j] = value_chunk(j);
             float top = s[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
@@ -330,6 +398,7 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             int any = 0;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) any |= shared_raise[t & 1][w];
+            u32x4 q0 = shared_p[other][0][lane], q1 = shared_p[other][1][lane];
             if (__builtin_amdgcn_readfirstlane(any)) {
                 // some row's maximum moves: both waves of each pair take the
                 // new one and compute their exponentials again
@@ -338,41 +407,38 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 m = nm;
                 l *= f;
 #pragma unroll
-                for (int k = 0; k < kOut; ++k)
+                for (int k = 0; k < kOut; ++k) {
+                    settle(o[k]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[k][i] *= f;
+                }
+                lds_barrier();  // the first ones are read
                 sum = exponentials();
                 lds_barrier();
+                q0 = shared_p[other][0][lane];
+                q1 = shared_p[other][1][lane];
             }
             l += sum;
             {
-                const bf16x8 q0 = __builtin_bit_cast(bf16x8, shared_p[other][0][lane]),
-                             q1 = __builtin_bit_cast(bf16x8, shared_p[other][1][lane]);
-                const bf16x8 p0 = p[0], p1 = p[1];
-                p[0] = side ? q0 : p0;
-                p[1] = side ? q1 : p1;
-                p[2] = side ? p0 : q0;
-                p[3] = side ? p1 : q1;
+                const bf16x8 p0 = p[0], p1 = p[1], r0 = __builtin_bit_cast(bf16x8, q0),
+                             r1 = __builtin_bit_cast(bf16x8, q1);
+                p[0] = side ? r0 : p0;
+                p[1] = side ? r1 : p1;
+                p[2] = side ? p0 : r0;
+                p[3] = side ? p1 : r1;
             }
             {
-                constexpr int kAhead = 6;
-                bf16x8 x[kAhead];
-                auto value_chunk = [&](int j) {
-                    const int k = j >> 2, v = j & 3;
-                    const unsigned at_key = tile + v * 16 * RANK * 2 + (k >> 2) * 256;
-                    return values_transposed(value_lo[k & 3] + at_key, value_hi[k & 3] + at_key);
-                };
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j) x[j] = value_chunk(j);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < 4 * kOut; ++j) {
-                    o[j >> 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j % kAhead], p[j & 3], o[j >> 2], 0, 0, 0);
+                    mfma_sums(o[j >> 2], x[j % kAhead], p[j & 3]);
                     if (j + kAhead < 4 * kOut) x[j % kAhead] = value_chunk(j + kAhead);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
+#pragma unroll
+        for (int k = 0; k < kOut; ++k) settle(o[k]);
         // totals over the tile halves of both waves
         l = half_sum(l);
         __syncthreads();
@@ -393,7 +459,7 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                                   pack_bf16(o[k][i * 4 + 2] * inv, o[k][i * 4 + 3] * inv)};
             }
         } else {
-            float* part = part_sums<ROWS, RANK>(a, run * 2 + (t_first == 0));
+            float* part = part_sums<ROWS, RANK>(a, (run * a.group + member) * 2 + (t_first == 0));
             const int r = rg * 32 + col;
 #pragma unroll
             for (int k = 0; k < kOut; ++k)
@@ -411,23 +477,20 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
     }
 }
 
-// Joins the partial sums of every (sequence, row block) that more than one
-// run worked on: a wave per row, the runs in order.
+// Joins the partial sums of every unit that more than one run worked on: a
+// wave per row, RANK / 64 columns per lane, the runs in order.
 template <int RANK, int ROWS>
-__global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a, int most_runs) {
-    constexpr int V = RANK / 64;  // columns per lane
+__global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
+    constexpr int V = RANK / 64;
     const int lane = threadIdx.x & 63;
     const int seq = blockIdx.y, row = blockIdx.x * 4 + wave_in_block();
-    int first, count;
-    seq_tokens(a, seq, first, count);
-    if (row >= count * a.heads) return;
-    const int total = total_tiles<ROWS>(a, lane), runs = run_count(total, most_runs);
-    int before = 0;
-    for (int b = lane; b < seq; b += 64) before += seq_tiles(a, b) * seq_blocks<ROWS>(a, b);
-    before = __builtin_amdgcn_readfirstlane(wave_sum_int(before));
-    const int tiles = seq_tiles(a, seq), block = row / ROWS, r = row % ROWS;
-    const int u0 = before + block * tiles, u1 = u0 + tiles;
-    // runs that hold the first and the last tile of the block
+    const SeqShape shape = seq_shape<ROWS>(a, seq);
+    if (row >= shape.count * a.heads) return;
+    int before;
+    const int total = count_tiles<ROWS>(a, seq, lane, before), runs = run_count(total, a.runs);
+    const int block = row / ROWS, r = row % ROWS, member = block % a.group;
+    const int u0 = before + block / a.group * shape.tiles, u1 = u0 + shape.tiles;
+    // runs that hold the unit's first and last tile
     auto run_of = [&](int tile) {
         int g = (int)((long)tile * runs / total);
         while (g + 1 < runs && run_start(total, runs, g + 1) <= tile) ++g;
@@ -436,49 +499,90 @@ __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a, int most
     };
     const int g0 = run_of(u0), g1 = run_of(u1 - 1);
     if (g0 == g1) return;  // one run held it all and wrote the result
+    auto part = [&](int g) { return part_sums<ROWS, RANK>(a, (g * a.group + member) * 2 + (g == g0)); };
     const float c = a.scale * 1.44269504088896340736f;
     float m = kNoMax, l = 0.0f, o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.0f;
-    for (int g = g0; g <= g1; ++g) {
-        const float* part = part_sums<ROWS, RANK>(a, g * 2 + (run_start(total, runs, g) <= u0));
-        const float pm = part[ROWS * RANK + r * 2], pl = part[ROWS * RANK + r * 2 + 1];
-        const float nm = fmaxf(m, pm), f = __builtin_amdgcn_exp2f((m - nm) * c), pf = __builtin_amdgcn_exp2f((pm - nm) * c);
-        m = nm;
-        l = l * f + pl * pf;
+    for (int b0 = g0; b0 <= g1; b0 += 64) {
+        // maxima and totals of up to 64 runs, one per lane
+        const int n = g1 + 1 - b0 < 64 ? g1 + 1 - b0 : 64;
+        float pm = kNoMax, pl = 0.0f;
+        if (lane < n) {
+            const float* p = part(b0 + lane) + ROWS * RANK + r * 2;
+            pm = p[0];
+            pl = p[1];
+        }
+        float top = pm;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = o[i] * f + part[(long)r * RANK + lane * V + i] * pf;
+        for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+        const float nm = fmaxf(m, top), f = __builtin_amdgcn_exp2f((m - nm) * c);
+        const float w = __builtin_amdgcn_exp2f((pm - nm) * c);
+        m = nm;
+        l = l * f + wave_sum(w * pl);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= f;
+        for (int k0 = 0; k0 < n; k0 += 4) {  // four runs' loads in flight
+            f32x4 v[4][V / 4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* p = part(b0 + (k0 + k < n ? k0 + k : n - 1)) + (long)r * RANK + lane * V;
+#pragma unroll
+                for (int i = 0; i < V / 4; ++i) v[k][i] = as_global<f32x4>(p)[i];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float wk = k0 + k < n ? readlane_f(w, k0 + k) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = fmaf(v[k][i / 4][i % 4], wk, o[i]);
+            }
+        }
     }
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    uint16_t* out = a.out + (long)(first + row / a.heads) * a.o_stride_t + (row % a.heads) * a.o_stride_h + lane * V;
+    uint16_t* out = a.out + (long)(shape.first + row / a.heads) * a.o_stride_t + (row % a.heads) * a.o_stride_h + lane * V;
 #pragma unroll
-    for (int i = 0; i < V; i += 2) *reinterpret_cast<unsigned*>(out + i) = pack_bf16(o[i] * inv, o[i + 1] * inv);
+    for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<u32x2*>(out + i) =
+            u32x2{pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv)};
 }
 
-// Most runs a call of these bounds can be cut into.
-int most_runs(int B, int max_q, int heads, int max_len, int rows) {
-    const long blocks = ((long)max_q * heads + rows - 1) / rows;
+// How a call of these bounds is cut: rows per workgroup, workgroups per
+// group, most runs.
+struct LatentCut {
+    int rows, group, runs;
+};
+LatentCut latent_cut(int B, int max_q, int heads, int max_len) {
+    LatentCut c;
+    const long rows = (long)max_q * heads;
+    c.rows = rows > 32 ? 64 : 32;
+    const long blocks = (rows + c.rows - 1) / c.rows;
+    c.group = (int)(blocks < kMaxGroup ? blocks : kMaxGroup);
+    const long passes = (blocks + c.group - 1) / c.group;
     const long tiles = max_len > kTile ? (max_len + kTile - 1) / kTile : 1;
-    const long runs = (B * blocks * tiles + kMinRun - 1) / kMinRun;
-    return (int)(runs < kMaxRuns ? runs : kMaxRuns);
+    const long most = kMaxWorkgroups / c.group, all = B * passes * tiles;
+    c.runs = (int)(all < most ? all : most);
+    return c;
 }
-int block_rows(int max_q, int heads) { return (long)max_q * heads > 32 ? 64 : 32; }
 
 template <int RANK, int RG>
-void launch_rows(const LatentArgs& a, hipStream_t s) {
-    const int runs = most_runs(a.B, a.max_q, a.heads, a.max_len, RG * 32);
-    hipLaunchKernelGGL((latent_attention_kernel<RANK, RG>), dim3(runs), dim3(RG * 128), 0, s, a);
-    if (runs > 1) {
+void launch_rows(LatentArgs a, const LatentCut& cut, hipStream_t s) {
+    a.group = cut.group;
+    a.runs = cut.runs;
+    a.per_seq = a.cu_q ? 0 : a.T / a.B;
+    const int grid = (cut.runs + 7) / 8 * 8 * cut.group;
+    hipLaunchKernelGGL((latent_attention_kernel<RANK, RG>), dim3(grid), dim3(RG * 128), 0, s, a);
+    if (cut.runs > 1) {
         const int rows = a.max_q * a.heads;
-        hipLaunchKernelGGL((latent_join_kernel<RANK, RG * 32>), dim3((rows + 3) / 4, a.B), dim3(256), 0, s, a, runs);
+        hipLaunchKernelGGL((latent_join_kernel<RANK, RG * 32>), dim3((rows + 3) / 4, a.B), dim3(256), 0, s, a);
     }
 }
 template <int RANK>
 void launch_rank(const LatentArgs& a, hipStream_t s) {
-    if (block_rows(a.max_q, a.heads) == 64)
-        launch_rows<RANK, 2>(a, s);
+    const LatentCut cut = latent_cut(a.B, a.max_q, a.heads, a.max_len);
+    if (cut.rows == 64)
+        launch_rows<RANK, 2>(a, cut, s);
     else
-        launch_rows<RANK, 1>(a, s);
+        launch_rows<RANK, 1>(a, cut, s);
 }
 
 }  // namespace
@@ -486,8 +590,8 @@ void launch_rank(const LatentArgs& a, hipStream_t s) {
 bool latent_shape_supported(int rank, int rope) { return rope == kRopeWidth && (rank == 512 || rank == 256); }
 
 size_t latent_workspace(int B, int max_q, int heads, int rank, int max_len) {
-    const int rows = block_rows(max_q, heads);
-    return (size_t)most_runs(B, max_q, heads, max_len, rows) * 2 * rows * (rank + 2) * sizeof(float);
+    const LatentCut c = latent_cut(B, max_q, heads, max_len);
+    return (size_t)c.runs * c.group * 2 * c.rows * (rank + 2) * sizeof(float);
 }
 
 hipError_t launch_latent_attention(const LatentArgs& a, hipStream_t s) {
