@@ -77,6 +77,12 @@ __device__ __forceinline__ void load_to_lds16(const void* base, unsigned offset,
                  "s"(__builtin_amdgcn_readfirstlane(dst))
                  : "memory");
 }
+// Four bytes per lane into LDS: lane l's bytes land at dst + 4 l.
+__device__ __forceinline__ void load_to_lds4(const void* src, unsigned dst) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(dst))
+                 : "memory");
+}
 // Waits until at most N of the wave's vector memory operations are
 // outstanding.
 template <int N>

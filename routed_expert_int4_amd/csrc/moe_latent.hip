@@ -132,7 +132,10 @@ __device__ __forceinline__ void find_tile(const LatentArgs& a, int at, int lane,
 
 // Runs the list is cut into, and where run g starts.
 __device__ __forceinline__ int run_count(int total, int most) { return total < most ? total : most; }
-__device__ __forceinline__ int run_start(int total, int runs, int g) { return (int)((long)total * g / runs); }
+__device__ __forceinline__ int run_start(int total, int runs, int g) {
+    const int each = total / runs, more = total - each * runs;  // the first `more` runs have one tile more
+    return g * each + (g < more ? g : more);
+}
 
 // Partial sums of one workgroup: [2][ROWS][RANK] fp32, then (maximum, total)
 // pairs; the second half is for the unit it starts, the first for the one it
@@ -152,16 +155,31 @@ __device__ __forceinline__ int place_mix(int r) { return ((r & 3) << 2) | ((r >>
 // registers of queries lie in the accumulation file, 128 of sums, the scores
 // and the LDS operands in the other (left to itself the compiler moves 240
 // registers between the two per tile).  It does not see hazards of assembly:
-// the leading s_nop covers operands written just before, settle() the states
-// from a matrix instruction to the first other reader of its result (19 at
-// most; instructions that accumulate into the same registers need none).
-__device__ __forceinline__ void mfma_scores(f32x16& s, bf16x8 keys, bf16x8 queries) {
-    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(keys), "a"(queries));
+// the s_nop covers operands that vector instructions have written just before
+// (the first of a row of instructions only: the others read what loads, whose
+// waits it inserts, brought), settle() the states from a matrix instruction to
+// the first other reader of its result (19 at most; instructions that
+// accumulate into the same registers need none).
+__device__ __forceinline__ void mfma_scores(f32x16& s, bf16x8 keys, bf16x8 queries, bool first) {
+    if (first)
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(keys), "a"(queries));
+    else
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(keys), "a"(queries));
 }
-__device__ __forceinline__ void mfma_sums(f32x16& o, bf16x8 values, bf16x8 p) {
-    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(o) : "v"(values), "v"(p));
+__device__ __forceinline__ void mfma_sums(f32x16& o, bf16x8 values, bf16x8 p, bool first) {
+    if (first)
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(o) : "v"(values), "v"(p));
+    else
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(o) : "v"(values), "v"(p));
 }
-__device__ __forceinline__ void settle(f32x16& v) { asm("s_nop 15\n\ts_nop 3" : "+v"(v)); }
+__device__ __forceinline__ void settle(f32x16& v) { asm volatile("s_nop 15\n\ts_nop 3" : "+v"(v)); }
+
+template <int N>
+__device__ __forceinline__ void settle(f32x16 (&o)[N]) {
+    settle(o[0]);
+#pragma unroll
+    for (int k = 1; k < N; ++k) asm volatile("" : "+v"(o[k]));  // volatile: behind the wait
+}
 
 // The n lowest bits (none below 0, all from 64 up).
 __device__ __forceinline__ unsigned long long low_bits(int n) {
@@ -194,24 +212,18 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
     const float c = a.scale * 1.44269504088896340736f;
     const unsigned page_magic = 0xFFFFFFFFu / (unsigned)a.page_size;
 
-    // This lane's places in a tile: keys (row reads, 16 bytes; the low bits of
-    // the chunk are mixed with the row, the rest is an immediate offset) and
-    // values (transposed reads of four keys, 8 bytes).
-    unsigned key_at[8], rope_at[kRope], value_lo[4], value_hi[4];
+    // This lane's places in a tile: keys (row reads of 16 bytes) and values
+    // (transposed reads of four keys, 8 bytes; the next four keys 8 rows on).
+    // Only the low four bits of a row's chunk are mixed with the row and rows
+    // are whole multiples of 256 bytes, so an exclusive or and an immediate
+    // offset reach every chunk from these.
+    unsigned key_at, rope_at, value_at;
     {
-        const int r = side * 32 + col;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) key_at[k] = r * RANK * 2 + ((k * 2 + half) ^ place_mix(r)) * 16;
-#pragma unroll
-        for (int k = 0; k < kRope; ++k)
-            rope_at[k] = kLatBytes + r * kRopeWidth * 2 + (((k * 2 + half) ^ (r >> 1)) & 7) * 16;
-        const int vr = half * 4 + ((lane & 15) >> 2);
-        const int chunk = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), sub = (lane & 1) * 8 + side * RANK;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            value_lo[k] = vr * RANK * 2 + ((k * 4 + chunk) ^ place_mix(vr)) * 16 + sub;
-            value_hi[k] = (vr + 8) * RANK * 2 + ((k * 4 + chunk) ^ place_mix(vr + 8)) * 16 + sub;
-        }
+        const int r = side * 32 + col, vr = half * 4 + ((lane & 15) >> 2);
+        key_at = lds0 + r * RANK * 2 + (half ^ place_mix(r)) * 16;
+        rope_at = lds0 + kLatBytes + r * kRopeWidth * 2 + ((half ^ (r >> 1)) & 7) * 16;
+        const int chunk = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+        value_at = lds0 + vr * RANK * 2 + side * RANK + (chunk ^ place_mix(vr)) * 16 + (lane & 1) * 8;
     }
 
     while (at < run_end) {
@@ -287,6 +299,10 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
         f32x16 o[kOut] = {};
         int off, page = page_of(t_first, off);
         unsigned long long valid = __ballot((unsigned)page < (unsigned)a.n_pages);
+        // the queries have landed: the compiler must not wait for them inside
+        // the loop, where other loads are on their way
+#pragma unroll
+        for (int k = 0; k < kLat + kRope; ++k) asm volatile("" : "+a"(qf[k]));
         {
             const unsigned long long addr = address(page, off);
 #pragma unroll
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             page = page_of(t + 2, off);
             int chunk = lane;
             asm volatile("" : "+v"(chunk));  // the mixed places are not worth a register each across the loop
-            const unsigned tile = lds0 + buf * kTileBytes;
+            const unsigned tile = buf * kTileBytes;
             f32x16 s = {};
             {
                 // operands are read kAhead instructions before their use; the
@@ -315,9 +331,9 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 bf16x8 x[kAhead];
                 unsigned key_base[8], rope_base[kRope];  // plus immediate offsets
 #pragma unroll
-                for (int k = 0; k < 8; ++k) key_base[k] = key_at[k] + tile;
+                for (int k = 0; k < 8; ++k) key_base[k] = (key_at + tile) ^ k * 32;
 #pragma unroll
-                for (int k = 0; k < kRope; ++k) rope_base[k] = rope_at[k] + tile;
+                for (int k = 0; k < kRope; ++k) rope_base[k] = (rope_at + tile) ^ k * 32;
                 auto key_chunk = [&](int k) {
                     return lds_chunk(k < kLat ? key_base[k & 7] + (k >> 3) * 256 : rope_base[k - kLat]);
                 };
@@ -325,7 +341,7 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 for (int k = 0; k < kAhead; ++k) x[k] = key_chunk(k);
 #pragma unroll
                 for (int k = 0; k < kLat + kRope; ++k) {
-                    mfma_scores(s, x[k % kAhead], qf[k]);
+                    mfma_scores(s, x[k % kAhead], qf[k], k == 0);
                     if (k + kAhead < kLat + kRope) x[k % kAhead] = key_chunk(k + kAhead);
                     // the next tile's loads, spread over the instructions (a
                     // wave that issues them in one go stalls in the queue)
@@ -363,8 +379,8 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             unsigned lo[4], hi[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                lo[k] = value_lo[k] + tile;
-                hi[k] = value_hi[k] + tile;
+                lo[k] = (value_at + tile) ^ k * 64;
+                hi[k] = (lo[k] ^ 32) + 8 * RANK * 2;
             }
             auto value_chunk = [&](int j) {
                 const int k = j >> 2, at_key = (j & 3) * 16 * RANK * 2 + (k >> 2) * 256;
@@ -406,11 +422,11 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 const float f = __builtin_amdgcn_exp2f((m - nm) * c);
                 m = nm;
                 l *= f;
+                if (t > t_first) {  // else there is nothing to bring to it
 #pragma unroll
-                for (int k = 0; k < kOut; ++k) {
-                    settle(o[k]);
+                    for (int k = 0; k < kOut; ++k)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[k][i] *= f;
+                        for (int i = 0; i < 16; ++i) o[k][i] *= f;
                 }
                 lds_barrier();  // the first ones are read
                 sum = exponentials();
@@ -431,14 +447,13 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < 4 * kOut; ++j) {
-                    mfma_sums(o[j >> 2], x[j % kAhead], p[j & 3]);
+                    mfma_sums(o[j >> 2], x[j % kAhead], p[j & 3], j == 0);
                     if (j + kAhead < 4 * kOut) x[j % kAhead] = value_chunk(j + kAhead);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                settle(o);
             }
         }
-#pragma unroll
-        for (int k = 0; k < kOut; ++k) settle(o[k]);
         // totals over the tile halves of both waves
         l = half_sum(l);
         __syncthreads();
@@ -491,12 +506,8 @@ __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
     const int block = row / ROWS, r = row % ROWS, member = block % a.group;
     const int u0 = before + block / a.group * shape.tiles, u1 = u0 + shape.tiles;
     // runs that hold the unit's first and last tile
-    auto run_of = [&](int tile) {
-        int g = (int)((long)tile * runs / total);
-        while (g + 1 < runs && run_start(total, runs, g + 1) <= tile) ++g;
-        while (g > 0 && run_start(total, runs, g) > tile) --g;
-        return g;
-    };
+    const int each = total / runs, more = total - each * runs, longer = more * (each + 1);
+    auto run_of = [&](int tile) { return tile < longer ? tile / (each + 1) : more + (tile - longer) / each; };
     const int g0 = run_of(u0), g1 = run_of(u1 - 1);
     if (g0 == g1) return;  // one run held it all and wrote the result
     auto part = [&](int g) { return part_sums<ROWS, RANK>(a, (g * a.group + member) * 2 + (g == g0)); };
