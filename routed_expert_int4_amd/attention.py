@@ -23,6 +23,8 @@ from . import binding as B
 
 _BF16, _F32, _FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _TYPES = {_BF16: 0, _F32: 1}  # MOE_BF16, MOE_F32
+_WIDE, _BF16_ONLY, _FP8_ONLY, _F32_ONLY = (_BF16, _F32), (_BF16,), (_FP8,), (_F32,)
+_I32_ONLY, _I64_ONLY = (torch.int32,), (torch.int64,)
 GROUP = 128                   # columns (and weight rows) that share a scale
 
 
@@ -42,17 +44,30 @@ class AppendOut(NamedTuple):
     key: torch.Tensor | None     # rotated position part of the keys
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(t: torch.Tensor, stream):
+    """Handle of `stream`, or of the current stream of t's device."""
+    if stream is None:
+        return _raw_stream(t.device.index) if _raw_stream is not None else torch.cuda.current_stream(t.device).cuda_stream
+    return B._stream_handle(stream)
+
+
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise B.MoeError(B.MOE_EINVAL, what)
 
 
-def _rows(t: torch.Tensor, name: str, dims: int, dtypes) -> None:
-    """A device tensor of `dims` dimensions with a contiguous last one."""
-    if t.dim() != dims or t.dtype not in dtypes or not t.is_cuda or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise B.MoeError(B.MOE_EINVAL, f"{name}: a device tensor of {dims} dimensions, contiguous in the last, of type "
-                                       f"{' or '.join(str(d) for d in dtypes)} is needed, got {t.dtype} {tuple(t.shape)} "
-                                       f"with strides {t.stride()} on {t.device}")
+def _rows(t: torch.Tensor, name: str, dims: int, dtypes):
+    """Shape and strides of a device tensor of `dims` dimensions with a
+    contiguous last one."""
+    shape, stride = t.shape, t.stride()
+    if len(stride) == dims and t.dtype in dtypes and t.is_cuda and (stride[-1] == 1 or shape[-1] <= 1):
+        return shape, stride
+    raise B.MoeError(B.MOE_EINVAL, f"{name}: a device tensor of {dims} dimensions, contiguous in the last, of type "
+                                   f"{' or '.join(str(d) for d in dtypes)} is needed, got {t.dtype} {tuple(shape)} "
+                                   f"with strides {stride} on {t.device}")
 
 
 def _scales(T: int, H: int, device) -> torch.Tensor:
@@ -74,34 +89,40 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, out: str = "bf16", 
     "fp8" (codes and one scale per 128 columns) or "both".  h is returned in
     the residual's type (sum_out, which may be the residual itself, receives
     it in place; want_sum=False leaves it out)."""
-    _rows(x, "x", 2, (_BF16, _F32))
-    _rows(weight, "weight", 1, (_BF16, _F32))
-    T, H = x.shape
-    _need(weight.shape[0] == H, f"weight has {weight.shape[0]} values, x {H} columns")
-    r_stride, r_type, sum_type = 0, 0, x.dtype
+    shape, strides = _rows(x, "x", 2, _WIDE)
+    wide, _ = _rows(weight, "weight", 1, _WIDE)
+    T, H = shape
+    if wide[0] != H:
+        _need(False, f"weight has {wide[0]} values, x {H} columns")
+    x_type = _TYPES[x.dtype]
+    residual_p, r_stride, r_type, sum_type = None, 0, 0, x.dtype
     if residual is not None:
-        _rows(residual, "residual", 2, (_BF16, _F32))
-        _need(residual.shape == x.shape, f"residual {tuple(residual.shape)}, x {tuple(x.shape)}")
-        r_stride, sum_type = residual.stride(0) if T > 1 else H, residual.dtype
+        r_shape, r_strides = _rows(residual, "residual", 2, _WIDE)
+        if r_shape != shape:
+            _need(False, f"residual {tuple(r_shape)}, x {tuple(shape)}")
+        residual_p, r_stride, sum_type = residual.data_ptr(), r_strides[0] if T > 1 else H, residual.dtype
         r_type = _TYPES[sum_type]
     dev = x.device
+    sum_p, s_stride = None, H
     if sum_out is not None:
-        _rows(sum_out, "sum_out", 2, (sum_type,))
-        _need(sum_out.shape == x.shape, f"sum_out {tuple(sum_out.shape)}, x {tuple(x.shape)}")
+        s_shape, s_strides = _rows(sum_out, "sum_out", 2, (sum_type,))
+        _need(s_shape == shape, f"sum_out {tuple(s_shape)}, x {tuple(shape)}")
+        sum_p, s_stride = sum_out.data_ptr(), s_strides[0] if T > 1 else H
     elif want_sum and residual is not None:
-        sum_out = torch.empty((T, H), dtype=sum_type, device=dev)
-    _need(out in ("bf16", "fp8", "both"), f"out: {out!r}")
-    y = torch.empty((T, H), dtype=_BF16, device=dev) if out != "fp8" else None
-    q = scale = None
+        sum_out = torch.empty(shape, dtype=sum_type, device=dev)
+        sum_p = sum_out.data_ptr()
+    y = q = scale = y_p = q_p = scale_p = None
+    pad = -(-H // 16) * 16
+    if out != "fp8":
+        _need(out in ("bf16", "both"), f"out: {out!r}")
+        y = torch.empty(shape, dtype=_BF16, device=dev)
+        y_p = y.data_ptr()
     if out != "bf16":
         q, scale = _codes(T, H, dev), _scales(T, H, dev)
-    B.check(B.lib().moe_add_rmsnorm(
-        x.data_ptr(), _TYPES[x.dtype], x.stride(0) if T > 1 else H, residual.data_ptr() if residual is not None else None,
-        r_type, r_stride, weight.data_ptr(), _TYPES[weight.dtype], T, H, eps,
-        sum_out.data_ptr() if sum_out is not None else None, sum_out.stride(0) if sum_out is not None and T > 1 else H,
-        y.data_ptr() if y is not None else None, H, q.data_ptr() if q is not None else None,
-        q.stride(0) if q is not None else H, scale.data_ptr() if scale is not None else None, 1, T,
-        B._stream_handle(stream)))
+        q_p, scale_p = q.data_ptr(), scale.data_ptr()
+    B.check(B.lib().moe_add_rmsnorm(x.data_ptr(), x_type, strides[0] if T > 1 else H, residual_p, r_type, r_stride,
+                                    weight.data_ptr(), _TYPES[weight.dtype], T, H, eps, sum_p, s_stride, y_p, H, q_p, pad,
+                                    scale_p, 1, T, _stream(x, stream)))
     return NormOut(sum_out, y, q, scale)
 
 
@@ -110,27 +131,26 @@ def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -
     w [N, K] 8-bit with w_scale [ceil(N / 128), ceil(K / 128)]: [M, N] in
     out_dtype (bf16 or fp32).  K is a multiple of 16; a_scale may have any
     strides (add_rmsnorm's are the fastest)."""
-    _rows(a, "a", 2, (_FP8,))
-    _rows(w, "w", 2, (_FP8,))
-    _rows(w_scale, "w_scale", 2, (_F32,))
-    (M, K), N = a.shape, w.shape[0]
-    kb = (K + GROUP - 1) // GROUP
-    _need(w.shape[1] == K, f"a has {K} inner columns, w {w.shape[1]}")
-    _need(a_scale.dtype == _F32 and a_scale.is_cuda and tuple(a_scale.shape) == (M, kb),
-          f"a_scale: fp32 {(M, kb)} on the device is needed, got {a_scale.dtype} {tuple(a_scale.shape)}")
-    _need(tuple(w_scale.shape) == ((N + GROUP - 1) // GROUP, kb),
-          f"w_scale {tuple(w_scale.shape)}, {((N + GROUP - 1) // GROUP, kb)} is needed")
+    (M, K), a_strides = _rows(a, "a", 2, _FP8_ONLY)
+    (N, wk), w_strides = _rows(w, "w", 2, _FP8_ONLY)
+    ws_shape, ws_strides = _rows(w_scale, "w_scale", 2, _F32_ONLY)
+    kb, nb = (K + GROUP - 1) // GROUP, (N + GROUP - 1) // GROUP
+    as_shape, as_strides = a_scale.shape, a_scale.stride()
+    if wk != K or a_scale.dtype is not _F32 or not a_scale.is_cuda or tuple(as_shape) != (M, kb) or tuple(ws_shape) != (nb, kb):
+        _need(False, f"a {(M, K)} and w {(N, wk)} need scales of fp32 {(M, kb)} and {(nb, kb)} on the device, got "
+                     f"{a_scale.dtype} {tuple(as_shape)} and {tuple(ws_shape)}, and the same inner width")
     if out is None:
         _need(out_dtype in _TYPES, f"out_dtype {out_dtype}: bf16 or fp32")
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out, o_stride = torch.empty((M, N), dtype=out_dtype, device=a.device), N
     else:
-        _rows(out, "out", 2, (_BF16, _F32))
-        _need(tuple(out.shape) == (M, N), f"out {tuple(out.shape)}, {(M, N)} is needed")
-    B.check(B.lib().moe_fp8_linear(
-        a.data_ptr(), a.stride(0) if M > 1 else -(-K // 16) * 16, a_scale.data_ptr(), a_scale.stride(0),
-        a_scale.stride(1), w.data_ptr(), w.stride(0) if N > 1 else -(-K // 16) * 16, w_scale.data_ptr(),
-        w_scale.stride(0) if w_scale.shape[0] > 1 else kb, M, N, K, out.data_ptr(), _TYPES[out.dtype],
-        out.stride(0) if M > 1 else N, B._stream_handle(stream)))
+        o_shape, o_strides = _rows(out, "out", 2, _WIDE)
+        _need(tuple(o_shape) == (M, N), f"out {tuple(o_shape)}, {(M, N)} is needed")
+        out_dtype, o_stride = out.dtype, o_strides[0] if M > 1 else N
+    pad = -(-K // 16) * 16  # the stride of a single row says nothing
+    B.check(B.lib().moe_fp8_linear(a.data_ptr(), a_strides[0] if M > 1 else pad, a_scale.data_ptr(), as_strides[0],
+                                   as_strides[1], w.data_ptr(), w_strides[0] if N > 1 else pad, w_scale.data_ptr(),
+                                   ws_strides[0] if nb > 1 else kb, M, N, K, out.data_ptr(), _TYPES[out_dtype], o_stride,
+                                   _stream(a, stream)))
     return out
 
 
@@ -138,19 +158,18 @@ def head_linear(x, w, out=None, stream=None) -> torch.Tensor:
     """x [T, heads, K] times the transpose of w [heads, N, K], head by head:
     [T, heads, N], all bf16.  x and out may be strided views (of a wider
     query, say)."""
-    _rows(x, "x", 3, (_BF16,))
-    _rows(w, "w", 3, (_BF16,))
-    T, heads, K = x.shape
-    N = w.shape[1]
-    _need(w.shape[0] == heads and w.shape[2] == K and w.is_contiguous(),
-          f"w: contiguous {(heads, 'N', K)} is needed, got {tuple(w.shape)} with strides {w.stride()}")
+    (T, heads, K), xs = _rows(x, "x", 3, _BF16_ONLY)
+    w_shape, _ = _rows(w, "w", 3, _BF16_ONLY)
+    N = w_shape[1]
+    if w_shape[0] != heads or w_shape[2] != K or not w.is_contiguous():
+        _need(False, f"w: contiguous {(heads, 'N', K)} is needed, got {tuple(w_shape)} with strides {w.stride()}")
     if out is None:
-        out = torch.empty((T, heads, N), dtype=_BF16, device=x.device)
+        out, os = torch.empty((T, heads, N), dtype=_BF16, device=x.device), (heads * N, N)
     else:
-        _rows(out, "out", 3, (_BF16,))
-        _need(tuple(out.shape) == (T, heads, N), f"out {tuple(out.shape)}, {(T, heads, N)} is needed")
-    B.check(B.lib().moe_head_linear(x.data_ptr(), x.stride(0), x.stride(1), w.data_ptr(), T, heads, K, N,
-                                    out.data_ptr(), out.stride(0), out.stride(1), B._stream_handle(stream)))
+        o_shape, os = _rows(out, "out", 3, _BF16_ONLY)
+        _need(tuple(o_shape) == (T, heads, N), f"out {tuple(o_shape)}, {(T, heads, N)} is needed")
+    B.check(B.lib().moe_head_linear(x.data_ptr(), xs[0], xs[1], w.data_ptr(), T, heads, K, N, out.data_ptr(), os[0], os[1],
+                                    _stream(x, stream)))
     return out
 
 
@@ -165,44 +184,45 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
     page_size, rank + rope] contiguous.  q_rope [T, heads, rope] is rotated
     into q_out (given, the view itself for in place, or new).  want_fp8: the
     normed latent in 8 bits too; want_key: the rotated key part too."""
-    _rows(kv, "kv", 2, (_BF16,))
-    _rows(weight, "weight", 1, (_BF16, _F32))
-    _rows(table, "table", 2, (_F32,))
-    _rows(positions, "positions", 1, (torch.int32,))
-    T, rank, rope = kv.shape[0], weight.shape[0], table.shape[1]
-    _need(kv.shape[1] == rank + rope, f"kv has {kv.shape[1]} columns, weight and table {rank} + {rope}")
-    _need(positions.shape[0] == T and table.is_contiguous(), "positions: one per token; table: contiguous")
+    (T, width), kvs = _rows(kv, "kv", 2, _BF16_ONLY)
+    (rank,), _ = _rows(weight, "weight", 1, _WIDE)
+    (n_positions, rope), _ = _rows(table, "table", 2, _F32_ONLY)
+    (n,), _ = _rows(positions, "positions", 1, _I32_ONLY)
+    if width != rank + rope or n != T or not table.is_contiguous():
+        _need(False, f"kv has {width} columns, weight and table {rank} + {rope}; {n} positions for {T} tokens; table "
+                     "contiguous")
     cache_p = slots_p = None
     n_slots = 0
     if cache is not None:
-        _need(cache.dtype == _BF16 and cache.is_cuda and cache.is_contiguous() and cache.shape[-1] == rank + rope,
-              f"cache: contiguous bf16 rows of {rank + rope} are needed, got {cache.dtype} {tuple(cache.shape)}")
+        if cache.dtype is not _BF16 or not cache.is_cuda or not cache.is_contiguous() or cache.shape[-1] != width:
+            _need(False, f"cache: contiguous bf16 rows of {width} are needed, got {cache.dtype} {tuple(cache.shape)}")
         _need(slots is not None, "a cache needs slots")
-        _rows(slots, "slots", 1, (torch.int64,))
-        _need(slots.shape[0] == T, f"{slots.shape[0]} slots for {T} tokens")
-        cache_p, slots_p, n_slots = cache.data_ptr(), slots.data_ptr(), cache.numel() // (rank + rope)
+        (n,), _ = _rows(slots, "slots", 1, _I64_ONLY)
+        _need(n == T, f"{n} slots for {T} tokens")
+        cache_p, slots_p, n_slots = cache.data_ptr(), slots.data_ptr(), cache.numel() // width
     heads, qs, qo, qp, qop = 0, (0, 0), (0, 0), None, None
     if q_rope is not None:
-        _rows(q_rope, "q_rope", 3, (_BF16,))
-        _need(q_rope.shape[0] == T and q_rope.shape[2] == rope, f"q_rope {tuple(q_rope.shape)}, {(T, 'heads', rope)} is needed")
-        heads = q_rope.shape[1]
+        q_shape, qs = _rows(q_rope, "q_rope", 3, _BF16_ONLY)
+        if q_shape[0] != T or q_shape[2] != rope:
+            _need(False, f"q_rope {tuple(q_shape)}, {(T, 'heads', rope)} is needed")
+        heads = q_shape[1]
         if q_out is None:
-            q_out = torch.empty((T, heads, rope), dtype=_BF16, device=kv.device)
+            q_out, qo = torch.empty(q_shape, dtype=_BF16, device=kv.device), (heads * rope, rope)
         else:
-            _rows(q_out, "q_out", 3, (_BF16,))
-            _need(q_out.shape == q_rope.shape, f"q_out {tuple(q_out.shape)}, q_rope {tuple(q_rope.shape)}")
-        qs, qo, qp, qop = q_rope.stride(), q_out.stride(), q_rope.data_ptr(), q_out.data_ptr()
-    q = scale = key = None
+            qo_shape, qo = _rows(q_out, "q_out", 3, _BF16_ONLY)
+            _need(qo_shape == q_shape, f"q_out {tuple(qo_shape)}, q_rope {tuple(q_shape)}")
+        qp, qop = q_rope.data_ptr(), q_out.data_ptr()
+    q = scale = key = q_p = scale_p = key_p = None
     if want_fp8:
         q, scale = _codes(T, rank, kv.device), _scales(T, rank, kv.device)
+        q_p, scale_p = q.data_ptr(), scale.data_ptr()
     if want_key:
         key = torch.empty((T, rope), dtype=_BF16, device=kv.device)
+        key_p = key.data_ptr()
     B.check(B.lib().moe_latent_append(
-        kv.data_ptr(), kv.stride(0) if T > 1 else rank + rope, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
-        table.data_ptr(), table.shape[0], positions.data_ptr(), slots_p, T, cache_p, n_slots, qp, heads, qs[0], qs[1],
-        qop, qo[0], qo[1], q.data_ptr() if q is not None else None, q.stride(0) if q is not None else 0,
-        scale.data_ptr() if scale is not None else None, 1, T, key.data_ptr() if key is not None else None, rope,
-        B._stream_handle(stream)))
+        kv.data_ptr(), kvs[0] if T > 1 else width, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
+        table.data_ptr(), n_positions, positions.data_ptr(), slots_p, T, cache_p, n_slots, qp, heads, qs[0], qs[1],
+        qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, key_p, rope, _stream(kv, stream)))
     return AppendOut(q_out if q_rope is not None else None, q, scale, key)
 
 
@@ -220,44 +240,44 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     the sequence's j-th new token, itself included if set).  Returns
     [T, heads, rank] bf16.  workspace: uint8 of
     moe_latent_attention_workspace() bytes (allocated per call if None)."""
-    _rows(q, "q", 3, (_BF16,))
-    _rows(cache, "cache", 3, (_BF16,))
-    _rows(pages, "pages", 2, (torch.int32,))
-    _rows(lens, "lens", 1, (torch.int32,))
-    T, heads, width = q.shape
-    n_pages, page_size = cache.shape[0], cache.shape[1]
-    nb, per_seq = pages.shape
+    (T, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY)
+    (n_pages, page_size, c_width), cs = _rows(cache, "cache", 3, _BF16_ONLY)
+    (nb, per_seq), ps = _rows(pages, "pages", 2, _I32_ONLY)
+    (n,), _ = _rows(lens, "lens", 1, _I32_ONLY)
     rope = 64
     rank = width - rope
-    _need(cache.shape[2] == width and (page_size == 1 or cache.stride(1) == width),
-          f"cache: rows of {width} one after another in a page are needed, got {tuple(cache.shape)} with strides {cache.stride()}")
-    _need(lens.shape[0] == nb, f"{lens.shape[0]} lengths for {nb} page rows")
+    if c_width != width or (page_size > 1 and cs[1] != width) or n != nb:
+        _need(False, f"cache: rows of {width} one after another in a page are needed, got {tuple(cache.shape)} with strides "
+                     f"{cs}; {n} lengths for {nb} page rows")
+    cu_p = tree_p = None
     if cu_q is not None:
-        _rows(cu_q, "cu_q", 1, (torch.int32,))
-        _need(cu_q.shape[0] == nb + 1, f"cu_q has {cu_q.shape[0]} entries for {nb} sequences")
-        _need(max_q is not None, "cu_q needs max_q")
+        (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY)
+        _need(n == nb + 1 and max_q is not None, f"cu_q has {n} entries for {nb} sequences; it needs max_q")
+        cu_p = cu_q.data_ptr()
     else:
         max_q = T // nb if nb else 0
     if max_len is None:
         max_len = per_seq * page_size
     if tree is not None:
-        _rows(tree, "tree", 1, (torch.int64,))
-        _need(tree.shape[0] == T, f"tree has {tree.shape[0]} masks for {T} tokens")
+        (n,), _ = _rows(tree, "tree", 1, _I64_ONLY)
+        _need(n == T, f"tree has {n} masks for {T} tokens")
+        tree_p = tree.data_ptr()
     if out is None:
-        out = torch.empty((T, heads, rank), dtype=_BF16, device=q.device)
+        out, os = torch.empty((T, heads, rank), dtype=_BF16, device=q.device), (heads * rank, rank)
     else:
-        _rows(out, "out", 3, (_BF16,))
-        _need(tuple(out.shape) == (T, heads, rank), f"out {tuple(out.shape)}, {(T, heads, rank)} is needed")
+        o_shape, os = _rows(out, "out", 3, _BF16_ONLY)
+        _need(tuple(o_shape) == (T, heads, rank), f"out {tuple(o_shape)}, {(T, heads, rank)} is needed")
     L = B.lib()
     if workspace is None:
-        workspace = torch.empty(L.moe_latent_attention_workspace(nb, max_q, heads, rank, max_len), dtype=torch.uint8,
-                                device=q.device)
+        n = L.moe_latent_attention_workspace(nb, max_q, heads, rank, max_len)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    else:
+        n = workspace.numel() * workspace.element_size()
     B.check(L.moe_latent_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), T, heads, rank, rope, cache.data_ptr(), n_pages, page_size,
-        cache.stride(0) if n_pages > 1 else page_size * width, pages.data_ptr(), pages.stride(0) if nb > 1 else per_seq,
-        per_seq, lens.data_ptr(), nb, cu_q.data_ptr() if cu_q is not None else None, max_q, max_len,
-        tree.data_ptr() if tree is not None else None, scale, out.data_ptr(), out.stride(0), out.stride(1),
-        workspace.data_ptr(), workspace.numel(), B._stream_handle(stream)))
+        q.data_ptr(), qs[0], qs[1], T, heads, rank, rope, cache.data_ptr(), n_pages, page_size,
+        cs[0] if n_pages > 1 else page_size * width, pages.data_ptr(), ps[0] if nb > 1 else per_seq, per_seq,
+        lens.data_ptr(), nb, cu_p, max_q, max_len, tree_p, scale, out.data_ptr(), os[0], os[1], workspace.data_ptr(), n,
+        _stream(q, stream)))
     return out
 
 
@@ -271,32 +291,28 @@ def prompt_attention(q, k, k_rope, v, scale: float, cu_q=None, cu_k=None, max_q:
     cu_k[b] .. cu_k[b + 1] (int32 [B + 1]; None: one sequence); its queries
     are its last positions.  max_q bounds the queries of a sequence; max_k is
     not needed.  Returns [Tq, heads, vdim] bf16."""
-    _rows(q, "q", 3, (_BF16,))
-    _rows(k, "k", 3, (_BF16,))
-    _rows(k_rope, "k_rope", 2, (_BF16,))
-    _rows(v, "v", 3, (_BF16,))
-    Tq, heads, width = q.shape
-    Tk, rope, vdim = k.shape[0], k_rope.shape[1], v.shape[2]
-    _need(k.shape[1] == heads and v.shape[1] == heads and v.shape[0] == Tk and k_rope.shape[0] == Tk
-          and k.shape[2] + rope == width,
-          f"q {tuple(q.shape)}, k {tuple(k.shape)}, k_rope {tuple(k_rope.shape)}, v {tuple(v.shape)} do not go together")
+    (Tq, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY)
+    (Tk, k_heads, nope), ks = _rows(k, "k", 3, _BF16_ONLY)
+    (r_rows, rope), rs = _rows(k_rope, "k_rope", 2, _BF16_ONLY)
+    (v_rows, v_heads, vdim), vs = _rows(v, "v", 3, _BF16_ONLY)
+    if k_heads != heads or v_heads != heads or v_rows != Tk or r_rows != Tk or nope + rope != width:
+        _need(False, f"q {tuple(q.shape)}, k {tuple(k.shape)}, k_rope {tuple(k_rope.shape)}, v {tuple(v.shape)} do not go "
+                     "together")
     _need((cu_q is None) == (cu_k is None), "cu_q and cu_k go together")
     if cu_q is None:
         cu_q = torch.tensor([0, Tq], dtype=torch.int32, device=q.device)
         cu_k = torch.tensor([0, Tk], dtype=torch.int32, device=q.device)
         max_q = Tq
-    _rows(cu_q, "cu_q", 1, (torch.int32,))
-    _rows(cu_k, "cu_k", 1, (torch.int32,))
-    _need(cu_q.shape == cu_k.shape and cu_q.shape[0] >= 1 and max_q is not None,
-          "cu_q and cu_k: one more entry than sequences each, and max_q")
+    (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY)
+    (n_k,), _ = _rows(cu_k, "cu_k", 1, _I32_ONLY)
+    _need(n == n_k and n >= 1 and max_q is not None, "cu_q and cu_k: one more entry than sequences each, and max_q")
     if out is None:
-        out = torch.empty((Tq, heads, vdim), dtype=_BF16, device=q.device)
+        out, os = torch.empty((Tq, heads, vdim), dtype=_BF16, device=q.device), (heads * vdim, vdim)
     else:
-        _rows(out, "out", 3, (_BF16,))
-        _need(tuple(out.shape) == (Tq, heads, vdim), f"out {tuple(out.shape)}, {(Tq, heads, vdim)} is needed")
+        o_shape, os = _rows(out, "out", 3, _BF16_ONLY)
+        _need(tuple(o_shape) == (Tq, heads, vdim), f"out {tuple(o_shape)}, {(Tq, heads, vdim)} is needed")
     B.check(B.lib().moe_prompt_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), k_rope.data_ptr(),
-        k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1), Tq, Tk, heads, k.shape[2], rope, vdim,
-        cu_q.data_ptr(), cu_k.data_ptr(), cu_q.shape[0] - 1, max_q, int(bool(causal)), scale, out.data_ptr(),
-        out.stride(0), out.stride(1), B._stream_handle(stream)))
+        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], k_rope.data_ptr(), rs[0], v.data_ptr(), vs[0], vs[1], Tq,
+        Tk, heads, nope, rope, vdim, cu_q.data_ptr(), cu_k.data_ptr(), n - 1, max_q, int(causal), scale, out.data_ptr(),
+        os[0], os[1], _stream(q, stream)))
     return out
