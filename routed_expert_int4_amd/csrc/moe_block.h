@@ -64,7 +64,7 @@ struct Fp8Args {
     void* out;
     long lda, as_t, as_k, ldw, ws_n, ldo;
     int M, N, K;
-    bool out_f32, out_vec;  // out_vec: four consecutive columns may be stored at once
+    bool out_f32, out_vec;  // out_vec: eight consecutive columns may be stored at once
 };
 hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t s);
 

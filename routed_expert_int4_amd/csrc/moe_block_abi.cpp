@@ -79,7 +79,7 @@ moe_status_t moe_fp8_linear(const uint8_t* d_a, int64_t a_stride, const float* d
     a.lda = a_stride, a.as_t = as_stride_m, a.as_k = as_stride_b, a.ldw = w_stride, a.ws_n = ws_stride;
     a.ldo = out_stride, a.M = M, a.N = N, a.K = K;
     a.out_f32 = out_type == MOE_F32;
-    a.out_vec = out_stride % 4 == 0 && on(d_out, a.out_f32 ? 16 : 8);
+    a.out_vec = out_stride % 8 == 0 && on(d_out, 16);
     return launched(launch_fp8_linear(a, static_cast<hipStream_t>(stream)), who);
 }
 

@@ -147,15 +147,18 @@ __global__ void __launch_bounds__(512) fp8_rows_kernel(Fp8Args a) {
 // --------------------------------------------------------------- many tokens
 // Bound by the matrix cores.  WN x WT waves, each NT x TT instruction tiles;
 // both operands of one block of 128 columns go through LDS, loaded
-// asynchronously one block ahead into the other of two buffers.  A row of a
-// buffer is 128 bytes; its 16-byte chunk c sits at place c ^ ((row / 2) & 7),
-// so that the 16 rows of an operand read cover all banks.
-template <int WN, int WT, int NT, int TT>
+// asynchronously two blocks ahead into a ring of three buffers, with the
+// activation scales of each wave's tokens beside them (so that the loop's
+// only vector memory operations are counted ones).  A row of a buffer is 128
+// bytes; its 16-byte chunk c sits at place c ^ ((row / 2) & 7), so that the 16
+// rows of an operand read cover all banks.
+template <int WN, int WT, int NT, int TT, int kRing>
 __global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
     constexpr int kWaves = WN * WT, BN = WN * NT * 16, BT = WT * TT * 16, kRows = BN + BT;
-    constexpr int kLoads = kRows / 8 / kWaves;  // asynchronous loads per wave and block
-    static_assert(kRows % (8 * kWaves) == 0 && 128 % (NT * 16) == 0 && BN % 8 == 0, "tile shape");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kRows * 128];
+    constexpr int kLoads = kRows / 8 / kWaves;  // asynchronous loads per wave and block, and one of scales
+    static_assert(kWaves % 2 == 0 && kRows % (8 * kWaves) == 0 && 128 % (NT * 16) == 0 && BN % (8 * kWaves) == 0 && TT * 16 <= 64, "tile shape");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing][kRows * 128];
+    __shared__ float scales[kWaves][kRing][64];
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = wave_in_block();
     const int wn = wave % WN, wt = wave / WN;
     // Workgroups are dealt to the eight dies in turn: each die gets a
@@ -168,74 +171,75 @@ __global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
     const int in_band = tiles_n - g * band < band ? tiles_n - g * band : band;
     const int n0 = (g * band + (pid % band_size) % in_band) * BN, t0 = ((pid % band_size) / in_band) * BT;
 
-    // per-lane source of each load: rows past the end repeat the last one
-    const uint8_t* base[kLoads];
-    int chunk[kLoads];
+    // Loads: offset of each from the tile's first row; rows past the end
+    // repeat the last one.  A wave's first loads are weights, the others
+    // activations.
+    constexpr int kWeightLoads = BN / 8 / kWaves;
+    const uint8_t* w_base = a.w + (long)n0 * a.ldw;
+    const uint8_t* a_base = a.a + (long)t0 * a.lda;
+    unsigned off[kLoads];
+    const int chunk = ((lane & 7) ^ ((wave * 8 + (lane >> 3)) >> 1)) & 7;  // the same in all of them: kWaves is even
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int r0 = (i * kWaves + wave) * 8, r = r0 + (lane >> 3);
-        chunk[i] = ((lane & 7) ^ (r >> 1)) & 7;
-        if (r0 < BN) {
-            const int n = n0 + r;
-            base[i] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
-        } else {
-            const int t = t0 + r - BN;
-            base[i] = a.a + (long)(t < a.M ? t : a.M - 1) * a.lda;
-        }
-        base[i] += chunk[i] * 16;
+        const int r = (i * kWaves + wave) * 8 + (lane >> 3);
+        const int n = n0 + r < a.N ? r : a.N - 1 - n0, t = t0 + r - BN < a.M ? r - BN : a.M - 1 - t0;
+        off[i] = (i < kWeightLoads ? (unsigned)n * (unsigned)a.ldw : (unsigned)t * (unsigned)a.lda) + chunk * 16;
     }
-    const int blocks = (a.K + 127) >> 7;
-    const unsigned lds0 = lds_address(&lds[0][0]);
-    auto issue = [&](int b) {
-        const unsigned dst = lds0 + (b & 1) * kRows * 128 + wave * 1024;
-        const bool whole = b * 128 + 128 <= a.K;
+    const int blocks = (a.K + 127) >> 7, wave_t = t0 + wt * TT * 16;
+    const int my_t = wave_t + lane % (TT * 16);
+    const float* my_scale = a.a_scale + (long)(my_t < a.M ? my_t : a.M - 1) * a.as_t;
+    const unsigned lds0 = lds_address(&lds[0][0]), scales0 = lds_address(&scales[wave][0][0]);
+    auto issue = [&](int b, int stage) {
+        const unsigned dst = lds0 + stage * kRows * 128 + wave * 1024;
+        load_to_lds4(my_scale + (long)b * a.as_k, scales0 + stage * 256);
+        if (b * 128 + 128 <= a.K) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint8_t* p = base[i] + (long)b * 128;
-            if (!whole) p = b * 128 + chunk[i] * 16 < a.K ? p : kZeros;
-            load_to_lds16(p, dst + i * kWaves * 1024);
+            for (int i = 0; i < kLoads; ++i)
+                load_to_lds16((i < kWeightLoads ? w_base : a_base) + (long)b * 128, off[i], dst + i * kWaves * 1024);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint8_t* p = (i < kWeightLoads ? w_base : a_base) + (long)b * 128 + off[i];
+                load_to_lds16(b * 128 + chunk * 16 < a.K ? p : kZeros, dst + i * kWaves * 1024);
+            }
         }
     };
-    const float* sx[TT];
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        const int t = t0 + (wt * TT + j) * 16 + col;
-        sx[j] = a.a_scale + (long)(t < a.M ? t : a.M - 1) * a.as_t;
-    }
-    int nb = (n0 + wn * NT * 16) >> 7;  // a tile past the last row has no scale of its own
-    const int last_nb = (a.N - 1) >> 7;
+    // 64 blocks' weight scales, one per lane
+    const int nb = (n0 + wn * NT * 16) >> 7, last_nb = (a.N - 1) >> 7;  // a tile past the last row has no scale of its own
     const float* sw = a.w_scale + (long)(nb < last_nb ? nb : last_nb) * a.ws_n;
+    float sb = 0.0f;
 
-    float sc[TT], sb = as_global<float>(sw)[0];
-#pragma unroll
-    for (int j = 0; j < TT; ++j) sc[j] = as_global<float>(sx[j])[0];
-    issue(0);
     f32x4 acc[NT][TT] = {};
+#pragma unroll
+    for (int b = 0; b < kRing - 1; ++b)
+        if (b < blocks) issue(b, b);
+    int stage = 0;
     for (int b = 0; b < blocks; ++b) {
-        wait_vmem<0>();
-        float s[TT];
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            s[j] = sc[j] * sb;
-            asm volatile("" : "+v"(s[j]));  // the scales have landed: no later wait covers the loads below
+        if ((b & 63) == 0) {
+            sb = as_global<float>(sw)[b + lane < blocks ? b + lane : blocks - 1];
+            asm volatile("" : "+v"(sb));  // waited for here, not between the loads below
         }
-        lds_barrier();  // block b is in LDS, and every wave is done with the other buffer
-        if (b + 1 < blocks) {
-            sb = as_global<float>(sw)[b + 1];
-#pragma unroll
-            for (int j = 0; j < TT; ++j) sc[j] = as_global<float>(sx[j])[(long)(b + 1) * a.as_k];
-            issue(b + 1);
-        }
-        const uint8_t* buf = lds[b & 1];
+        if (b + kRing - 2 < blocks)  // the blocks after b are on their way
+            wait_vmem<(kRing - 2) * (kLoads + 1)>();
+        else
+            wait_vmem<0>();
+        lds_barrier();  // block b is in LDS, and every wave is done with block b - 1
+        if (b + kRing - 1 < blocks) issue(b + kRing - 1, stage == 0 ? kRing - 1 : stage - 1);
+        const uint8_t* buf = lds[stage];
         auto operand = [&](int row0) {
-            const int r = row0 + col, sw0 = (r >> 1) & 7;
-            const u32x4 lo = *reinterpret_cast<const u32x4*>(buf + r * 128 + ((quad ^ sw0) * 16));
-            const u32x4 hi = *reinterpret_cast<const u32x4*>(buf + r * 128 + (((quad + 4) ^ sw0) * 16));
+            const int r = row0 + col, mix = (r >> 1) & 7;
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(buf + r * 128 + ((quad ^ mix) * 16));
+            const u32x4 hi = *reinterpret_cast<const u32x4*>(buf + r * 128 + (((quad + 4) ^ mix) * 16));
             return join(lo, hi);
         };
+        float s[TT];
         i32x8 xf[TT];
+        const float w_scale = readlane_f(sb, b & 63);
 #pragma unroll
-        for (int j = 0; j < TT; ++j) xf[j] = operand(BN + (wt * TT + j) * 16);
+        for (int j = 0; j < TT; ++j) {
+            xf[j] = operand(BN + (wt * TT + j) * 16);
+            s[j] = scales[wave][stage][j * 16 + col] * w_scale;
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const i32x8 wf = operand((wn * NT + i) * 16);
@@ -246,29 +250,45 @@ __global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(s[j], p[e], acc[i][j][e]);
             }
         }
+        stage = stage == kRing - 1 ? 0 : stage + 1;
     }
+    // Out through LDS, one wave's tile at a time in its own corner of the
+    // buffers: [token][n] rows, so that a store covers whole rows of the tile
+    // (the instruction's layout would store 32 bytes of each of 16 rows).
+    lds_barrier();  // every wave is done with the last block
+    constexpr int kRow = NT * 16 + 4;  // floats; the pad spreads the tokens over the banks
+    static_assert(kWaves * 16 * kRow * 4 <= kRing * kRows * 128, "the corner fits");
+    float* corner = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
+    constexpr int kPieces = NT * 2, kPer = 64 / kPieces;  // 8-column pieces of a row, tokens per turn
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-        const int t = t0 + (wt * TT + j) * 16 + col;
-        if (t >= a.M) continue;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int n = n0 + (wn * NT + i) * 16 + quad * 4;
-            const f32x4 v = acc[i][j];
+        for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(&corner[col * kRow + i * 16 + quad * 4]) = acc[i][j];
+        const int n = n0 + wn * NT * 16 + lane % kPieces * 8;
+#pragma unroll
+        for (int r = 0; r < 16; r += kPer) {
+            const int row = r + lane / kPieces, t = t0 + (wt * TT + j) * 16 + row;
+            const float* p = &corner[row * kRow + lane % kPieces * 8];
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+            if (t >= a.M || n >= a.N) continue;
             if (a.out_f32) {
                 float* o = static_cast<float*>(a.out) + (long)t * a.ldo + n;
-                if (n + 3 < a.N && a.out_vec)
-                    *reinterpret_cast<f32x4*>(o) = v;
-                else
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < a.N) o[e] = v[e];
+                if (n + 7 < a.N && a.out_vec) {
+                    reinterpret_cast<f32x4*>(o)[0] = lo;
+                    reinterpret_cast<f32x4*>(o)[1] = hi;
+                } else {
+                    for (int e = 0; e < 8; ++e)
+                        if (n + e < a.N) o[e] = e < 4 ? lo[e] : hi[e - 4];
+                }
             } else {
                 uint16_t* o = static_cast<uint16_t*>(a.out) + (long)t * a.ldo + n;
-                if (n + 3 < a.N && a.out_vec)
-                    *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                else
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < a.N) o[e] = round_bf16(v[e]);
+                if (n + 7 < a.N && a.out_vec) {
+                    *reinterpret_cast<u32x4*>(o) = u32x4{pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]),
+                                                         pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
+                } else {
+                    for (int e = 0; e < 8; ++e)
+                        if (n + e < a.N) o[e] = round_bf16(e < 4 ? lo[e] : hi[e - 4]);
+                }
             }
         }
     }
@@ -280,11 +300,11 @@ void launch_rows(const Fp8Args& a, hipStream_t s) {
     hipLaunchKernelGGL((fp8_rows_kernel<NT, TT>), grid, dim3(512), 0, s, a);
 }
 
-template <int WN, int WT, int NT, int TT>
+template <int WN, int WT, int NT, int TT, int RING>
 void launch_tiles(const Fp8Args& a, hipStream_t s) {
     constexpr int BN = WN * NT * 16, BT = WT * TT * 16;
     const int total = ((a.N + BN - 1) / BN) * ((a.M + BT - 1) / BT);
-    hipLaunchKernelGGL((fp8_tiles_kernel<WN, WT, NT, TT>), dim3(total), dim3(WN * WT * 64), 0, s, a);
+    hipLaunchKernelGGL((fp8_tiles_kernel<WN, WT, NT, TT, RING>), dim3(total), dim3(WN * WT * 64), 0, s, a);
 }
 
 }  // namespace
@@ -297,7 +317,7 @@ hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t s) {
     else if (a.M <= 64)
         launch_rows<1, 4>(a, s);
     else
-        launch_tiles<2, 2, 4, 4>(a, s);
+        launch_tiles<2, 4, 4, 4, 2>(a, s);
     return hipGetLastError();
 }
 
