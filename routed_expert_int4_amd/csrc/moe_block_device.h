@@ -73,6 +73,9 @@ __device__ __forceinline__ void load_to_lds16(const void* src, unsigned dst) {
 }
 // The same from a wave-uniform base plus a byte offset per lane.
 __device__ __forceinline__ void load_to_lds16(const void* base, unsigned offset, unsigned dst) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)p), hi = __builtin_amdgcn_readfirstlane((unsigned)(p >> 32));
+    base = reinterpret_cast<const void*>((uint64_t)hi << 32 | lo);
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base),
                  "s"(__builtin_amdgcn_readfirstlane(dst))
                  : "memory");

@@ -152,14 +152,20 @@ __global__ void __launch_bounds__(512) fp8_rows_kernel(Fp8Args a) {
 // only vector memory operations are counted ones).  A row of a buffer is 128
 // bytes; its 16-byte chunk c sits at place c ^ ((row / 2) & 7), so that the 16
 // rows of an operand read cover all banks.
-template <int WN, int WT, int NT, int TT, int kRing>
-__global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
+//
+// With KS > 1 as many groups of WN x WT waves take the blocks in turn, each
+// with a ring of its own, and their sums are joined in group order: tiles too
+// few to fill the chip are bound by the latency of one block after another.
+template <int WN, int WT, int NT, int TT, int kRing, int KS>
+__global__ void __launch_bounds__(WN* WT* KS * 64) fp8_tiles_kernel(Fp8Args a) {
     constexpr int kWaves = WN * WT, BN = WN * NT * 16, BT = WT * TT * 16, kRows = BN + BT;
     constexpr int kLoads = kRows / 8 / kWaves;  // asynchronous loads per wave and block, and one of scales
     static_assert(kWaves % 2 == 0 && kRows % (8 * kWaves) == 0 && 128 % (NT * 16) == 0 && BN % (8 * kWaves) == 0 && TT * 16 <= 64, "tile shape");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing][kRows * 128];
-    __shared__ float scales[kWaves][kRing][64];
-    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = wave_in_block();
+    __shared__ __attribute__((aligned(1024))) uint8_t rings[KS][kRing][kRows * 128];
+    __shared__ float scales[KS * kWaves][kRing][64];
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    const int group = wave_in_block() / kWaves, wave = wave_in_block() % kWaves;  // its place in the group
+    uint8_t(*lds)[kRows * 128] = rings[group];
     const int wn = wave % WN, wt = wave / WN;
     // Workgroups are dealt to the eight dies in turn: each die gets a
     // contiguous run of the tile order, in which bands of eight weight tiles
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
     const int blocks = (a.K + 127) >> 7, wave_t = t0 + wt * TT * 16;
     const int my_t = wave_t + lane % (TT * 16);
     const float* my_scale = a.a_scale + (long)(my_t < a.M ? my_t : a.M - 1) * a.as_t;
-    const unsigned lds0 = lds_address(&lds[0][0]), scales0 = lds_address(&scales[wave][0][0]);
+    const unsigned lds0 = lds_address(&lds[0][0]), scales0 = lds_address(&scales[wave_in_block()][0][0]);
     auto issue = [&](int b, int stage) {
         const unsigned dst = lds0 + stage * kRows * 128 + wave * 1024;
         load_to_lds4(my_scale + (long)b * a.as_k, scales0 + stage * 256);
@@ -211,20 +217,22 @@ __global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
 
     f32x4 acc[NT][TT] = {};
 #pragma unroll
-    for (int b = 0; b < kRing - 1; ++b)
-        if (b < blocks) issue(b, b);
+    for (int i = 0; i < kRing - 1; ++i)
+        if (i * KS + group < blocks) issue(i * KS + group, i);
     int stage = 0;
-    for (int b = 0; b < blocks; ++b) {
-        if ((b & 63) == 0) {
-            sb = as_global<float>(sw)[b + lane < blocks ? b + lane : blocks - 1];
+    for (int b0 = 0; b0 < blocks; b0 += KS) {
+        const int b = b0 + group;
+        if ((b0 & 63) == 0) {
+            sb = as_global<float>(sw)[b0 + lane < blocks ? b0 + lane : blocks - 1];
             asm volatile("" : "+v"(sb));  // waited for here, not between the loads below
         }
-        if (b + kRing - 2 < blocks)  // the blocks after b are on their way
+        if (b + (kRing - 2) * KS < blocks)  // the blocks after b are on their way
             wait_vmem<(kRing - 2) * (kLoads + 1)>();
         else
             wait_vmem<0>();
-        lds_barrier();  // block b is in LDS, and every wave is done with block b - 1
-        if (b + kRing - 1 < blocks) issue(b + kRing - 1, stage == 0 ? kRing - 1 : stage - 1);
+        lds_barrier();  // block b is in LDS, and every wave is done with the one before
+        if (b + (kRing - 1) * KS < blocks) issue(b + (kRing - 1) * KS, stage == 0 ? kRing - 1 : stage - 1);
+        if (KS > 1 && b >= blocks) break;  // only in the last turn, which ends the loop for all
         const uint8_t* buf = lds[stage];
         auto operand = [&](int row0) {
             const int r = row0 + col, mix = (r >> 1) & 7;
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
             xf[j] = operand(BN + (wt * TT + j) * 16);
-            s[j] = scales[wave][stage][j * 16 + col] * w_scale;
+            s[j] = scales[wave_in_block()][stage][j * 16 + col] * w_scale;
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -256,6 +264,27 @@ __global__ void __launch_bounds__(WN* WT * 64) fp8_tiles_kernel(Fp8Args a) {
     // buffers: [token][n] rows, so that a store covers whole rows of the tile
     // (the instruction's layout would store 32 bytes of each of 16 rows).
     lds_barrier();  // every wave is done with the last block
+    if constexpr (KS > 1) {
+        static_assert((KS - 1) * BN * BT * 4 <= KS * kRing * kRows * 128, "the sums fit");
+        f32x4* sums = reinterpret_cast<f32x4*>(&rings[0][0][0]);
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < TT; ++j) sums[(((group - 1) * kWaves + wave) * NT * TT + i * TT + j) * 64 + lane] = acc[i][j];
+        }
+        lds_barrier();
+        if (group == 0) {
+#pragma unroll
+            for (int g = 0; g < KS - 1; ++g)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < TT; ++j) acc[i][j] += sums[((g * kWaves + wave) * NT * TT + i * TT + j) * 64 + lane];
+        }
+        lds_barrier();
+        if (group > 0) return;
+    }
     constexpr int kRow = NT * 16 + 4;  // floats; the pad spreads the tokens over the banks
     static_assert(kWaves * 16 * kRow * 4 <= kRing * kRows * 128, "the corner fits");
     float* corner = reinterpret_cast<float*>(lds) + wave * 16 * kRow;
@@ -300,24 +329,60 @@ void launch_rows(const Fp8Args& a, hipStream_t s) {
     hipLaunchKernelGGL((fp8_rows_kernel<NT, TT>), grid, dim3(512), 0, s, a);
 }
 
-template <int WN, int WT, int NT, int TT, int RING>
+template <int WN, int WT, int NT, int TT, int RING, int KS>
 void launch_tiles(const Fp8Args& a, hipStream_t s) {
     constexpr int BN = WN * NT * 16, BT = WT * TT * 16;
     const int total = ((a.N + BN - 1) / BN) * ((a.M + BT - 1) / BT);
-    hipLaunchKernelGGL((fp8_tiles_kernel<WN, WT, NT, TT, RING>), dim3(total), dim3(WN * WT * 64), 0, s, a);
+    hipLaunchKernelGGL((fp8_tiles_kernel<WN, WT, NT, TT, RING, KS>), dim3(total), dim3(WN * WT * KS * 64), 0, s, a);
+}
+
+// Tile shapes of the many-token kernel: what a round of tiles over the chip's
+// 256 CUs costs per block of 128 columns, in tenths of a microsecond, measured
+// at 6144 or 8192 inner columns (one workgroup per CU; two for the second).
+// 512 x 6144 x 8192, say, took 39 us in 128 x 128 tiles (one round), 49 in
+// 64 x 64, 64 in 128 x 256; 4096 x 6144 x 8192 took 205 in 128 x 256 (three
+// rounds), 240 in 128 x 128 and 235 in 256 x 256 (one and a half);
+// 4096 x 16384 x 512 took 56 and 52 us in the last two shapes.
+struct TileShape {
+    int bn, bt, slots, cost;
+};
+constexpr TileShape kTileShapes[] = {{64, 64, 256, 30}, {64, 64, 512, 42}, {128, 128, 256, 60}, {128, 256, 256, 100},
+                                     {256, 256, 256, 175}};
+int best_shape(int M, int N) {
+    int best = 0;
+    long least = 0;
+    for (int i = 0; i < 5; ++i) {
+        const TileShape& t = kTileShapes[i];
+        const long tiles = (long)((N + t.bn - 1) / t.bn) * ((M + t.bt - 1) / t.bt);
+        const long cost = (tiles + t.slots - 1) / t.slots * t.cost;
+        if (i == 0 || cost < least) best = i, least = cost;
+    }
+    return best;
 }
 
 }  // namespace
 
 hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t s) {
-    if (a.K <= kShort)
+    if (a.K <= kShort) {
         hipLaunchKernelGGL(fp8_short_kernel, dim3((a.N + 63) / 64, (a.M + 3) / 4), dim3(256), 0, s, a);
-    else if (a.M <= 16)
-        launch_rows<1, 1>(a, s);
-    else if (a.M <= 64)
-        launch_rows<1, 4>(a, s);
-    else
-        launch_tiles<2, 4, 4, 4, 2>(a, s);
+    } else if (a.M <= 64 && (a.M <= 8 || a.N <= 2048)) {
+        // Few tokens go straight to registers while the weights are what is
+        // read (1 x 6144 x 8192: 13.9 us, 20.1 in tiles; 32 x 2048 x 6144:
+        // 12.8 and 15.4).  With more tokens and rows each workgroup reads the
+        // activations again, and tiles win (32 x 6144 x 8192: 29.4 and 19.9).
+        if (a.M <= 16)
+            launch_rows<1, 1>(a, s);
+        else
+            launch_rows<1, 2>(a, s);
+    } else {
+        switch (best_shape(a.M, a.N)) {
+            case 0: launch_tiles<2, 2, 2, 2, 3, 2>(a, s); break;
+            case 1: launch_tiles<2, 2, 2, 2, 2, 2>(a, s); break;
+            case 2: launch_tiles<2, 2, 4, 4, 2, 2>(a, s); break;
+            case 3: launch_tiles<2, 4, 4, 4, 2, 1>(a, s); break;
+            default: launch_tiles<2, 4, 8, 4, 2, 1>(a, s); break;
+        }
+    }
     return hipGetLastError();
 }
 
