@@ -13,6 +13,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kFp8Max = 448.0f;  // largest E4M3 value
@@ -148,6 +149,24 @@ __device__ __forceinline__ float half_sum(float v) {
     return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
 }
 
+// Exponentials of eight scores as the product with the values takes them, and
+// their sum added to l (of the rounded ones, two at a time, so that numerator
+// and denominator agree).
+__device__ __forceinline__ bf16x8 exponentials(const float* s, float c, float mc, float& l) {
+    bf16x8 p;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc)), f = __builtin_amdgcn_exp2f(fmaf(s[i + 1], c, -mc));
+        const unsigned pair = pack_bf16(e, f);
+        const unsigned one = 0x3F803F80u;
+        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(i16x2, pair), __builtin_bit_cast(i16x2, one), l, false);
+        const bf16x2 v = __builtin_bit_cast(bf16x2, pair);
+        p[i] = v[0];
+        p[i + 1] = v[1];
+    }
+    return p;
+}
+
 // Running statistics start from a finite value, so that a row of masked
 // scores (-inf) gives exponentials of zero and never inf - inf.
 constexpr float kNoMax = -1e30f;
@@ -155,6 +174,8 @@ constexpr float kNoMax = -1e30f;
 // score exceeds it by more than this many powers of two: exponentials stay
 // below 2^8, which costs fp32 sums and bf16 exponentials no relative accuracy.
 constexpr float kMaxSlack = 8.0f;
+// The same bound on a tile's sum of exponentials.
+constexpr float kMaxSum = 65536.0f;
 
 }  // namespace
 }  // namespace moe

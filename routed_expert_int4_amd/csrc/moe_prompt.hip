@@ -35,7 +35,11 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
     const int lane = threadIdx.x & 63, wave = wave_in_block(), half = lane >> 5, col = lane & 31;
     const int h = blockIdx.x, b = blockIdx.z;
     // bounds come from device memory: kept inside the tensors whatever they say
-    auto inside = [](int v, int n) { return v < 0 ? 0 : (v > n ? n : v); };
+    auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    auto inside = [&](int v, int n) {
+        v = uniform(v);
+        return v < 0 ? 0 : (v > n ? n : v);
+    };
     const int q_first = inside(a.cu_q[b], a.Tq), q_count = inside(a.cu_q[b + 1], a.Tq) - q_first;
     const int k_first = inside(a.cu_k[b], a.Tk), k_count_all = inside(a.cu_k[b + 1], a.Tk) - k_first;
     const int k_count = k_count_all > 0 ? k_count_all : 0;
@@ -61,9 +65,9 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
     const int last_q = q0 + 127 < q_count ? q0 + 127 : q_count - 1;
     const int wave_last = q0 + wave * 32 + 31 < q_count ? q0 + wave * 32 + 31 : q_count - 1;
     const int limit = row_ok ? visible(my_q) : 0;
-    const int wave_limit = q0 + wave * 32 < q_count ? visible(wave_last) : 0;
-    const int wave_full = a.causal ? visible(q0 + wave * 32) : k_count;  // keys that all of the wave's rows see
-    const int tiles = (visible(last_q) + KT - 1) / KT;
+    const int wave_limit = uniform(q0 + wave * 32 < q_count ? visible(wave_last) : 0);
+    const int wave_full = uniform(a.causal ? visible(q0 + wave * 32) : k_count);  // keys that all of the wave's rows see
+    const int tiles = uniform((visible(last_q) + KT - 1) / KT);
 
     // Loads of one tile: an instruction covers whole rows, and the place of a
     // lane's chunk is the same in all of a kind.
@@ -98,9 +102,20 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
             issue_part(v_base, a.v_stride_t, key0, vr + i * 4 * kValueRows, v_chunk, dst + kParts * kPartBytes + i * 4096);
     };
 
+    // This lane's places in a tile: keys (row reads of 16 bytes) and values
+    // (transposed reads of four keys); an exclusive or with the low part of a
+    // chunk and an immediate offset reach every operand.
+    const unsigned key_at = lds0 + col * 128 + key_place(half, col) * 16;
+    const int vrow = half * 4 + ((lane & 15) >> 2), vchunk = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+    const unsigned value_at =
+        lds0 + kParts * kPartBytes + vrow * VD * 2 + value_place<VD * 2>(vchunk, vrow) * 16 + (lane & 1) * 8;
     const float c = a.scale * 1.44269504088896340736f;
     float m = kNoMax, l = 0.0f;
     f32x16 o[kOut] = {};
+    // the queries have landed: the compiler must not wait for them inside the
+    // loop, where the next tile is on its way
+#pragma unroll
+    for (int k = 0; k < kParts * 4; ++k) asm volatile("" : "+v"(qf[k]));
     if (tiles > 0) issue(0);
     for (int t = 0; t < tiles; ++t) {
         wait_vmem<0>();
@@ -108,60 +123,88 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
         if (t + 1 < tiles) issue(t + 1);
         const int key0 = t * KT;
         if (key0 >= wave_limit) continue;
-        const unsigned buf = lds0 + (t & 1) * kTileBytes;
+        const unsigned buf = (t & 1) * kTileBytes;
         f32x16 s[kSub] = {};
+        unsigned key_base[4];  // the rest of an address is an immediate offset
 #pragma unroll
-        for (int u = 0; u < kSub; ++u) {
-            const int r = u * 32 + col;
+        for (int k = 0; k < 4; ++k) key_base[k] = (key_at + buf) ^ k * 32;
+        // operands are read kAhead instructions before their use (the
+        // scheduling barriers keep that order); tiles of 32 keys alternate
+        constexpr int kAhead = 4;
+        bf16x8 x[kAhead];
+        auto key_chunk = [&](int i) {
+            const int k = i / kSub, u = i % kSub;
+            return lds_chunk(key_base[k % 4] + (k / 4) * kPartBytes + u * 32 * 128);
+        };
 #pragma unroll
-            for (int k = 0; k < kParts * 4; ++k)
-                s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    lds_chunk(buf + (k / 4) * kPartBytes + r * 128 + key_place((k % 4) * 2 + half, r) * 16), qf[k], s[u],
-                    0, 0, 0);
+        for (int i = 0; i < kAhead; ++i) x[i] = key_chunk(i);
+#pragma unroll
+        for (int i = 0; i < kParts * 4 * kSub; ++i) {
+            s[i % kSub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i % kAhead], qf[i / kSub], s[i % kSub], 0, 0, 0);
+            if (i + kAhead < kParts * 4 * kSub) x[i % kAhead] = key_chunk(i + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        unsigned value_base[4];
+#pragma unroll
+        for (int k = 0; k < (kOut < 4 ? kOut : 4); ++k) value_base[k] = (value_at + buf) ^ k * 64;
+        auto value_chunk = [&](int i) {
+            const int k = i / (kSub * 2), u = i % (kSub * 2);
+            const unsigned lo = value_base[k % 4] + (k / 4) * 256 + u * 16 * VD * 2;
+            return values_transposed(lo, lo + 8 * VD * 2);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) x[i] = value_chunk(i);
         if (key0 + KT > wave_full) {
+            int left = limit - key0 - 4 * half;  // keys of this tile that this lane's query sees
+            asm volatile("" : "+v"(left));       // keeps the comparisons in this branch
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (key0 + u * 32 + 8 * (i / 4) + 4 * half + i % 4 >= limit) s[u][i] = -__builtin_inff();
+                    if (u * 32 + 8 * (i / 4) + i % 4 >= left) s[u][i] = -__builtin_inff();
         }
-        float top = s[0][0];
+        // Exponentials against the running maximum as it is.  It only has to
+        // move when they grow large: their sum says so (and, at the first
+        // tile, infinitely so), without a maximum over every tile.
+        bf16x8 p[kSub * 2];
+        auto all_exponentials = [&]() {
+            float sum = 0.0f;
+            const float mc = m * c;
 #pragma unroll
-        for (int u = 0; u < kSub; ++u)
+            for (int u = 0; u < kSub; ++u) {
+                float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-        top = half_max(top);
-        if (__any((top - m) * c > kMaxSlack)) {
-            const float nm = fmaxf(m, top), f = __builtin_amdgcn_exp2f((m - nm) * c);
+                for (int i = 0; i < 16; ++i) v[i] = s[u][i];
+                p[u * 2] = exponentials(v, c, mc, sum);
+                p[u * 2 + 1] = exponentials(v + 8, c, mc, sum);
+            }
+            return sum;
+        };
+        float sum = all_exponentials();
+        if (__any(sum > kMaxSum)) {
+            float top = s[0][0];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+            const float nm = fmaxf(m, half_max(top)), f = __builtin_amdgcn_exp2f((m - nm) * c);
             m = nm;
             l *= f;
 #pragma unroll
             for (int k = 0; k < kOut; ++k)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[k][i] *= f;
+            sum = all_exponentials();
         }
-        const float mc = m * c;
-        bf16x8 p[kSub * 2];
+        l += sum;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < kSub; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[u][i], c, -mc));
-                l += e;
-                p[u * 2 + i / 8][i % 8] = (__bf16)e;
-            }
-        const unsigned values = buf + kParts * kPartBytes;
-        const int vrow = half * 4 + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-#pragma unroll
-        for (int k = 0; k < kOut; ++k)
-#pragma unroll
-            for (int u = 0; u < kSub * 2; ++u) {
-                const int r = u * 16 + vrow, ch = (k * 32 + vcol) / 8, sub = (vcol & 4) * 2;
-                const unsigned lo = values + r * VD * 2 + value_place<VD * 2>(ch, r) * 16 + sub;
-                const unsigned hi = values + (r + 8) * VD * 2 + value_place<VD * 2>(ch, r + 8) * 16 + sub;
-                o[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_transposed(lo, hi), p[u], o[k], 0, 0, 0);
-            }
+        for (int i = 0; i < kOut * kSub * 2; ++i) {
+            const int k = i / (kSub * 2), u = i % (kSub * 2);
+            o[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i % kAhead], p[u], o[k], 0, 0, 0);
+            if (i + kAhead < kOut * kSub * 2) x[i % kAhead] = value_chunk(i + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
     if (!row_ok) return;
     l = half_sum(l);
