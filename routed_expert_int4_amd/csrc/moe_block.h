@@ -53,6 +53,7 @@ struct HeadArgs {
     uint16_t* out;
     long x_stride_t, x_stride_h, o_stride_t, o_stride_h;
     int T, heads, K, N;
+    bool out_vec;  // eight neighbouring outputs may be stored at once
 };
 hipError_t launch_head_linear(const HeadArgs& a, hipStream_t s);
 

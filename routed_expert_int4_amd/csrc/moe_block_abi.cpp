@@ -100,6 +100,7 @@ moe_status_t moe_head_linear(const uint16_t* d_x, int64_t x_stride_t, int64_t x_
     a.x = d_x, a.w = d_w, a.out = d_out;
     a.x_stride_t = x_stride_t, a.x_stride_h = x_stride_h, a.o_stride_t = out_stride_t, a.o_stride_h = out_stride_h;
     a.T = T, a.heads = heads, a.K = K, a.N = N;
+    a.out_vec = N % 8 == 0 && out_stride_t % 8 == 0 && out_stride_h % 8 == 0 && on(d_out, 16);
     return launched(launch_head_linear(a, static_cast<hipStream_t>(stream)), who);
 }
 

@@ -87,100 +87,135 @@ __global__ void __launch_bounds__(256) head_linear_kernel(HeadArgs a) {
     }
 }
 
-// Many tokens: a workgroup owns 64 tokens of one head and all n.  Their rows
-// (KC inner columns at a time) are loaded asynchronously into LDS, all at
-// once, so that a CU has 128 KB in flight (64-token rows lie heads * K apart
-// in memory; through registers the same loads would be bound by latency at
-// two waves per SIMD).  Weights come from the L2, which all token tiles of a
-// head share.  The 16-byte chunk c of row r sits at place c ^ (r & 15): the
-// 16 rows of an operand read cover all banks.
-template <int KC>
-__global__ void __launch_bounds__(256, 2) head_linear_tile_kernel(HeadArgs a) {
-    constexpr int NT = 2, TT = 4, kSteps = KC / 32, kChunks = KC / 8;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[64 * KC * 2];
+// Many tokens: a wave keeps the weights of its NW x 16 rows and KC inner
+// columns in registers and a workgroup of four passes over tiles
+// of 64 tokens of one head, loaded asynchronously one ahead into the other of
+// two LDS buffers: token rows lie heads * K apart in memory, and 64 KB in
+// flight per CU are what reading them takes (1024 tokens x 64 heads, 512 to
+// 128: through registers 50 us, 64 tokens per workgroup with the weights read
+// again for each 38 us).  The 16-byte chunk c of row r sits at place
+// c ^ (r & 15): the 16 rows of an operand read cover all banks.  Row m of
+// instruction tile i is n = m / 4 * 4 NW + 4 i + m % 4, so that a lane holds
+// 4 NW neighbouring outputs of one token.
+template <int KC, int NW, int PER_CU>
+__global__ void __launch_bounds__(256, PER_CU) head_linear_tile_kernel(HeadArgs a) {
+    constexpr int TT = 4, kSteps = KC / 32, kChunks = KC / 8, kTileBytes = 64 * KC * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTileBytes];
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = wave_in_block();
-    // all token tiles of a head on one die (they are dealt in turn)
-    const int h = blockIdx.x, t0 = blockIdx.y * 64;
+    // a head's workgroups lie on one die (they are dealt in turn)
+    const int h = blockIdx.x, n0 = (blockIdx.y * 4 + wave) * NW * 16;
+    const int tiles = (a.T + 63) / 64, turns = (a.K + KC - 1) / KC;
     const uint16_t* x = a.x + h * a.x_stride_h;
     const unsigned lds0 = lds_address(lds);
-    auto issue = [&](int k0) {
+    auto issue = [&](int tile, int turn, int buf) {
 #pragma unroll
-        for (int i = 0; i < KC * 128 / 4096; ++i) {
-            const int at = (i * 4 + wave) * 64 + lane, r = at / kChunks, k = k0 + ((at % kChunks) ^ (r & 15)) * 8;
-            const int t = t0 + r;
+        for (int i = 0; i < kTileBytes / 4096; ++i) {
+            const int at = (i * 4 + wave) * 64 + lane, r = at / kChunks, k = turn * KC + ((at % kChunks) ^ (r & 15)) * 8;
+            const int t = tile * 64 + r;
             const uint16_t* p = x + (long)t * a.x_stride_t + k;
-            load_to_lds16(t < a.T && k < a.K ? static_cast<const void*>(p) : kZeros, lds0 + (i * 4 + wave) * 1024);
+            load_to_lds16(t < a.T && k < a.K ? static_cast<const void*>(p) : kZeros,
+                          lds0 + buf * kTileBytes + (i * 4 + wave) * 1024);
         }
     };
-    issue(0);
-    // every wave takes every turn (the barriers need all four); one whose rows
-    // lie past the end repeats the last row and stores nothing
-    for (int block = 0; block < a.N; block += 4 * NT * 16) {
-        const int n0 = block + wave * NT * 16;
-        const uint16_t* w[NT];
+    const uint16_t* w[NW];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int n = n0 + i * 16 + col;
-            w[i] = a.w + ((long)h * a.N + (n < a.N ? n : a.N - 1)) * a.K;
-        }
-        f32x4 acc[NT][TT] = {};
-        for (int k0 = 0; k0 < a.K; k0 += KC) {
-            bf16x8 wf[NT][kSteps];
+    for (int i = 0; i < NW; ++i) {
+        const int n = n0 + (col >> 2) * 4 * NW + i * 4 + (col & 3);
+        w[i] = a.w + ((long)h * a.N + (n < a.N ? n : a.N - 1)) * a.K;
+    }
+    bf16x8 wf[NW][kSteps];
+    // (complete on return: the compiler must not wait for weights inside the
+    // loop, where the next tile is on its way)
+    auto load_weights = [&](int turn) {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
+        for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) wf[i][s] = row_chunk(w[i], k0 + s * 32 + quad * 8, a.K);
-            if (k0 > 0 || (block > 0 && a.K > KC)) {  // more inner columns than a tile holds
-                lds_barrier();
-                issue(k0);
-            }
-            wait_vmem<0>();
-            lds_barrier();
+            for (int i = 0; i < NW; ++i) wf[i][s] = row_chunk(w[i], turn * KC + s * 32 + quad * 8, a.K);
+        wait_vmem<0>();
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int i = 0; i < NW; ++i) asm volatile("" : "+v"(wf[i][s]));
+    };
+    int tile = blockIdx.z, buf = 0;
+    issue(tile, 0, 0);
+    load_weights(0);
+    lds_barrier();
+    for (; tile < tiles; tile += gridDim.z) {
+        f32x4 acc[NW][TT] = {};
+        for (int turn = 0; turn < turns; ++turn) {
+            // what comes after this part: the next inner columns, or the next tile
+            const bool last = turn + 1 == turns;
+            const int next_tile = last ? tile + (int)gridDim.z : tile, next_turn = last ? 0 : turn + 1;
+            const bool more = next_tile < tiles;
+            if (more) issue(next_tile, next_turn, buf ^ 1);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 bf16x8 xf[TT];
 #pragma unroll
                 for (int j = 0; j < TT; ++j) {
                     const int r = j * 16 + col;
-                    xf[j] = lds_chunk(lds0 + r * KC * 2 + ((s * 4 + quad) ^ (r & 15)) * 16);
+                    xf[j] = lds_chunk(lds0 + buf * kTileBytes + r * KC * 2 + ((s * 4 + quad) ^ (r & 15)) * 16);
                 }
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+                for (int i = 0; i < NW; ++i)
 #pragma unroll
                     for (int j = 0; j < TT; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i][s], xf[j], acc[i][j], 0, 0, 0);
             }
+            if (turns > 1 && more) load_weights(next_turn);  // more inner columns than the registers hold
+            wait_vmem<0>();
+            lds_barrier();  // the next part is in LDS, and every wave is done with this one
+            buf ^= 1;
         }
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
-            const int t = t0 + j * 16 + col;
+            const int t = tile * 64 + j * 16 + col;
             if (t >= a.T) continue;
-            uint16_t* o = a.out + (long)t * a.o_stride_t + h * a.o_stride_h;
+            const int n = n0 + quad * 4 * NW;
+            uint16_t* o = a.out + (long)t * a.o_stride_t + h * a.o_stride_h + n;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int n = n0 + i * 16 + quad * 4;
-                const u32x2 v = {pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
-                if (n < a.N) *reinterpret_cast<u32x2*>(o + n) = v;
+            for (int i = 0; i < NW; i += 2) {
+                const u32x4 v = {pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3]),
+                                 pack_bf16(acc[i + 1][j][0], acc[i + 1][j][1]), pack_bf16(acc[i + 1][j][2], acc[i + 1][j][3])};
+                if (n + i * 4 + 7 < a.N && a.out_vec) {
+                    *reinterpret_cast<u32x4*>(o + i * 4) = v;
+                } else {  // N is a multiple of 4
+                    if (n + i * 4 < a.N) *reinterpret_cast<u32x2*>(o + i * 4) = u32x2{v[0], v[1]};
+                    if (n + i * 4 + 4 < a.N) *reinterpret_cast<u32x2*>(o + i * 4 + 4) = u32x2{v[2], v[3]};
+                }
             }
         }
     }
 }
 
 template <int NT, int TT>
-void launch_tiles(const HeadArgs& a, hipStream_t s) {
+void launch_rows(const HeadArgs& a, hipStream_t s) {
     const dim3 grid((a.N + 64 * NT - 1) / (64 * NT), (a.T + 16 * TT - 1) / (16 * TT), a.heads);
     hipLaunchKernelGGL((head_linear_kernel<NT, TT>), grid, dim3(256), 0, s, a);
+}
+template <int KC, int NW, int PER_CU>
+void launch_tiles(const HeadArgs& a, hipStream_t s) {
+    // workgroups that share a head's token tiles: enough of them to fill the chip
+    const int blocks = (a.N + 64 * NW - 1) / (64 * NW), tiles = (a.T + 63) / 64;
+    int share = (256 * PER_CU + a.heads * blocks - 1) / (a.heads * blocks);
+    share = share < tiles ? share : tiles;
+    hipLaunchKernelGGL((head_linear_tile_kernel<KC, NW, PER_CU>), dim3(a.heads, blocks, share), dim3(256), 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_head_linear(const HeadArgs& a, hipStream_t s) {
+    // Few tokens: what counts is the weights' one reading (32 tokens, 64
+    // heads, 128 to 512: 7.1 us, 8.9 in token tiles; 512 to 128: 8.4 and 8.0).
     if (a.T <= 16)
-        launch_tiles<1, 1>(a, s);
+        launch_rows<1, 1>(a, s);
+    else if (a.K <= 128 && a.T <= 64)
+        launch_rows<1, 2>(a, s);
     else if (a.K <= 128)
-        hipLaunchKernelGGL(head_linear_tile_kernel<128>, dim3(a.heads, (a.T + 63) / 64), dim3(256), 0, s, a);
+        launch_tiles<128, 2, 4>(a, s);
     else
-        hipLaunchKernelGGL(head_linear_tile_kernel<512>, dim3(a.heads, (a.T + 63) / 64), dim3(256), 0, s, a);
+        launch_tiles<512, 2, 1>(a, s);
     return hipGetLastError();
 }
 
