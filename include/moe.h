@@ -441,7 +441,8 @@ enum { MOE_BF16 = 0, MOE_F32 = 1 };
 
 /* moe_add_rmsnorm: h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight,
  * for T rows of H <= 32768 columns.  The statistics use h before rounding.
- * d_residual may be NULL.  d_sum (or NULL) receives h in the residual's type
+ * d_residual may be NULL.  d_weight NULL leaves the norm out (y = h: addition
+ * and conversion alone).  d_sum (or NULL) receives h in the residual's type
  * (x's without one) and may be d_residual itself.  d_y (or NULL) receives y
  * in bf16.  d_q (or NULL) receives y in 8 bits with one scale per 128
  * columns, the largest magnitude / 448 (at least 1e-12; NaN for a group that
@@ -487,8 +488,9 @@ moe_status_t moe_head_linear(const uint16_t* d_x, int64_t x_stride_t, int64_t x_
  * NaN.  Two tokens must not share a slot.  d_cache may be NULL (d_slots
  * then unused).  Further outputs, each optional: d_q_rope [T][heads][rope]
  * rotated into d_q_out (which may be d_q_rope itself); d_lat_q / d_lat_scale:
- * the normed latent in 8 bits as in moe_add_rmsnorm (input of the key/value
- * expansion); d_key [T][rope]: a copy of the rotated position part.
+ * the normed latent in 8 bits as in moe_add_rmsnorm; d_rows [T][rank + rope]:
+ * a copy of the cache rows, one after another (input of a prompt's key and
+ * value expansion).
  * rank <= 2048; rank, rope and all bf16 strides multiples of 8, pointers
  * 16-byte aligned (d_lat_q 8-byte). */
 moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const void* d_weight, int weight_type,
@@ -497,7 +499,7 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
                                int64_t n_slots, const uint16_t* d_q_rope, int heads, int64_t q_stride_t,
                                int64_t q_stride_h, uint16_t* d_q_out, int64_t qo_stride_t, int64_t qo_stride_h,
                                uint8_t* d_lat_q, int64_t lat_stride, float* d_lat_scale, int64_t ls_stride_t,
-                               int64_t ls_stride_g, uint16_t* d_key, int64_t key_stride, void* stream);
+                               int64_t ls_stride_g, uint16_t* d_rows, int64_t rows_stride, void* stream);
 
 /* moe_latent_attention: attention over the paged latent cache, absorbed form.
  * d_q [T][heads][rank + rope] (queries already in the latent space, and their

@@ -2,6 +2,7 @@
 layers of a model with latent attention, as calls on torch tensors.
 
     add_rmsnorm       residual addition and root-mean-square norm, bf16 and / or 8-bit output
+    quantize          8-bit codes and scales alone
     fp8_linear        8-bit product with a scale per 128 columns (activations) and 128 x 128 block (weights)
     head_linear       one product per head (queries into the latent space, outputs back out)
     latent_append     norm, rotation and write of new rows of the latent cache
@@ -41,7 +42,8 @@ class AppendOut(NamedTuple):
     q_rope: torch.Tensor | None  # rotated position part of the queries
     q: torch.Tensor | None       # the normed latent in 8 bits
     scale: torch.Tensor | None
-    key: torch.Tensor | None     # rotated position part of the keys
+    key: torch.Tensor | None     # rotated position part of the keys (a view of rows)
+    rows: torch.Tensor | None    # the cache rows, one after another
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -85,15 +87,19 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, out: str = "bf16", 
                 stream=None) -> NormOut:
     """h = x + residual and its root-mean-square norm times weight.
 
-    x [T, H] bf16 or fp32, weight [H], residual [T, H] or None.  out: "bf16",
+    x [T, H] bf16 or fp32, weight [H] (None: no norm, the addition and the
+    conversion alone), residual [T, H] or None.  out: "bf16",
     "fp8" (codes and one scale per 128 columns) or "both".  h is returned in
     the residual's type (sum_out, which may be the residual itself, receives
     it in place; want_sum=False leaves it out)."""
     shape, strides = _rows(x, "x", 2, _WIDE)
-    wide, _ = _rows(weight, "weight", 1, _WIDE)
     T, H = shape
-    if wide[0] != H:
-        _need(False, f"weight has {wide[0]} values, x {H} columns")
+    weight_p, w_type = None, 0
+    if weight is not None:
+        wide, _ = _rows(weight, "weight", 1, _WIDE)
+        if wide[0] != H:
+            _need(False, f"weight has {wide[0]} values, x {H} columns")
+        weight_p, w_type = weight.data_ptr(), _TYPES[weight.dtype]
     x_type = _TYPES[x.dtype]
     residual_p, r_stride, r_type, sum_type = None, 0, 0, x.dtype
     if residual is not None:
@@ -121,9 +127,27 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, out: str = "bf16", 
         q, scale = _codes(T, H, dev), _scales(T, H, dev)
         q_p, scale_p = q.data_ptr(), scale.data_ptr()
     B.check(B.lib().moe_add_rmsnorm(x.data_ptr(), x_type, strides[0] if T > 1 else H, residual_p, r_type, r_stride,
-                                    weight.data_ptr(), _TYPES[weight.dtype], T, H, eps, sum_p, s_stride, y_p, H, q_p, pad,
+                                    weight_p, w_type, T, H, eps, sum_p, s_stride, y_p, H, q_p, pad,
                                     scale_p, 1, T, _stream(x, stream)))
     return NormOut(sum_out, y, q, scale)
+
+
+def quantize(x, stream=None):
+    """x [T, H] bf16 or fp32 in 8 bits: (codes, scales [T, ceil(H / 128)])."""
+    r = add_rmsnorm(x, None, 0.0, out="fp8", stream=stream)
+    return r.q, r.scale
+
+
+def quantize_weight(w):
+    """A weight [N, K] in 8 bits with one scale per 128 x 128 block, as
+    fp8_linear reads it.  Done once when a model is loaded, in torch."""
+    N, K = w.shape
+    nb, kb = -(-N // GROUP), -(-K // GROUP)
+    wide = torch.nn.functional.pad(w.float(), (0, kb * GROUP - K, 0, nb * GROUP - N))
+    blocks = wide.view(nb, GROUP, kb, GROUP)
+    scale = (blocks.abs().amax((1, 3)) / 448.0).clamp_min(1e-12)
+    codes = (blocks / scale[:, None, :, None]).clamp(-448.0, 448.0).view(nb * GROUP, kb * GROUP)[:N, :K]
+    return codes.to(_FP8).contiguous(), scale.contiguous()
 
 
 def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -> torch.Tensor:
@@ -212,18 +236,18 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
             qo_shape, qo = _rows(q_out, "q_out", 3, _BF16_ONLY)
             _need(qo_shape == q_shape, f"q_out {tuple(qo_shape)}, q_rope {tuple(q_shape)}")
         qp, qop = q_rope.data_ptr(), q_out.data_ptr()
-    q = scale = key = q_p = scale_p = key_p = None
+    q = scale = rows = q_p = scale_p = rows_p = None
     if want_fp8:
         q, scale = _codes(T, rank, kv.device), _scales(T, rank, kv.device)
         q_p, scale_p = q.data_ptr(), scale.data_ptr()
     if want_key:
-        key = torch.empty((T, rope), dtype=_BF16, device=kv.device)
-        key_p = key.data_ptr()
+        rows = torch.empty((T, width), dtype=_BF16, device=kv.device)
+        rows_p = rows.data_ptr()
     B.check(B.lib().moe_latent_append(
         kv.data_ptr(), kvs[0] if T > 1 else width, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
         table.data_ptr(), n_positions, positions.data_ptr(), slots_p, T, cache_p, n_slots, qp, heads, qs[0], qs[1],
-        qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, key_p, rope, _stream(kv, stream)))
-    return AppendOut(q_out if q_rope is not None else None, q, scale, key)
+        qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, rows_p, width, _stream(kv, stream)))
+    return AppendOut(q_out if q_rope is not None else None, q, scale, rows[:, rank:] if want_key else None, rows)
 
 
 def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = None, cu_q=None,

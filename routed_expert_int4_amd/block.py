@@ -1,0 +1,216 @@
+"""One decoder block: latent attention and the routed MoE layer.
+
+    python -m routed_expert_int4_amd.block            # a prompt, then decoded tokens, timed
+
+Per token (colibri summary, "Principales fonctionnalites": q/kv-LoRA, partial
+interleaved rotary positions, one latent vector per token in the cache):
+
+    h      = residual + delta;  x = norm(h)                          add_rmsnorm, 8-bit out
+    q      = W_qb norm(W_qa x);  c | k_r = W_kva x                   fp8_linear, add_rmsnorm
+    cache <- norm(c) | rotate(k_r);  q_r = rotate(q_r)               latent_append
+    prompt:  k = W_uk c, v = W_uv c per head, attention over them    head_linear, prompt_attention
+    decode:  q_c = q W_uk per head, attention over the cache,        head_linear, latent_attention,
+             o = W_uv o_c per head                                   head_linear
+    delta  = W_o o                                                   quantize, fp8_linear
+    h      = h + delta;  delta = MoE(norm(h))                        add_rmsnorm, DeviceLayer.forward
+
+The latents stay in bf16 in both forms (rounding them to 8 bits for the
+prompt's expansion would give a prompt other keys and values than the tokens
+decoded after it), so the expansions W_uk and W_uv are bf16 and per head.
+
+The block holds its weights (8-bit projections, bf16 expansions), the cache pages of its sequences and nothing else; the residual
+stream and the MoE output go from block to block.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import attention as A
+
+
+@dataclass(frozen=True)
+class BlockConfig:
+    hidden: int = 6144
+    heads: int = 64
+    q_rank: int = 2048
+    rank: int = 512
+    rope: int = 64
+    nope: int = 128
+    vdim: int = 128
+    page: int = 64
+    eps: float = 1e-6
+
+    @property
+    def scale(self) -> float:
+        return (self.nope + self.rope) ** -0.5
+
+
+def rope_table(n: int, rope: int, base: float = 10000.0, device: str = "cuda:0"):
+    """Cosines, then sines, of position * base^(-2 i / rope), from 64 bits."""
+    angle = torch.arange(n, dtype=torch.float64)[:, None] * base ** (-torch.arange(0, rope, 2, dtype=torch.float64) / rope)
+    return torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
+
+
+def random_weights(cfg: BlockConfig, seed: int, device: str = "cuda:0") -> dict:
+    """bf16 weights of the block's shapes (there are no checkpoints here)."""
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+
+    def normal(n, k):
+        return (torch.randn(n, k, generator=g, device=device) * k ** -0.5).bfloat16()
+
+    def gain(n):
+        return (1.0 + 0.1 * torch.randn(n, generator=g, device=device)).bfloat16()
+
+    head = cfg.nope + cfg.rope
+    return {"norm_in": gain(cfg.hidden), "norm_q": gain(cfg.q_rank), "norm_kv": gain(cfg.rank), "norm_moe": gain(cfg.hidden),
+            "q_a": normal(cfg.q_rank, cfg.hidden), "q_b": normal(cfg.heads * head, cfg.q_rank),
+            "kv_a": normal(cfg.rank + cfg.rope, cfg.hidden), "kv_b": normal(cfg.heads * (cfg.nope + cfg.vdim), cfg.rank),
+            "o": normal(cfg.hidden, cfg.heads * cfg.vdim)}
+
+
+class LatentCache:
+    """Pages of one block's latent cache and the page lists of its sequences."""
+
+    def __init__(self, cfg: BlockConfig, n_pages: int, max_seqs: int, max_len: int, device: str = "cuda:0"):
+        self.cfg, self.max_len = cfg, max_len
+        self.pool = torch.zeros(n_pages, cfg.page, cfg.rank + cfg.rope, dtype=torch.bfloat16, device=device)
+        self.pages = torch.full((max_seqs, -(-max_len // cfg.page)), -1, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=device)
+        self.host_lens = [0] * max_seqs
+        self._lists = [[] for _ in range(max_seqs)]
+        self._free = list(range(n_pages))[::-1]
+
+    def extend(self, counts):
+        """Makes room for counts[b] new rows of sequence b.  Returns their
+        positions (int32) and cache rows (int64), sequence after sequence."""
+        cfg, positions, slots = self.cfg, [], []
+        for b, n in enumerate(counts):
+            have = self.host_lens[b]
+            if have + n > self.max_len:
+                raise ValueError(f"sequence {b}: {have + n} rows, the cache holds {self.max_len} per sequence")
+            while len(self._lists[b]) * cfg.page < have + n:
+                if not self._free:
+                    raise ValueError("the latent cache has no free page")
+                self._lists[b].append(self._free.pop())
+            positions += range(have, have + n)
+            slots += [self._lists[b][p // cfg.page] * cfg.page + p % cfg.page for p in range(have, have + n)]
+            self.host_lens[b] = have + n
+        dev = self.pool.device
+        for b, pages in enumerate(self._lists):
+            if pages:
+                self.pages[b, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
+        self.lens.copy_(torch.tensor(self.host_lens, dtype=torch.int32))
+        return (torch.tensor(positions, dtype=torch.int32).to(dev), torch.tensor(slots, dtype=torch.int64).to(dev))
+
+
+class DecoderBlock:
+    """The attention half around a DeviceLayer (or None: attention only)."""
+
+    def __init__(self, cfg: BlockConfig, weights: dict, moe=None, max_positions: int = 4096, device: str = "cuda:0"):
+        self.cfg, self.moe = cfg, moe
+        self.norms = {k: weights[k] for k in ("norm_in", "norm_q", "norm_kv", "norm_moe")}
+        self.lin = {k: A.quantize_weight(weights[k]) for k in ("q_a", "q_b", "kv_a", "o")}
+        # the per-head expansions, for the absorbed form with the keys'
+        # transposed (queries go the other way)
+        code, s = A.quantize_weight(weights["kv_b"])
+        self.lin["kv_b"] = code, s
+        kb = s.repeat_interleave(128, 0)[:code.shape[0]].repeat_interleave(128, 1)[:, :code.shape[1]]
+        full = (code.float() * kb).view(cfg.heads, cfg.nope + cfg.vdim, cfg.rank)
+        self.w_uk = full[:, :cfg.nope].contiguous().bfloat16()
+        self.w_uk_t = self.w_uk.transpose(1, 2).contiguous()
+        self.w_uv = full[:, cfg.nope:].contiguous().bfloat16()
+        self.table = rope_table(max_positions, cfg.rope, device=device)
+
+    def _linear(self, x, name):
+        return A.fp8_linear(x[0], x[1], *self.lin[name])
+
+    def _queries(self, delta, residual):
+        cfg = self.cfg
+        n = A.add_rmsnorm(delta, self.norms["norm_in"], cfg.eps, residual=residual, out="fp8")
+        x = (n.q, n.scale)
+        qa = A.add_rmsnorm(self._linear(x, "q_a"), self.norms["norm_q"], cfg.eps, out="fp8")
+        q = self._linear((qa.q, qa.scale), "q_b").view(-1, cfg.heads, cfg.nope + cfg.rope)
+        return n.sum, q, self._linear(x, "kv_a")
+
+    def _finish(self, o, h):
+        """Output projection, second norm and the MoE layer: the residual and
+        the next delta."""
+        delta = self._linear(A.quantize(o.reshape(o.shape[0], -1)), "o")
+        if self.moe is None:
+            return h, delta
+        n = A.add_rmsnorm(delta, self.norms["norm_moe"], self.cfg.eps, residual=h, out="bf16", sum_out=h)
+        return h, self.moe.forward(n.y)[0]
+
+    def prompt(self, delta, residual, cache: LatentCache, counts):
+        """Prompts of counts[b] tokens, one after another in delta and
+        residual [T, hidden], for sequences that have no rows yet."""
+        cfg = self.cfg
+        if any(n and cache.host_lens[b] for b, n in enumerate(counts)):
+            raise ValueError("prompt() starts sequences; decode() continues them")
+        positions, slots = cache.extend(counts)
+        h, q, kv = self._queries(delta, residual)
+        new = A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, positions, slots, cache.pool,
+                              q_rope=q[..., cfg.nope:], q_out=q[..., cfg.nope:], want_key=True)
+        latents = new.rows[:, None, :cfg.rank].expand(-1, cfg.heads, -1)  # every head reads the same
+        k, v = A.head_linear(latents, self.w_uk), A.head_linear(latents, self.w_uv)
+        cu = torch.tensor([sum(counts[:b]) for b in range(len(counts) + 1)], dtype=torch.int32).to(q.device)
+        o = A.prompt_attention(q, k, new.key, v, cfg.scale, cu_q=cu, cu_k=cu,
+                               max_q=max(counts))
+        return self._finish(o, h)
+
+    def decode(self, delta, residual, cache: LatentCache, count: int = 1, tree=None, positions=None):
+        """`count` new tokens of every sequence: one decoded token, a causal
+        chunk, or with tree (int64 masks [T]) drafted tokens, whose positions
+        in the text the caller gives (int32 [T]; siblings share one)."""
+        cfg = self.cfg
+        running, slots = cache.extend([count] * len(cache.host_lens))
+        h, q, kv = self._queries(delta, residual)
+        ql = torch.empty(q.shape[0], cfg.heads, cfg.rank + cfg.rope, dtype=torch.bfloat16, device=q.device)
+        A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, running if positions is None else positions, slots,
+                        cache.pool, q_rope=q[..., cfg.nope:], q_out=ql[..., cfg.rank:])
+        A.head_linear(q[..., :cfg.nope], self.w_uk_t, out=ql[..., :cfg.rank])
+        o = A.latent_attention(ql, cache.pool, cache.pages, cache.lens, cfg.scale, max_len=max(cache.host_lens), tree=tree)
+        return self._finish(A.head_linear(o, self.w_uv), h)
+
+
+def main() -> None:
+    """A GLM-shaped block on synthetic weights: one prompt of 2048 tokens, then
+    single tokens and trees of 4 drafted tokens for 8 sequences."""
+    import time
+
+    cfg = BlockConfig()
+    block = DecoderBlock(cfg, random_weights(cfg, 0))
+    cache = LatentCache(cfg, n_pages=8 * 40, max_seqs=8, max_len=2400)
+
+    def timed(what, call, n):
+        call()
+        torch.cuda.synchronize()
+        t = time.perf_counter()
+        for _ in range(n):
+            call()
+        torch.cuda.synchronize()
+        print(f"{what}: {(time.perf_counter() - t) / n * 1e6:.1f} us", flush=True)
+
+    def inputs(T):
+        return torch.randn(T, cfg.hidden, device="cuda:0"), torch.randn(T, cfg.hidden, device="cuda:0").bfloat16()
+
+    counts = [2048] + [2048 - 64 * b for b in range(1, 8)]
+    x, r = inputs(sum(counts))
+    block.prompt(x, r, cache, counts)
+    x, r = inputs(8)
+    timed("one token for each of 8 sequences, attention half", lambda: block.decode(x, r, cache), 20)
+    x4, r4 = inputs(32)
+    tree = torch.tensor([1, 3, 5, 11] * 8, dtype=torch.int64, device="cuda:0")  # two branches
+
+    def verify():
+        at = torch.tensor([n + d for n in cache.host_lens for d in (0, 1, 1, 2)], dtype=torch.int32).to("cuda:0")
+        block.decode(x4, r4, cache, 4, tree=tree, positions=at)
+
+    timed("a tree of 4 drafted tokens for each, attention half", verify, 20)
+
+
+if __name__ == "__main__":
+    main()

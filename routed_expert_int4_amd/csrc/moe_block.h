@@ -37,9 +37,9 @@ struct AppendArgs {
     uint16_t* q_out;
     uint8_t* lat_q;            // [T][rank] E4M3, or nullptr
     float* lat_scale;
-    uint16_t* key;             // [T][rope], or nullptr
+    uint16_t* rows;            // [T][rank + rope], or nullptr
     long kv_stride, n_slots, q_stride_t, q_stride_h, qo_stride_t, qo_stride_h, lat_stride, ls_stride_t, ls_stride_g,
-        key_stride;
+        rows_stride;
     int T, rank, rope, heads, n_positions;
     float eps;
     bool weight_f32;

@@ -35,7 +35,7 @@ moe_status_t moe_add_rmsnorm(const void* d_x, int x_type, int64_t x_stride, cons
     if (!(eps >= 0.0f)) return fail(MOE_EINVAL, "%s: eps must be >= 0", who);
     if (H > kNormMaxWidth) return fail(MOE_EUNSUPPORTED, "%s: H (%d) is over %d", who, H, kNormMaxWidth);
     if (T == 0) return MOE_OK;
-    if (!d_x || !d_weight) return fail(MOE_EINVAL, "%s: NULL x or weight", who);
+    if (!d_x) return fail(MOE_EINVAL, "%s: NULL x", who);
     if (!d_sum && !d_y && !d_q) return fail(MOE_EINVAL, "%s: no output", who);
     if (d_q && !d_scale) return fail(MOE_EINVAL, "%s: 8-bit output without scales", who);
     const bool sum_f32 = (d_residual ? residual_type : x_type) == MOE_F32;
@@ -110,7 +110,7 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
                                int64_t n_slots, const uint16_t* d_q_rope, int heads, int64_t q_stride_t,
                                int64_t q_stride_h, uint16_t* d_q_out, int64_t qo_stride_t, int64_t qo_stride_h,
                                uint8_t* d_lat_q, int64_t lat_stride, float* d_lat_scale, int64_t ls_stride_t,
-                               int64_t ls_stride_g, uint16_t* d_key, int64_t key_stride, void* stream) {
+                               int64_t ls_stride_g, uint16_t* d_rows, int64_t rows_stride, void* stream) {
     const char* who = "moe_latent_append";
     if (T < 0 || rank < 1 || rope < 1 || n_positions < 0 || n_slots < 0 || (d_q_rope && heads < 1))
         return fail(MOE_EINVAL, "%s: T (%d), rank (%d), rope (%d), heads (%d), positions (%d) or slots", who, T, rank,
@@ -122,23 +122,23 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
     if (d_cache && !d_slots) return fail(MOE_EINVAL, "%s: a cache without slots", who);
     if (!d_q_rope != !d_q_out) return fail(MOE_EINVAL, "%s: queries need both an input and an output", who);
     if (!d_lat_q != !d_lat_scale) return fail(MOE_EINVAL, "%s: the 8-bit latent needs codes and scales", who);
-    if (!d_cache && !d_q_rope && !d_lat_q && !d_key) return fail(MOE_EINVAL, "%s: no output", who);
-    if (kv_stride < rank + rope || (d_lat_q && lat_stride < rank) || (d_key && key_stride < rope))
+    if (!d_cache && !d_q_rope && !d_lat_q && !d_rows) return fail(MOE_EINVAL, "%s: no output", who);
+    if (kv_stride < rank + rope || (d_lat_q && lat_stride < rank) || (d_rows && rows_stride < rank + rope))
         return fail(MOE_EINVAL, "%s: a row stride is below its row", who);
     if (rank > kAppendMaxRank) return fail(MOE_EUNSUPPORTED, "%s: rank (%d) is over %d", who, rank, kAppendMaxRank);
     if (rank % 8 || rope % 8 || kv_stride % 8 || q_stride_t % 8 || q_stride_h % 8 || qo_stride_t % 8 ||
-        qo_stride_h % 8 || lat_stride % 8 || key_stride % 8 || !on(d_kv, 16) || !on(d_weight, 16) ||
-        !on(d_cache, 16) || !on(d_q_rope, 16) || !on(d_q_out, 16) || !on(d_lat_q, 8) || !on(d_key, 16))
+        qo_stride_h % 8 || lat_stride % 8 || rows_stride % 8 || !on(d_kv, 16) || !on(d_weight, 16) ||
+        !on(d_cache, 16) || !on(d_q_rope, 16) || !on(d_q_out, 16) || !on(d_lat_q, 8) || !on(d_rows, 16))
         return fail(MOE_EUNSUPPORTED, "%s: rank, rope and the strides must be multiples of 8, pointers 16-byte aligned",
                     who);
     if (!on(d_table, 4) || !on(d_positions, 4) || !on(d_slots, 8) || !on(d_lat_scale, 4))
         return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
     AppendArgs a{};
     a.kv = d_kv, a.weight = d_weight, a.table = d_table, a.positions = d_positions, a.slots = d_slots;
-    a.cache = d_cache, a.q = d_q_rope, a.q_out = d_q_out, a.lat_q = d_lat_q, a.lat_scale = d_lat_scale, a.key = d_key;
+    a.cache = d_cache, a.q = d_q_rope, a.q_out = d_q_out, a.lat_q = d_lat_q, a.lat_scale = d_lat_scale, a.rows = d_rows;
     a.kv_stride = kv_stride, a.n_slots = n_slots, a.q_stride_t = q_stride_t, a.q_stride_h = q_stride_h;
     a.qo_stride_t = qo_stride_t, a.qo_stride_h = qo_stride_h, a.lat_stride = lat_stride, a.ls_stride_t = ls_stride_t;
-    a.ls_stride_g = ls_stride_g, a.key_stride = key_stride;
+    a.ls_stride_g = ls_stride_g, a.rows_stride = rows_stride;
     a.T = T, a.rank = rank, a.rope = rope, a.heads = heads, a.n_positions = n_positions, a.eps = eps;
     a.weight_f32 = weight_type == MOE_F32;
     return launched(launch_latent_append(a, static_cast<hipStream_t>(stream)), who);

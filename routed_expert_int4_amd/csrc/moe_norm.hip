@@ -104,15 +104,17 @@ __device__ __forceinline__ void store_fp8(const float (&y)[8], int c, int H, uin
 // One row per workgroup, eight columns per lane and round, I rounds: the row
 // stays in registers.  TYPES fixes the operand types of the 16-byte path (a
 // branch on them between the loads would wait for each in turn): residual 0
-// none, 1 bf16, 2 fp32, + 3 for fp32 x, + 6 for fp32 weights; -1 leaves all
-// to the arguments and moves single elements.
+// none, 1 bf16, 2 fp32, + 3 for fp32 x, + 6 for fp32 weights, + 12 for none (no
+// norm: the addition and the 8-bit output alone); -1 leaves all to the
+// arguments and moves single elements.
 template <int I, int TYPES>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a) {
     constexpr bool VEC = TYPES >= 0;
     __shared__ float part[16];
     const long t = blockIdx.x;
     if constexpr (VEC) {
-        a.x_f32 = TYPES / 3 % 2, a.weight_f32 = TYPES / 6;
+        a.x_f32 = TYPES / 3 % 2, a.weight_f32 = TYPES / 6 == 1;
+        if (TYPES >= 12) a.weight = nullptr;
         a.residual_f32 = TYPES % 3 == 2;
         if (TYPES % 3 == 0) a.residual = nullptr;
         a.sum_f32 = TYPES % 3 ? a.residual_f32 : a.x_f32;
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a) {
         for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
         if (c < a.H) {
             load8<VEC>(v[i], x, c, a.H, a.x_f32);
-            load8<VEC>(w[i], a.weight, c, a.H, a.weight_f32);
+            if (a.weight) load8<VEC>(w[i], a.weight, c, a.H, a.weight_f32);
             if (r) {
                 float u[8];
                 load8<VEC>(u, r, c, a.H, a.residual_f32);
@@ -142,14 +144,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a) {
     for (int i = 0; i < I; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-    const float rms = 1.0f / sqrtf(block_sum(ss, part) / (float)a.H + a.eps);
+    const float rms = a.weight ? 1.0f / sqrtf(block_sum(ss, part) / (float)a.H + a.eps) : 1.0f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c < a.H && sum) store8<VEC>(v[i], sum, c, a.H, a.sum_f32);
         float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = c + j < a.H ? v[i][j] * rms * w[i][j] : 0.0f;
+        for (int j = 0; j < 8; ++j) y[j] = c + j < a.H ? (a.weight ? v[i][j] * rms * w[i][j] : v[i][j]) : 0.0f;
         if (c < a.H && a.y) store8<VEC>(y, a.y + t * a.y_stride, c, a.H, false);
         if (a.q) store_fp8<VEC>(y, c, a.H, a.q + t * a.q_stride, a.scale + t * a.scale_stride_t, a.scale_stride_g);
     }
@@ -209,6 +211,7 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rms * w[j];
             if (c < a.rank && row) store8<true>(y, row, c, a.rank, false);
+            if (c < a.rank && a.rows) store8<true>(y, a.rows + t * a.rows_stride, c, a.rank, false);
             if (a.lat_q)
                 store_fp8<true>(y, c, a.rank, a.lat_q + t * a.lat_stride, a.lat_scale + t * a.ls_stride_t,
                                 a.ls_stride_g);
@@ -219,10 +222,10 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
     for (int k = blockDim.x - 1 - threadIdx.x; k < jobs; k += blockDim.x) {
         const int h = k / rope8 - 1, c = (k % rope8) * 8;
         if (h < 0) {
-            if (!row && !a.key) continue;
+            if (!row && !a.rows) continue;
             const u32x4 o = known ? rotate8(as_global<u32x4>(kv + a.rank)[c / 8], angle, c, a.rope) : nan;
             if (row) *reinterpret_cast<u32x4*>(row + a.rank + c) = o;
-            if (a.key) *reinterpret_cast<u32x4*>(a.key + t * a.key_stride + c) = o;
+            if (a.rows) *reinterpret_cast<u32x4*>(a.rows + t * a.rows_stride + a.rank + c) = o;
         } else {
             const u32x4 u = *as_global<u32x4>(a.q + t * a.q_stride_t + h * a.q_stride_h + c);
             *reinterpret_cast<u32x4*>(a.q_out + t * a.qo_stride_t + h * a.qo_stride_h + c) =
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
 
 template <int I, int TYPES>
 void launch_norm_types(const NormArgs& a, int types, int threads, hipStream_t s) {
-    if constexpr (TYPES < 12) {
+    if constexpr (TYPES < 18) {
         if (types == TYPES)
             hipLaunchKernelGGL((add_rmsnorm_kernel<I, TYPES>), dim3(a.T), dim3(threads), 0, s, a);
         else
@@ -242,7 +245,9 @@ void launch_norm_types(const NormArgs& a, int types, int threads, hipStream_t s)
 }
 template <int I>
 void launch_norm_rounds(const NormArgs& a, int threads, bool vec, hipStream_t s) {
-    const int types = vec ? (a.residual ? 1 + a.residual_f32 : 0) + 3 * a.x_f32 + 6 * a.weight_f32 : -1;
+    const int types = vec ? (a.residual ? 1 + a.residual_f32 : 0) + 3 * a.x_f32 +
+                                (a.weight ? 6 * a.weight_f32 : 12)
+                          : -1;
     launch_norm_types<I, -1>(a, types, threads, s);
 }
 
@@ -253,7 +258,7 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
     // 16-byte accesses where every row of every tensor starts on 16 bytes
     // (8 for the codes)
-    const bool vec = a.H % 8 == 0 && aligned(a.x, 16) && a.x_stride % 8 == 0 && aligned(a.weight, 16) &&
+    const bool vec = a.H % 8 == 0 && aligned(a.x, 16) && a.x_stride % 8 == 0 && (!a.weight || aligned(a.weight, 16)) &&
                      (!a.residual || (aligned(a.residual, 16) && a.residual_stride % 8 == 0)) &&
                      (!a.sum || (aligned(a.sum, 16) && a.sum_stride % 8 == 0)) &&
                      (!a.y || (aligned(a.y, 16) && a.y_stride % 8 == 0)) &&

@@ -594,3 +594,25 @@ def test_no_tokens():
     assert out.shape == (0, 4, 256)
     z = normal(g, 0, 4, 128)
     assert A.prompt_attention(normal(g, 0, 4, 192), z, normal(g, 0, 64), z, 1.0).shape == (0, 4, 128)
+
+
+@pytest.mark.parametrize("T,H", [(1, 6144), (5, 1000), (600, 512), (3, 7)])
+def test_quantize(T, H):
+    g = gen(T + H)
+    for x in (normal(g, T, H, std=3.0), normal(g, T, H, std=3.0, dtype=torch.float32)):
+        q, scale = A.quantize(x)
+        check_codes(q, scale, x.to(D))
+    r = normal(g, T, H)
+    both = A.add_rmsnorm(x, None, residual=r, out="both")
+    h = x.to(D) + r.to(D)
+    close(both.y, h, U * h.abs() + 1e-6, "sum without a norm")
+    check_codes(both.q, both.scale, h)
+
+
+@pytest.mark.parametrize("N,K", [(128, 128), (576, 6144), (100, 272), (1, 16)])
+def test_quantize_weight(N, K):
+    w = normal(gen(N), N, K)
+    code, scale = A.quantize_weight(w)
+    full = scale.to(D).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    assert tuple(scale.shape) == (-(-N // 128), -(-K // 128))
+    close(code.to(D) * full, w.to(D), torch.maximum(w.to(D).abs() * 2 ** -4, full * 2.0 ** -10) * (1 + 1e-5))
