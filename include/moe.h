@@ -514,8 +514,9 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
  * those whose bit is set in the 64-bit d_tree[t] (bit j = the sequence's j-th
  * new token; a token's own bit is not implied; tokens past 64 are unseen).
  * Rows on a page index outside [0, n_pages) or past the table are unseen.  A
- * token that sees nothing gets zeros; what unseen rows hold (NaN included)
- * does not matter unless another token of the same sequence sees them.
+ * token that sees nothing gets zeros.  Rows that a token does not see have no
+ * part in its output, whatever they hold (NaN and infinities included); a
+ * seen row with such values may turn all columns of the output to NaN.
  * max_q and max_len bound the new tokens and rows of a sequence (they size
  * the launch and the workspace only).  rank 512 or 256 with rope 64; scale
  * positive.  moe_latent_attention_workspace: device bytes needed, 256-byte
@@ -535,7 +536,8 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
  * queries d_cu_q[b] .. d_cu_q[b + 1] and keys d_cu_k[b] .. d_cu_k[b + 1].
  * causal != 0: its i-th query of n sees keys up to i + (keys - n) (the
  * queries are the last positions); else all.  A query that sees nothing gets
- * zeros.  (nope, rope, vdim) in {(64, 64, 64), (128, 64, 128),
+ * zeros; keys and values that it does not see have no part in its output,
+ * whatever they hold.  (nope, rope, vdim) in {(64, 64, 64), (128, 64, 128),
  * (192, 64, 256)}; strides multiples of 8 and pointers 16-byte aligned;
  * scale positive.  max_q bounds the queries of a sequence. */
 moe_status_t moe_prompt_attention(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* d_k,

@@ -14,6 +14,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef short i16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kFp8Max = 448.0f;  // largest E4M3 value
@@ -133,6 +134,7 @@ __device__ __forceinline__ bf16x8 values_transposed(unsigned lo, unsigned hi) {
 __device__ __forceinline__ bf16x8 lds_chunk(unsigned addr) {
     return __builtin_bit_cast(bf16x8, *(lds_u32x4*)addr);
 }
+__device__ __forceinline__ void lds_store(unsigned addr, u32x4 v) { *(lds_u32x4*)addr = v; }
 #pragma clang diagnostic pop
 
 // Largest value of the two lanes (halves of the wave) that share a query.
@@ -147,6 +149,30 @@ __device__ __forceinline__ float half_sum(float v) {
     const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
     const unsigned a = r[0], b = r[1];
     return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+}
+
+// Values that are not finite.  A masked key has an exponential of zero, and
+// zero times infinity is NaN: in tiles where some query does not see a key
+// that others do, values are looked over first, and where one is not finite
+// only the finite ones enter the sums; a query that does see such a key
+// becomes NaN through its exponential.
+// Largest magnitudes, as bits, of the even and the odd values; not_finite says
+// whether one of them is not finite.
+__device__ __forceinline__ u16x2 magnitudes(u32x4 v) {
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7FFF7FFFu));
+    return m;
+}
+__device__ __forceinline__ bool not_finite(u16x2 m) { return m[0] >= 0x7F80 || m[1] >= 0x7F80; }
+__device__ __forceinline__ u32x4 finite_only(u32x4 u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned low = (u[i] & 0x7F80u) == 0x7F80u ? 0u : u[i] & 0xFFFFu;
+        const unsigned high = (u[i] & 0x7F800000u) == 0x7F800000u ? 0u : u[i] & 0xFFFF0000u;
+        u[i] = low | high;
+    }
+    return u;
 }
 
 // Exponentials of eight scores as the product with the values takes them, and

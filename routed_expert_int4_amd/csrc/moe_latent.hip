@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 }
                 settle(s);
             }
+            bool bad = false;  // a value that is not finite
             if (now != ~0ull || (t + 1) * kTile > context + (a.tree ? 0 : 1)) {
                 // visible keys of this tile, a bit each; this lane's registers
                 // hold keys 8 (i / 4) + 4 half + i % 4 of the wave's half
@@ -372,6 +373,14 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[i] = word >> (8 * (i / 4) + i % 4) & 1 ? s[i] : -__builtin_inff();
+                if (before < kTile && (a.tree || count > 1)) {
+                    // new tokens that some of them do not see: this wave looks
+                    // over its share of the rows
+                    unsigned p = lds0 + tile + wave * (kLatBytes / kWaves) + lane * 16;
+#pragma unroll 4
+                    for (int i = 0; i < kLatBytes / kWaves / 1024; ++i, p += 1024)
+                        bad |= not_finite(magnitudes(__builtin_bit_cast(u32x4, lds_chunk(p))));
+                }
             }
             // the first values are read before the exchange
             constexpr int kAhead = 6;
@@ -409,13 +418,27 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             };
             float sum = exponentials();
             if (half == 0) shared_top[wave][col] = top;
-            if (lane == 0) shared_raise[t & 1][wave] = raise;
+            const bool guard = __any(bad);
+            if (lane == 0) shared_raise[t & 1][wave] = raise + 2 * guard;
             lds_barrier();
             int any = 0;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) any |= shared_raise[t & 1][w];
             u32x4 q0 = shared_p[other][0][lane], q1 = shared_p[other][1][lane];
-            if (__builtin_amdgcn_readfirstlane(any)) {
+            any = __builtin_amdgcn_readfirstlane(any);
+            if (any & 2) {
+                // Every wave has taken its scores: only the finite values stay
+                // in the tile.  A row that sees one of the others has it in its
+                // score, the value being part of the key.
+                unsigned at_row = lds0 + tile + wave * (kLatBytes / kWaves) + lane * 16;
+#pragma unroll 1
+                for (int i = 0; i < kLatBytes / kWaves / 1024; ++i, at_row += 1024)
+                    lds_store(at_row, finite_only(__builtin_bit_cast(u32x4, lds_chunk(at_row))));
+                lds_barrier();
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) x[j] = value_chunk(j);
+            }
+            if (any & 1) {
                 // some row's maximum moves: both waves of each pair take the
                 // new one and compute their exponentials again
                 const float nm = fmaxf(m, fmaxf(top, shared_top[other][col]));

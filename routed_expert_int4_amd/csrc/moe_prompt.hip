@@ -6,9 +6,22 @@
 // workgroup owns 128 queries of one head, 32 per wave; tiles of KT keys go
 // through LDS, loaded asynchronously one tile ahead into the other of two
 // buffers.  Bound by the matrix cores: per 64 keys a wave issues 40 matrix
-// instructions of 32 x 32 x 16 (widths 192 and 128) and some 900 cycles of
-// exponentials and statistics, which the second workgroup on the same CU
-// fills in (half of LDS each).
+// instructions of 32 x 32 x 16 (widths 192 and 128), 1280 cycles, and some
+// 900 cycles of exponentials and statistics, which the second workgroup on
+// the same CU fills in (half of LDS each).
+//
+// 64 heads of widths 192 and 128, causal: 8192 tokens 1.22 ms, 1.13 PFLOP/s
+// (a large bf16 matrix product reaches 1.50); three sequences of 257 tokens
+// 17 us, where launch and the longest run of tiles count.
+// 4096 tokens, 32 heads: 107 us (64, 64), 163 us (128, 128), 391 us
+// (192, 256; tiles of 64 keys spill: 729).
+//
+// A weight of zero times a value that is not finite would still make NaN, so
+// tiles that some query of the wave does not see whole are searched for such
+// values first; where there are any, they count as zero in the products and
+// the scores of their keys, where seen, turn NaN.
+#include <type_traits>
+
 #include "moe_block.h"
 #include "moe_block_device.h"
 
@@ -66,7 +79,8 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
     const int wave_last = q0 + wave * 32 + 31 < q_count ? q0 + wave * 32 + 31 : q_count - 1;
     const int limit = row_ok ? visible(my_q) : 0;
     const int wave_limit = uniform(q0 + wave * 32 < q_count ? visible(wave_last) : 0);
-    const int wave_full = uniform(a.causal ? visible(q0 + wave * 32) : k_count);  // keys that all of the wave's rows see
+    // tiles that all of the wave's rows see whole
+    const int wave_full = uniform((q0 + wave * 32 < q_count ? visible(q0 + wave * 32) : 0) / KT);
     const int tiles = uniform((visible(last_q) + KT - 1) / KT);
 
     // Loads of one tile: an instruction covers whole rows, and the place of a
@@ -116,13 +130,13 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
     // loop, where the next tile is on its way
 #pragma unroll
     for (int k = 0; k < kParts * 4; ++k) asm volatile("" : "+v"(qf[k]));
-    if (tiles > 0) issue(0);
-    for (int t = 0; t < tiles; ++t) {
+    auto next_tile = [&](int t) {
         wait_vmem<0>();
         lds_barrier();  // tile t is in LDS, and every wave is done with the other buffer
         if (t + 1 < tiles) issue(t + 1);
+    };
+    auto one_tile = [&](int t, auto masked) __attribute__((always_inline)) {
         const int key0 = t * KT;
-        if (key0 >= wave_limit) continue;
         const unsigned buf = (t & 1) * kTileBytes;
         f32x16 s[kSub] = {};
         unsigned key_base[4];  // the rest of an address is an immediate offset
@@ -130,7 +144,7 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
         for (int k = 0; k < 4; ++k) key_base[k] = (key_at + buf) ^ k * 32;
         // operands are read kAhead instructions before their use (the
         // scheduling barriers keep that order); tiles of 32 keys alternate
-        constexpr int kAhead = 4;
+        constexpr int kAhead = 3;
         bf16x8 x[kAhead];
         auto key_chunk = [&](int i) {
             const int k = i / kSub, u = i % kSub;
@@ -144,6 +158,42 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
             if (i + kAhead < kParts * 4 * kSub) x[i % kAhead] = key_chunk(i + kAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
+        bool guarded = false;  // a value of this tile is not finite, and some query does not see all of it
+        if constexpr (masked.value) {
+            const int left = limit - key0 - 4 * half;  // keys of this tile that this lane's query sees
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (u * 32 + 8 * (i / 4) + i % 4 >= left) s[u][i] = -__builtin_inff();
+            constexpr int kReads = KT * VD * 2 / 1024, kRowLanes = VD / 8;
+            const unsigned at = lds0 + buf + kParts * kPartBytes + lane * 16;
+            u16x2 most = {0, 0};
+#pragma unroll
+            for (int i = 0; i < kReads; ++i)
+                most = __builtin_elementwise_max(most, magnitudes(__builtin_bit_cast(u32x4, lds_chunk(at + i * 1024))));
+            guarded = __any(not_finite(most));
+            if (guarded) {
+                unsigned long long keys = 0;
+#pragma unroll 1
+                for (int i = 0; i < kReads; ++i) {
+                    const unsigned long long bad =
+                        __ballot(not_finite(magnitudes(__builtin_bit_cast(u32x4, lds_chunk(at + i * 1024)))));
+                    for (int r = 0; r < 64 / kRowLanes; ++r)
+                        if (bad >> (r * kRowLanes) & ((1ull << kRowLanes) - 1)) keys |= 1ull << (i * (64 / kRowLanes) + r);
+                }
+                // the scores of these keys turn NaN where they are seen
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    const unsigned word = (unsigned)(keys >> (u * 32)) >> (4 * half);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int key = 8 * (i / 4) + i % 4;
+                        if ((word >> key & 1) && u * 32 + key < left) s[u][i] = __builtin_nanf("");
+                    }
+                }
+            }
+        }
         unsigned value_base[4];
 #pragma unroll
         for (int k = 0; k < (kOut < 4 ? kOut : 4); ++k) value_base[k] = (value_at + buf) ^ k * 64;
@@ -152,17 +202,9 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
             const unsigned lo = value_base[k % 4] + (k / 4) * 256 + u * 16 * VD * 2;
             return values_transposed(lo, lo + 8 * VD * 2);
         };
+        // the first values are read before the exponentials
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) x[i] = value_chunk(i);
-        if (key0 + KT > wave_full) {
-            int left = limit - key0 - 4 * half;  // keys of this tile that this lane's query sees
-            asm volatile("" : "+v"(left));       // keeps the comparisons in this branch
-#pragma unroll
-            for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (u * 32 + 8 * (i / 4) + i % 4 >= left) s[u][i] = -__builtin_inff();
-        }
         // Exponentials against the running maximum as it is.  It only has to
         // move when they grow large: their sum says so (and, at the first
         // tile, infinitely so), without a maximum over every tile.
@@ -197,6 +239,16 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
             sum = all_exponentials();
         }
         l += sum;
+        if (masked.value && guarded) {
+#pragma unroll
+            for (int i = 0; i < kOut * kSub * 2; ++i) {
+                const int k = i / (kSub * 2), u = i % (kSub * 2);
+                const bf16x8 v = __builtin_bit_cast(bf16x8, finite_only(__builtin_bit_cast(u32x4, value_chunk(i))));
+                o[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[u], o[k], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            return;
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < kOut * kSub * 2; ++i) {
@@ -205,6 +257,18 @@ __global__ void __launch_bounds__(256, PER_CU) prompt_attention_kernel(PromptArg
             if (i + kAhead < kOut * kSub * 2) x[i % kAhead] = value_chunk(i + kAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    // Two loops, so that the one over whole tiles carries nothing of the
+    // masks; every wave passes one barrier per tile in either.
+    if (tiles > 0) issue(0);
+    int t = 0;
+    for (; t < wave_full; ++t) {
+        next_tile(t);
+        one_tile(t, std::false_type{});
+    }
+    for (; t < tiles; ++t) {
+        next_tile(t);
+        if (t * KT < wave_limit) one_tile(t, std::true_type{});
     }
     if (!row_ok) return;
     l = half_sum(l);
@@ -237,7 +301,7 @@ hipError_t launch_prompt_attention(const PromptArgs& a, hipStream_t s) {
     else if (a.nope == 128)
         launch_shape<128, 64, 128, 64, 2>(a, s);
     else  // 230 registers of queries and sums: one wave per SIMD
-        launch_shape<192, 64, 256, 64, 1>(a, s);
+        launch_shape<192, 64, 256, 32, 1>(a, s);
     return hipGetLastError();
 }
 

@@ -616,3 +616,44 @@ def test_quantize_weight(N, K):
     full = scale.to(D).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
     assert tuple(scale.shape) == (-(-N // 128), -(-K // 128))
     close(code.to(D) * full, w.to(D), torch.maximum(w.to(D).abs() * 2 ** -4, full * 2.0 ** -10) * (1 + 1e-5))
+
+
+@pytest.mark.parametrize("nope,vdim", [(64, 64), (128, 128), (192, 256)])
+@pytest.mark.parametrize("at", [0, 37, 63, 64, 150, 199])
+def test_prompt_attention_not_finite_in_masked_places(nope, vdim, at):
+    """What a query does not see does not reach it; what it does see, does."""
+    g = gen(at)
+    T, heads = 200, 2
+    q, k, v, kr = normal(g, T, heads, nope + 64), normal(g, T, heads, nope), normal(g, T, heads, vdim), normal(g, T, 64)
+    ref, mag = prompt_ref(q, k, kr, v, [T], [T], 0.08)
+    for what, bad in (("v", float("nan")), ("v", float("inf")), ("v", -float("inf")), ("k", float("nan"))):
+        kk, vv = k.clone(), v.clone()
+        if what == "v":
+            vv[at, 1, 5] = bad
+        else:
+            kk[at, 1, 5] = bad
+        out = A.prompt_attention(q, kk, kr, vv, 0.08)
+        close(out[:, 0], ref[:, 0], U * ref[:, 0].abs() + U * mag[:, 0], f"other head, {what} {bad}")
+        close(out[:at], ref[:at], U * ref[:at].abs() + U * mag[:at], f"earlier queries, {what} {bad}")
+        assert not out[at:, 1, 5].isfinite().any(), f"later queries, {what} {bad}"
+
+
+@pytest.mark.parametrize("heads,rank", [(64, 512), (8, 512), (16, 256)])
+def test_latent_attention_not_finite_in_masked_places(heads, rank):
+    g = gen(heads)
+    lens, nq = [130, 66, 7], 5
+    q, cache, pages, dl = latent_case(g, lens, [nq] * 3, heads, rank, 16)
+    tree = torch.tensor([0b1, 0b11, 0b101, 0b1001, 0b10011] * 3, dtype=torch.int64, device=DEV)
+    for masks, sees in ((None, [2, 3, 4]), (tree, [2])):  # tokens that see the new token 2
+        ref, mag = latent_ref(q, cache, pages, lens, [nq] * 3, 0.07, rank, tree=masks)
+        for bad in (float("nan"), float("inf")):
+            dirty = cache.clone()
+            for b, n in enumerate(lens):
+                p = n - nq + 2
+                dirty[int(pages[b, p // 16]), p % 16, 3:300:7] = bad
+            out = A.latent_attention(q, dirty, pages, dl, 0.07, max_len=130, tree=masks)
+            for t in range(3 * nq):
+                if t % nq in sees:
+                    assert not out[t].isfinite().all(), (masks is None, t)
+                else:
+                    close(out[t], ref[t], U * ref[t].abs() + U * mag[t], f"token {t}, {bad}")
