@@ -13,13 +13,22 @@
 // token per sequence is bound by reading the cache and several tokens by the
 // matrix cores.  A tile of 64 cache rows is loaded asynchronously one ahead
 // into the other of two LDS buffers and serves as keys (row reads) and as
-// values (transposed reads).  Two waves share 32 rows: each computes the
-// scores of its half of the tile's keys and the sums of its half of the
-// columns, so a wave holds 144 registers of queries and 128 of sums (rows
-// whole in one wave would need 400, more than the compiler can place), and
-// hands the other wave its exponentials, rounded to bf16, through LDS: the
-// two layouts agree lane by lane, 32 bytes each.  A workgroup is one or two
-// such pairs.
+// values (transposed reads).  Four waves share 32 rows: each computes partial
+// scores of half of the tile's keys over half of the inner dimension, takes
+// the other half's from its neighbour, and then has the exponentials of a
+// quarter of the keys, rounded to bf16, for all four, each of which sums a
+// quarter of the columns.  A wave thus holds 72 registers of queries and 64 of
+// sums, and two waves fit a SIMD (rows whole in one wave would need 400).  All
+// exchanges go through LDS, which is full: 144 KB of tiles, 16 KB of slots.  A
+// workgroup is one or two such fours, 32 or 64 rows.
+//
+// Measured, rank 512, 64 heads: 32 sequences of 16384 rows, one token each,
+// 132 us (4.6 TB/s), four tokens 357 us (0.83 PFLOP/s); trees of four tokens
+// over ragged rows, 10400 on average, 214 us.  One sequence, one token: 1013
+// rows 21 us, 16384 rows 33 us, 65536 rows 40 us.  A tile takes a workgroup
+// 2.6 us, of which matrix instructions are 1.0; the loads stall the waves that
+// issue them for about 0.5 (issued all at once: 4 % slower; some of them after
+// the scores, so that they arrive late: 3 to 9 %).
 //
 // Row blocks of one sequence read the same cache rows, so GS workgroups work
 // as a group: on the same die (one L2), over the same tiles, each on its own
@@ -151,34 +160,8 @@ __device__ __forceinline__ float* part_sums(const LatentArgs& a, int slot) {
 // by four chunks cover all banks.
 __device__ __forceinline__ int place_mix(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 
-// Matrix instructions with the register file of each operand fixed: 144
-// registers of queries lie in the accumulation file, 128 of sums, the scores
-// and the LDS operands in the other (left to itself the compiler moves 240
-// registers between the two per tile).  It does not see hazards of assembly:
-// the s_nop covers operands that vector instructions have written just before
-// (the first of a row of instructions only: the others read what loads, whose
-// waits it inserts, brought), settle() the states from a matrix instruction to
-// the first other reader of its result (19 at most; instructions that
-// accumulate into the same registers need none).
-__device__ __forceinline__ void mfma_scores(f32x16& s, bf16x8 keys, bf16x8 queries, bool first) {
-    if (first)
-        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(keys), "a"(queries));
-    else
-        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(s) : "v"(keys), "a"(queries));
-}
-__device__ __forceinline__ void mfma_sums(f32x16& o, bf16x8 values, bf16x8 p, bool first) {
-    if (first)
-        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(o) : "v"(values), "v"(p));
-    else
-        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(o) : "v"(values), "v"(p));
-}
-__device__ __forceinline__ void settle(f32x16& v) { asm volatile("s_nop 15\n\ts_nop 3" : "+v"(v)); }
-
-template <int N>
-__device__ __forceinline__ void settle(f32x16 (&o)[N]) {
-    settle(o[0]);
-#pragma unroll
-    for (int k = 1; k < N; ++k) asm volatile("" : "+v"(o[k]));  // volatile: behind the wait
+__device__ __forceinline__ void mfma(f32x16& c, bf16x8 a, bf16x8 b) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
 // The n lowest bits (none below 0, all from 64 up).
@@ -187,17 +170,21 @@ __device__ __forceinline__ unsigned long long low_bits(int n) {
 }
 
 template <int RANK, int RG>
-__global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArgs a) {
-    constexpr int kWaves = RG * 2, ROWS = RG * 32;
-    constexpr int kLat = RANK / 16, kRope = kRopeWidth / 16, kOut = RANK / 64, WIDTH = RANK + kRopeWidth;
+__global__ void __launch_bounds__(RG * 256, 1) latent_attention_kernel(LatentArgs a) {
+    constexpr int kWaves = RG * 4, ROWS = RG * 32, WIDTH = RANK + kRopeWidth;
+    // a wave's inner steps of 16 (latent, position part), its columns by 32
+    constexpr int kLat = RANK / 32, kRope = kRopeWidth / 32, kSteps = kLat + kRope, kOut = RANK / 128;
     constexpr int kLatBytes = kTile * RANK * 2, kTileBytes = kLatBytes + kTile * kRopeWidth * 2;
     constexpr int kRowsPerLoad = 1024 / (RANK * 2);  // cache rows per asynchronous load
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTileBytes];
-    __shared__ u32x4 shared_p[kWaves][2][64];   // exponentials of a wave's half of the keys
-    __shared__ float shared_top[kWaves][32];    // largest score of its rows in this tile (at the end: totals)
-    __shared__ int shared_raise[2][kWaves];     // a row's maximum has to move (by tile parity)
+    // Slots by which the four waves of 32 rows hand over partial scores, then
+    // exponentials, maxima and flags.  A wave writes its scores to its own
+    // slot, reads those of wave ^ 1, and then owns what it has read.
+    __shared__ u32x4 slots[kWaves][2][64];
     const int lane = threadIdx.x & 63, wave = wave_in_block(), half = lane >> 5, col = lane & 31;
-    const int rg = wave >> 1, side = wave & 1, other = wave ^ 1;
+    const int rg = wave >> 2, quarter = wave & 3, side = quarter >> 1, inner = quarter & 1, other = wave ^ 1;
+    float* const my_top = reinterpret_cast<float*>(slots[other][1]);  // 32 maxima (at the end: totals)
+    auto slot_of = [&](int w) { return reinterpret_cast<const float*>(slots[w ^ 1][1]); };
     // workgroups are dealt to the eight dies in turn: group g lies on die g % 8
     const int turn = blockIdx.x >> 3, run = (blockIdx.x & 7) + 8 * (turn / a.group), member = turn % a.group;
     int before;
@@ -220,10 +207,11 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
     unsigned key_at, rope_at, value_at;
     {
         const int r = side * 32 + col, vr = half * 4 + ((lane & 15) >> 2);
-        key_at = lds0 + r * RANK * 2 + (half ^ place_mix(r)) * 16;
-        rope_at = lds0 + kLatBytes + r * kRopeWidth * 2 + ((half ^ (r >> 1)) & 7) * 16;
-        const int chunk = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-        value_at = lds0 + vr * RANK * 2 + side * RANK + (chunk ^ place_mix(vr)) * 16 + (lane & 1) * 8;
+        key_at = lds0 + r * RANK * 2 + inner * RANK + (half ^ place_mix(r)) * 16;
+        rope_at = lds0 + kLatBytes + r * kRopeWidth * 2 + (((half | inner * 4) ^ (r >> 1)) & 7) * 16;
+        const int first = quarter * (RANK / 32);  // the wave's first chunk of a row
+        const int chunk = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1) + (first & 15);
+        value_at = lds0 + vr * RANK * 2 + (first >> 4) * 256 + (chunk ^ place_mix(vr)) * 16 + (lane & 1) * 8;
     }
 
     while (at < run_end) {
@@ -246,12 +234,14 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
         const bool row_ok = row < count * a.heads;
         const int token = row_ok ? row / a.heads : 0, head = row_ok ? row % a.heads : 0;
         const long long mask = a.tree && row_ok ? a.tree[first + token] : 0;
-        bf16x8 qf[kLat + kRope];
+        bf16x8 qf[kSteps];
         {
             const uint16_t* p = a.q + (first + token) * a.q_stride_t + head * a.q_stride_h + half * 8;
 #pragma unroll
-            for (int k = 0; k < kLat + kRope; ++k)
-                qf[k] = __builtin_bit_cast(bf16x8, *as_global<u32x4>(p + k * 16));
+            for (int k = 0; k < kSteps; ++k) {
+                const int at_inner = k < kLat ? inner * (RANK / 2) + k * 16 : RANK + inner * 32 + (k - kLat) * 16;
+                qf[k] = __builtin_bit_cast(bf16x8, *as_global<u32x4>(p + at_inner));
+            }
         }
         // Page and place of cache row t * 64 + lane (-1 past the end).
         const int32_t* my_pages = a.pages + seq * a.pages_stride;
@@ -302,7 +292,7 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
         // the queries have landed: the compiler must not wait for them inside
         // the loop, where other loads are on their way
 #pragma unroll
-        for (int k = 0; k < kLat + kRope; ++k) asm volatile("" : "+a"(qf[k]));
+        for (int k = 0; k < kSteps; ++k) asm volatile("" : "+v"(qf[k]));
         {
             const unsigned long long addr = address(page, off);
 #pragma unroll
@@ -322,8 +312,9 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             int chunk = lane;
             asm volatile("" : "+v"(chunk));  // the mixed places are not worth a register each across the loop
             const unsigned tile = buf * kTileBytes;
-            f32x16 s = {};
+            float s[8];  // of the wave's 32 keys, registers inner * 8 on
             {
+                f32x16 sum = {};  // over the wave's half of the inner dimension
                 // operands are read kAhead instructions before their use; the
                 // scheduling barriers keep the compiler from reading them all
                 // at once
@@ -340,23 +331,37 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) x[k] = key_chunk(k);
 #pragma unroll
-                for (int k = 0; k < kLat + kRope; ++k) {
-                    mfma_scores(s, x[k % kAhead], qf[k], k == 0);
-                    if (k + kAhead < kLat + kRope) x[k % kAhead] = key_chunk(k + kAhead);
+                for (int k = 0; k < kSteps; ++k) {
+                    mfma(sum, x[k % kAhead], qf[k]);
+                    if (k + kAhead < kSteps) x[k % kAhead] = key_chunk(k + kAhead);
                     // the next tile's loads, spread over the instructions (a
                     // wave that issues them in one go stalls in the queue)
-                    constexpr int kSteps = kLat + kRope;
 #pragma unroll
                     for (int i = k * kLoads / kSteps; i < (k + 1) * kLoads / kSteps; ++i)
                         if (more) issue(i, buf ^ 1, next, chunk);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                settle(s);
+                f32x4 give[2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s[i] = inner ? sum[8 + i] : sum[i];
+                    give[i / 4][i % 4] = inner ? sum[i] : sum[8 + i];
+                }
+                slots[wave][0][lane] = __builtin_bit_cast(u32x4, give[0]);
+                slots[wave][1][lane] = __builtin_bit_cast(u32x4, give[1]);
+                lds_barrier();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f32x4 got = __builtin_bit_cast(f32x4, slots[other][j][lane]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[j * 4 + i] += got[i];
+                }
             }
             bool bad = false;  // a value that is not finite
             if (now != ~0ull || (t + 1) * kTile > context + (a.tree ? 0 : 1)) {
                 // visible keys of this tile, a bit each; this lane's registers
-                // hold keys 8 (i / 4) + 4 half + i % 4 of the wave's half
+                // hold keys 16 inner + 8 (i / 4) + 4 half + i % 4 of the
+                // wave's half
                 const int before = context - t * kTile;  // place of the first new token
                 unsigned long long sees;
                 if (a.tree) {
@@ -369,9 +374,9 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                     sees = low_bits(before + token + 1);
                 }
                 sees &= now;
-                const unsigned word = (unsigned)(sees >> (side * 32)) >> (4 * half);
+                const unsigned word = (unsigned)(sees >> (quarter * 16)) >> (4 * half);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8; ++i)
                     s[i] = word >> (8 * (i / 4) + i % 4) & 1 ? s[i] : -__builtin_inff();
                 if (before < kTile && (a.tree || count > 1)) {
                     // new tokens that some of them do not see: this wave looks
@@ -385,48 +390,54 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             // the first values are read before the exchange
             constexpr int kAhead = 6;
             bf16x8 x[kAhead];
-            unsigned lo[4], hi[4];
+            unsigned lo[kOut], hi[kOut];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kOut; ++k) {
                 lo[k] = (value_at + tile) ^ k * 64;
                 hi[k] = (lo[k] ^ 32) + 8 * RANK * 2;
             }
             auto value_chunk = [&](int j) {
-                const int k = j >> 2, at_key = (j & 3) * 16 * RANK * 2 + (k >> 2) * 256;
-                return values_transposed(lo[k & 3] + at_key, hi[k & 3] + at_key);
+                const int k = j >> 2, at_key = (j & 3) * 16 * RANK * 2;
+                return values_transposed(lo[k] + at_key, hi[k] + at_key);
             };
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) x[j] = value_chunk(j);
             float top = s[0];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
             top = half_max(top);
             const bool raise = __any((top - m) * c > kMaxSlack);
-            bf16x8 p[4];  // of both waves' keys, in key order
             auto exponentials = [&]() {
                 const float mc = m * c;
                 float sum = 0.0f;
+                bf16x8 p;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
                     sum += e;
-                    p[i / 8][i % 8] = (__bf16)e;
+                    p[i] = (__bf16)e;
                 }
-                shared_p[wave][0][lane] = __builtin_bit_cast(u32x4, p[0]);
-                shared_p[wave][1][lane] = __builtin_bit_cast(u32x4, p[1]);
+                slots[other][0][lane] = __builtin_bit_cast(u32x4, p);
                 return sum;
             };
             float sum = exponentials();
-            if (half == 0) shared_top[wave][col] = top;
+            if (half == 0) my_top[col] = top;
             const bool guard = __any(bad);
-            if (lane == 0) shared_raise[t & 1][wave] = raise + 2 * guard;
+            // the position part of this tile has served: flags lie there, a byte
+            // per wave
+            uint8_t* const flags = lds + tile + kLatBytes;
+            if (lane == 0) flags[wave] = (uint8_t)(raise + 2 * guard);
             lds_barrier();
-            int any = 0;
+            unsigned any = reinterpret_cast<const unsigned*>(flags)[0];
+            if constexpr (kWaves > 4) any |= reinterpret_cast<const unsigned*>(flags)[1];
+            bf16x8 p[4];  // of all 64 keys, in key order
+            auto take = [&]() {
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) any |= shared_raise[t & 1][w];
-            u32x4 q0 = shared_p[other][0][lane], q1 = shared_p[other][1][lane];
+                for (int w = 0; w < 4; ++w) p[w] = __builtin_bit_cast(bf16x8, slots[rg * 4 + (w ^ 1)][0][lane]);
+            };
+            take();
             any = __builtin_amdgcn_readfirstlane(any);
-            if (any & 2) {
+            if (any & 0x02020202u) {
                 // Every wave has taken its scores: only the finite values stay
                 // in the tile.  A row that sees one of the others has it in its
                 // score, the value being part of the key.
@@ -438,10 +449,12 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) x[j] = value_chunk(j);
             }
-            if (any & 1) {
-                // some row's maximum moves: both waves of each pair take the
-                // new one and compute their exponentials again
-                const float nm = fmaxf(m, fmaxf(top, shared_top[other][col]));
+            if (any & 0x01010101u) {
+                // some row's maximum moves: the four waves of its block take
+                // the new one and compute their exponentials again
+                float nm = m;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) nm = fmaxf(nm, slot_of(rg * 4 + w)[col]);
                 const float f = __builtin_amdgcn_exp2f((m - nm) * c);
                 m = nm;
                 l *= f;
@@ -454,40 +467,32 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
                 lds_barrier();  // the first ones are read
                 sum = exponentials();
                 lds_barrier();
-                q0 = shared_p[other][0][lane];
-                q1 = shared_p[other][1][lane];
+                take();
             }
             l += sum;
-            {
-                const bf16x8 p0 = p[0], p1 = p[1], r0 = __builtin_bit_cast(bf16x8, q0),
-                             r1 = __builtin_bit_cast(bf16x8, q1);
-                p[0] = side ? r0 : p0;
-                p[1] = side ? r1 : p1;
-                p[2] = side ? p0 : r0;
-                p[3] = side ? p1 : r1;
-            }
             {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < 4 * kOut; ++j) {
-                    mfma_sums(o[j >> 2], x[j % kAhead], p[j & 3], j == 0);
+                    mfma(o[j >> 2], x[j % kAhead], p[j & 3]);
                     if (j + kAhead < 4 * kOut) x[j % kAhead] = value_chunk(j + kAhead);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                settle(o);
             }
         }
-        // totals over the tile halves of both waves
+        // totals over the keys of all four waves
         l = half_sum(l);
         __syncthreads();
-        if (half == 0) shared_top[wave][col] = l;
+        if (half == 0) my_top[col] = l;
         __syncthreads();
-        l += shared_top[other][col];
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) l += slot_of(rg * 4 + w)[col];
         if (t_first == 0 && t_last == tiles) {
             if (row_ok) {
                 // a row that sees no key gives zero
                 const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-                uint16_t* out = a.out + (first + token) * a.o_stride_t + head * a.o_stride_h + side * (RANK / 2) + half * 4;
+                uint16_t* out = a.out + (first + token) * a.o_stride_t + head * a.o_stride_h + quarter * (RANK / 4) + half * 4;
 #pragma unroll
                 for (int k = 0; k < kOut; ++k)
 #pragma unroll
@@ -503,9 +508,9 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
             for (int k = 0; k < kOut; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<f32x4*>(part + (long)r * RANK + side * (RANK / 2) + k * 32 + i * 8 + half * 4) =
+                    *reinterpret_cast<f32x4*>(part + (long)r * RANK + quarter * (RANK / 4) + k * 32 + i * 8 + half * 4) =
                         f32x4{o[k][i * 4], o[k][i * 4 + 1], o[k][i * 4 + 2], o[k][i * 4 + 3]};
-            if (half == 0 && side == 0) {
+            if (half == 0 && quarter == 0) {
                 part[ROWS * RANK + r * 2] = m;
                 part[ROWS * RANK + r * 2 + 1] = l;
             }
@@ -515,13 +520,16 @@ __global__ void __launch_bounds__(RG * 128, 1) latent_attention_kernel(LatentArg
     }
 }
 
-// Joins the partial sums of every unit that more than one run worked on: a
-// wave per row, RANK / 64 columns per lane, the runs in order.
-template <int RANK, int ROWS>
+// Joins the partial sums of every unit that more than one run worked on:
+// RANK / 64 columns per lane, the runs in order.  SPLIT waves share a row, 16
+// runs each in turn, and are joined in wave order.
+template <int RANK, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
-    constexpr int V = RANK / 64;
-    const int lane = threadIdx.x & 63;
-    const int seq = blockIdx.y, row = blockIdx.x * 4 + wave_in_block();
+    constexpr int V = RANK / 64, kAtOnce = SPLIT > 1 ? 16 : 64;
+    __shared__ float shared_o[SPLIT > 1 ? 4 : 1][V][64];
+    __shared__ float shared_ml[4][2];
+    const int lane = threadIdx.x & 63, wave = wave_in_block(), part_of = wave % SPLIT;
+    const int seq = blockIdx.y, row = blockIdx.x * (4 / SPLIT) + wave / SPLIT;
     const SeqShape shape = seq_shape<ROWS>(a, seq);
     if (row >= shape.count * a.heads) return;
     int before;
@@ -538,9 +546,9 @@ __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
     float m = kNoMax, l = 0.0f, o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.0f;
-    for (int b0 = g0; b0 <= g1; b0 += 64) {
-        // maxima and totals of up to 64 runs, one per lane
-        const int n = g1 + 1 - b0 < 64 ? g1 + 1 - b0 : 64;
+    for (int b0 = g0 + part_of * kAtOnce; b0 <= g1; b0 += SPLIT * kAtOnce) {
+        // maxima and totals of these runs, one per lane
+        const int n = g1 + 1 - b0 < kAtOnce ? g1 + 1 - b0 : kAtOnce;
         float pm = kNoMax, pl = 0.0f;
         if (lane < n) {
             const float* p = part(b0 + lane) + ROWS * RANK + r * 2;
@@ -572,6 +580,29 @@ __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
             }
         }
     }
+    if constexpr (SPLIT > 1) {
+        static_assert(SPLIT == 4, "a workgroup per row");
+#pragma unroll
+        for (int i = 0; i < V; ++i) shared_o[wave][i][lane] = o[i];
+        if (lane == 0) {
+            shared_ml[wave][0] = m;
+            shared_ml[wave][1] = l;
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int w = 1; w < SPLIT; ++w) m = fmaxf(m, shared_ml[w][0]);
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < SPLIT; ++w) {
+            const float f = __builtin_amdgcn_exp2f((shared_ml[w][0] - m) * c);
+            l = fmaf(shared_ml[w][1], f, l);
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = fmaf(shared_o[w][i][lane], f, o[i]);
+        }
+    }
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     uint16_t* out = a.out + (long)(shape.first + row / a.heads) * a.o_stride_t + (row % a.heads) * a.o_stride_h + lane * V;
 #pragma unroll
@@ -598,16 +629,25 @@ LatentCut latent_cut(int B, int max_q, int heads, int max_len) {
     return c;
 }
 
+// Up to this many rows get a workgroup each in the join, so that more of the
+// chip reads the sums: one sequence of 16384 rows 54 to 33 us (64 heads),
+// four tokens of it 37 to 35; at 8 sequences of 4096 a wave per row is
+// better, 30 against 32.
+constexpr long kFewRows = 256;
+
 template <int RANK, int RG>
 void launch_rows(LatentArgs a, const LatentCut& cut, hipStream_t s) {
     a.group = cut.group;
     a.runs = cut.runs;
     a.per_seq = a.cu_q ? 0 : a.T / a.B;
     const int grid = (cut.runs + 7) / 8 * 8 * cut.group;
-    hipLaunchKernelGGL((latent_attention_kernel<RANK, RG>), dim3(grid), dim3(RG * 128), 0, s, a);
+    hipLaunchKernelGGL((latent_attention_kernel<RANK, RG>), dim3(grid), dim3(RG * 256), 0, s, a);
     if (cut.runs > 1) {
         const int rows = a.max_q * a.heads;
-        hipLaunchKernelGGL((latent_join_kernel<RANK, RG * 32>), dim3((rows + 3) / 4, a.B), dim3(256), 0, s, a);
+        if ((long)rows * a.B <= kFewRows)
+            hipLaunchKernelGGL((latent_join_kernel<RANK, RG * 32, 4>), dim3(rows, a.B), dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((latent_join_kernel<RANK, RG * 32, 1>), dim3((rows + 3) / 4, a.B), dim3(256), 0, s, a);
     }
 }
 template <int RANK>
