@@ -11,8 +11,10 @@ layers of a model with latent attention, as calls on torch tensors.
 
 Every step runs in the HIP kernels behind include/moe.h; this module checks
 shapes and types, allocates outputs where none are given, and passes pointers
-and strides.  Calls run on torch's current stream unless `stream` is given,
-return at once, and can be captured in a graph.  There is no CPU fallback.
+and strides.  Calls run on torch's current stream, or on `stream` as if under
+torch.cuda.stream(stream) (outputs and workspaces belong to it, and it has to
+be behind whatever makes the inputs), return at once, and can be captured in a
+graph.  There is no CPU fallback.
 """
 from __future__ import annotations
 
@@ -49,11 +51,25 @@ class AppendOut(NamedTuple):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(t: torch.Tensor, stream):
-    """Handle of `stream`, or of the current stream of t's device."""
-    if stream is None:
-        return _raw_stream(t.device.index) if _raw_stream is not None else torch.cuda.current_stream(t.device).cuda_stream
-    return B._stream_handle(stream)
+def _stream(t: torch.Tensor):
+    """Handle of the current stream of t's device."""
+    return _raw_stream(t.device.index) if _raw_stream is not None else torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _elsewhere(stream, f, *args):
+    """f(*args) on `stream` (torch's, or a handle): what it allocates belongs
+    to that stream, and memory of the inputs is not used again before a stream
+    of torch's has passed the call (a handle's owner sees to that)."""
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            out = f(*args)
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+        return out
+    handle = B._stream_handle(stream)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
+        return f(*args)
 
 
 def _need(ok: bool, what: str) -> None:
@@ -92,6 +108,8 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, out: str = "bf16", 
     "fp8" (codes and one scale per 128 columns) or "both".  h is returned in
     the residual's type (sum_out, which may be the residual itself, receives
     it in place; want_sum=False leaves it out)."""
+    if stream is not None:
+        return _elsewhere(stream, add_rmsnorm, x, weight, eps, residual, out, sum_out, want_sum)
     shape, strides = _rows(x, "x", 2, _WIDE)
     T, H = shape
     weight_p, w_type = None, 0
@@ -128,7 +146,7 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, out: str = "bf16", 
         q_p, scale_p = q.data_ptr(), scale.data_ptr()
     B.check(B.lib().moe_add_rmsnorm(x.data_ptr(), x_type, strides[0] if T > 1 else H, residual_p, r_type, r_stride,
                                     weight_p, w_type, T, H, eps, sum_p, s_stride, y_p, H, q_p, pad,
-                                    scale_p, 1, T, _stream(x, stream)))
+                                    scale_p, 1, T, _stream(x)))
     return NormOut(sum_out, y, q, scale)
 
 
@@ -155,6 +173,8 @@ def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -
     w [N, K] 8-bit with w_scale [ceil(N / 128), ceil(K / 128)]: [M, N] in
     out_dtype (bf16 or fp32).  K is a multiple of 16; a_scale may have any
     strides (add_rmsnorm's are the fastest)."""
+    if stream is not None:
+        return _elsewhere(stream, fp8_linear, a, a_scale, w, w_scale, out_dtype, out)
     (M, K), a_strides = _rows(a, "a", 2, _FP8_ONLY)
     (N, wk), w_strides = _rows(w, "w", 2, _FP8_ONLY)
     ws_shape, ws_strides = _rows(w_scale, "w_scale", 2, _F32_ONLY)
@@ -174,7 +194,7 @@ def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -
     B.check(B.lib().moe_fp8_linear(a.data_ptr(), a_strides[0] if M > 1 else pad, a_scale.data_ptr(), as_strides[0],
                                    as_strides[1], w.data_ptr(), w_strides[0] if N > 1 else pad, w_scale.data_ptr(),
                                    ws_strides[0] if nb > 1 else kb, M, N, K, out.data_ptr(), _TYPES[out_dtype], o_stride,
-                                   _stream(a, stream)))
+                                   _stream(a)))
     return out
 
 
@@ -182,6 +202,8 @@ def head_linear(x, w, out=None, stream=None) -> torch.Tensor:
     """x [T, heads, K] times the transpose of w [heads, N, K], head by head:
     [T, heads, N], all bf16.  x and out may be strided views (of a wider
     query, say)."""
+    if stream is not None:
+        return _elsewhere(stream, head_linear, x, w, out)
     (T, heads, K), xs = _rows(x, "x", 3, _BF16_ONLY)
     w_shape, _ = _rows(w, "w", 3, _BF16_ONLY)
     N = w_shape[1]
@@ -193,7 +215,7 @@ def head_linear(x, w, out=None, stream=None) -> torch.Tensor:
         o_shape, os = _rows(out, "out", 3, _BF16_ONLY)
         _need(tuple(o_shape) == (T, heads, N), f"out {tuple(o_shape)}, {(T, heads, N)} is needed")
     B.check(B.lib().moe_head_linear(x.data_ptr(), xs[0], xs[1], w.data_ptr(), T, heads, K, N, out.data_ptr(), os[0], os[1],
-                                    _stream(x, stream)))
+                                    _stream(x)))
     return out
 
 
@@ -208,6 +230,9 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
     page_size, rank + rope] contiguous.  q_rope [T, heads, rope] is rotated
     into q_out (given, the view itself for in place, or new).  want_fp8: the
     normed latent in 8 bits too; want_key: the rotated key part too."""
+    if stream is not None:
+        return _elsewhere(stream, latent_append, kv, weight, eps, table, positions, slots, cache, q_rope, q_out,
+                          want_fp8, want_key)
     (T, width), kvs = _rows(kv, "kv", 2, _BF16_ONLY)
     (rank,), _ = _rows(weight, "weight", 1, _WIDE)
     (n_positions, rope), _ = _rows(table, "table", 2, _F32_ONLY)
@@ -246,7 +271,7 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
     B.check(B.lib().moe_latent_append(
         kv.data_ptr(), kvs[0] if T > 1 else width, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
         table.data_ptr(), n_positions, positions.data_ptr(), slots_p, T, cache_p, n_slots, qp, heads, qs[0], qs[1],
-        qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, rows_p, width, _stream(kv, stream)))
+        qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, rows_p, width, _stream(kv)))
     return AppendOut(q_out if q_rope is not None else None, q, scale, rows[:, rank:] if want_key else None, rows)
 
 
@@ -264,6 +289,9 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     the sequence's j-th new token, itself included if set).  Returns
     [T, heads, rank] bf16.  workspace: uint8 of
     moe_latent_attention_workspace() bytes (allocated per call if None)."""
+    if stream is not None:
+        return _elsewhere(stream, latent_attention, q, cache, pages, lens, scale, max_len, cu_q, max_q, tree, out,
+                          workspace)
     (T, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY)
     (n_pages, page_size, c_width), cs = _rows(cache, "cache", 3, _BF16_ONLY)
     (nb, per_seq), ps = _rows(pages, "pages", 2, _I32_ONLY)
@@ -301,7 +329,7 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
         q.data_ptr(), qs[0], qs[1], T, heads, rank, rope, cache.data_ptr(), n_pages, page_size,
         cs[0] if n_pages > 1 else page_size * width, pages.data_ptr(), ps[0] if nb > 1 else per_seq, per_seq,
         lens.data_ptr(), nb, cu_p, max_q, max_len, tree_p, scale, out.data_ptr(), os[0], os[1], workspace.data_ptr(), n,
-        _stream(q, stream)))
+        _stream(q)))
     return out
 
 
@@ -315,6 +343,8 @@ def prompt_attention(q, k, k_rope, v, scale: float, cu_q=None, cu_k=None, max_q:
     cu_k[b] .. cu_k[b + 1] (int32 [B + 1]; None: one sequence); its queries
     are its last positions.  max_q bounds the queries of a sequence; max_k is
     not needed.  Returns [Tq, heads, vdim] bf16."""
+    if stream is not None:
+        return _elsewhere(stream, prompt_attention, q, k, k_rope, v, scale, cu_q, cu_k, max_q, max_k, causal, out)
     (Tq, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY)
     (Tk, k_heads, nope), ks = _rows(k, "k", 3, _BF16_ONLY)
     (r_rows, rope), rs = _rows(k_rope, "k_rope", 2, _BF16_ONLY)
@@ -324,8 +354,8 @@ def prompt_attention(q, k, k_rope, v, scale: float, cu_q=None, cu_k=None, max_q:
                      "together")
     _need((cu_q is None) == (cu_k is None), "cu_q and cu_k go together")
     if cu_q is None:
-        cu_q = torch.tensor([0, Tq], dtype=torch.int32, device=q.device)
-        cu_k = torch.tensor([0, Tk], dtype=torch.int32, device=q.device)
+        ends = torch.arange(2, dtype=torch.int32, device=q.device)
+        cu_q, cu_k = ends * Tq, ends * Tk
         max_q = Tq
     (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY)
     (n_k,), _ = _rows(cu_k, "cu_k", 1, _I32_ONLY)
@@ -338,5 +368,5 @@ def prompt_attention(q, k, k_rope, v, scale: float, cu_q=None, cu_k=None, max_q:
     B.check(B.lib().moe_prompt_attention(
         q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], k_rope.data_ptr(), rs[0], v.data_ptr(), vs[0], vs[1], Tq,
         Tk, heads, nope, rope, vdim, cu_q.data_ptr(), cu_k.data_ptr(), n - 1, max_q, int(causal), scale, out.data_ptr(),
-        os[0], os[1], _stream(q, stream)))
+        os[0], os[1], _stream(q)))
     return out

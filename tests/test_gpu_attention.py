@@ -457,6 +457,36 @@ def test_latent_attention_repeats_and_streams():
         assert torch.equal(first, out)
 
 
+def test_calls_on_a_given_stream():
+    # while `stream` is still busy, the current stream gets none of the memory
+    # that a call on it has taken or still reads
+    g = gen(18)
+    q, cache, pages, dl = latent_case(g, [900, 333, 64], [2] * 3, 64, 512, 64)
+    x, w, res = normal(g, 512, 2048), normal(g, 2048), normal(g, 512, 2048)
+    k, v, kr = normal(g, 700, 4, 128), normal(g, 700, 4, 128), normal(g, 700, 64)
+    pq = normal(g, 700, 4, 192)
+    first = A.latent_attention(q, cache, pages, dl, 0.07, max_len=900)
+    norm = A.add_rmsnorm(x, w, residual=res, out="both")
+    prompt = A.prompt_attention(pq, k, kr, v, 0.07)
+    busy = normal(g, 4096, 4096)
+    torch.cuda.synchronize()
+    for as_handle in (False, True):
+        side = torch.cuda.Stream()
+        stream = side.cuda_stream if as_handle else side
+        with torch.cuda.stream(side):
+            for _ in range(50):
+                busy @ busy
+        got = A.latent_attention(q, cache, pages, dl, 0.07, max_len=900, stream=stream)
+        got_norm = A.add_rmsnorm(x, w, residual=res, out="both", stream=stream)
+        got_prompt = A.prompt_attention(pq, k, kr, v, 0.07, stream=stream)
+        size = B.lib().moe_latent_attention_workspace(3, 2, 64, 512, 900)
+        mine = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(bool((m == 7).all()) for m in mine)
+        assert torch.equal(got, first) and torch.equal(got_prompt, prompt)
+        assert all(torch.equal(a.float(), b.float()) for a, b in zip(got_norm, norm))
+
+
 # ---------------------------------------------------------------- expanded attention
 def prompt_ref(q, k, kr, v, nq, nk, scale, causal=True):
     out, mag = [], []
