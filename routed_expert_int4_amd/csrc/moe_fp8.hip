@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(256) fp8_short_kernel(Fp8Args a) {
 }
 
 // ---------------------------------------------------------------- few tokens
-// Bound by reading the weights once.  A workgroup owns NT x 16 rows of W and
+// Bound by reading the weights once, and by latency (1 x 576 x 6144: 6.0 us
+// for 3.5 MB).  A workgroup owns NT x 16 rows of W and
 // TT x 16 tokens; its eight waves take the blocks of the inner dimension in
 // turn, straight from global memory in operand order, and their sums are
 // joined through LDS in wave order.
@@ -145,7 +146,9 @@ __global__ void __launch_bounds__(512) fp8_rows_kernel(Fp8Args a) {
 }
 
 // --------------------------------------------------------------- many tokens
-// Bound by the matrix cores.  WN x WT waves, each NT x TT instruction tiles;
+// Bound by the issue of matrix instructions and the scaling between them:
+// 4096 x 6144 x 8192 takes 205 us, 2.0 PFLOP/s (a library product of that
+// shape without block scales 2.3; matrix cores 39 % busy).  WN x WT waves, each NT x TT instruction tiles;
 // both operands of one block of 128 columns go through LDS, loaded
 // asynchronously two blocks ahead into a ring of three buffers, with the
 // activation scales of each wave's tokens beside them (so that the loop's

@@ -21,7 +21,8 @@ __device__ __forceinline__ bf16x8 row_chunk(const uint16_t* row, int k, int K) {
     return __builtin_bit_cast(bf16x8, u);
 }
 
-// A wave owns NT x TT tiles of 16 n by 16 tokens; the four waves of a
+// Few tokens: one token, 64 heads, 128 to 512 takes 3.6 us, of which reading
+// 8.4 MB of weights is 1.8.  A wave owns NT x TT tiles of 16 n by 16 tokens; the four waves of a
 // workgroup lie along n.
 template <int NT, int TT>
 __global__ void __launch_bounds__(256) head_linear_kernel(HeadArgs a) {
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(256) head_linear_kernel(HeadArgs a) {
 // two LDS buffers: token rows lie heads * K apart in memory, and 64 KB in
 // flight per CU are what reading them takes (1024 tokens x 64 heads, 512 to
 // 128: through registers 50 us, 64 tokens per workgroup with the weights read
-// again for each 38 us).  The 16-byte chunk c of row r sits at place
+// again for each 38 us; so 20.5, 4.5 TB/s).  The 16-byte chunk c of row r sits at place
 // c ^ (r & 15): the 16 rows of an operand read cover all banks.  Row m of
 // instruction tile i is n = m / 4 * 4 NW + 4 i + m % 4, so that a lane holds
 // 4 NW neighbouring outputs of one token.
