@@ -83,25 +83,40 @@ class LatentCache:
         self._lists = [[] for _ in range(max_seqs)]
         self._free = list(range(n_pages))[::-1]
 
+    def _slot(self, b: int, p: int) -> int:
+        """Cache row of place p of sequence b."""
+        return self._lists[b][p // self.cfg.page] * self.cfg.page + p % self.cfg.page
+
+    def _check(self, counts) -> None:
+        """Refuses counts that extend() could not place."""
+        if len(counts) > len(self.host_lens):
+            raise ValueError(f"{len(counts)} sequences, the cache holds {len(self.host_lens)}")
+        pages = 0
+        for b, n in enumerate(counts):
+            rows = self.host_lens[b] + n
+            if n < 0 or rows > self.max_len:
+                raise ValueError(f"sequence {b}: {n} new rows after {self.host_lens[b]}, the cache holds {self.max_len} per "
+                                 "sequence")
+            pages += -(-rows // self.cfg.page) - len(self._lists[b])
+        if pages > len(self._free):
+            raise ValueError(f"{pages} more pages are needed, the latent cache has {len(self._free)} free ones")
+
     def extend(self, counts):
         """Makes room for counts[b] new rows of sequence b.  Returns their
-        positions (int32) and cache rows (int64), sequence after sequence."""
-        cfg, positions, slots = self.cfg, [], []
+        positions (int32) and cache rows (int64), sequence after sequence.
+        What does not fit is refused as a whole: nothing has changed then."""
+        self._check(counts)
+        positions, slots, dev = [], [], self.pool.device
         for b, n in enumerate(counts):
-            have = self.host_lens[b]
-            if have + n > self.max_len:
-                raise ValueError(f"sequence {b}: {have + n} rows, the cache holds {self.max_len} per sequence")
-            while len(self._lists[b]) * cfg.page < have + n:
-                if not self._free:
-                    raise ValueError("the latent cache has no free page")
-                self._lists[b].append(self._free.pop())
+            have, pages = self.host_lens[b], self._lists[b]
+            held = len(pages)
+            while len(pages) * self.cfg.page < have + n:
+                pages.append(self._free.pop())
+            if len(pages) > held:
+                self.pages[b, held:len(pages)] = torch.tensor(pages[held:], dtype=torch.int32)
             positions += range(have, have + n)
-            slots += [self._lists[b][p // cfg.page] * cfg.page + p % cfg.page for p in range(have, have + n)]
+            slots += [self._slot(b, p) for p in range(have, have + n)]
             self.host_lens[b] = have + n
-        dev = self.pool.device
-        for b, pages in enumerate(self._lists):
-            if pages:
-                self.pages[b, :len(pages)] = torch.tensor(pages, dtype=torch.int32)
         self.lens.copy_(torch.tensor(self.host_lens, dtype=torch.int32))
         return (torch.tensor(positions, dtype=torch.int32).to(dev), torch.tensor(slots, dtype=torch.int64).to(dev))
 
