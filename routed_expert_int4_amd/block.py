@@ -23,6 +23,7 @@ stream and the MoE output go from block to block.
 """
 from __future__ import annotations
 
+from contextlib import contextmanager
 from dataclasses import dataclass
 
 import torch
@@ -120,6 +121,27 @@ class LatentCache:
         self.lens.copy_(torch.tensor(self.host_lens, dtype=torch.int32))
         return (torch.tensor(positions, dtype=torch.int32).to(dev), torch.tensor(slots, dtype=torch.int64).to(dev))
 
+    def _cut(self, lens) -> None:
+        """Keeps the first lens[b] rows of sequence b and frees the pages after them."""
+        for b, n in enumerate(lens):
+            keep = -(-n // self.cfg.page)
+            self._free += self._lists[b][keep:][::-1]
+            del self._lists[b][keep:]
+            self.host_lens[b] = n
+        self.lens.copy_(torch.tensor(self.host_lens, dtype=torch.int32))
+
+    @contextmanager
+    def step(self, counts):
+        """extend() around the calls that fill the rows: if one of them is
+        refused, the rows are taken back."""
+        before = list(self.host_lens)
+        rows = self.extend(counts)
+        try:
+            yield rows
+        except BaseException:
+            self._cut(before)
+            raise
+
 
 class DecoderBlock:
     """The attention half around a DeviceLayer (or None: attention only)."""
@@ -163,32 +185,31 @@ class DecoderBlock:
         """Prompts of counts[b] tokens, one after another in delta and
         residual [T, hidden], for sequences that have no rows yet."""
         cfg = self.cfg
-        if any(n and cache.host_lens[b] for b, n in enumerate(counts)):
+        if any(n and have for n, have in zip(counts, cache.host_lens)):
             raise ValueError("prompt() starts sequences; decode() continues them")
-        positions, slots = cache.extend(counts)
-        h, q, kv = self._queries(delta, residual)
-        new = A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, positions, slots, cache.pool,
-                              q_rope=q[..., cfg.nope:], q_out=q[..., cfg.nope:], want_key=True)
-        latents = new.rows[:, None, :cfg.rank].expand(-1, cfg.heads, -1)  # every head reads the same
-        k, v = A.head_linear(latents, self.w_uk), A.head_linear(latents, self.w_uv)
-        cu = torch.tensor([sum(counts[:b]) for b in range(len(counts) + 1)], dtype=torch.int32).to(q.device)
-        o = A.prompt_attention(q, k, new.key, v, cfg.scale, cu_q=cu, cu_k=cu,
-                               max_q=max(counts))
-        return self._finish(o, h)
+        with cache.step(counts) as (positions, slots):
+            h, q, kv = self._queries(delta, residual)
+            new = A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, positions, slots, cache.pool,
+                                  q_rope=q[..., cfg.nope:], q_out=q[..., cfg.nope:], want_key=True)
+            latents = new.rows[:, None, :cfg.rank].expand(-1, cfg.heads, -1)  # every head reads the same
+            k, v = A.head_linear(latents, self.w_uk), A.head_linear(latents, self.w_uv)
+            cu = torch.tensor([sum(counts[:b]) for b in range(len(counts) + 1)], dtype=torch.int32).to(q.device)
+            o = A.prompt_attention(q, k, new.key, v, cfg.scale, cu_q=cu, cu_k=cu, max_q=max(counts))
+            return self._finish(o, h)
 
     def decode(self, delta, residual, cache: LatentCache, count: int = 1, tree=None, positions=None):
         """`count` new tokens of every sequence: one decoded token, a causal
         chunk, or with tree (int64 masks [T]) drafted tokens, whose positions
         in the text the caller gives (int32 [T]; siblings share one)."""
         cfg = self.cfg
-        running, slots = cache.extend([count] * len(cache.host_lens))
-        h, q, kv = self._queries(delta, residual)
-        ql = torch.empty(q.shape[0], cfg.heads, cfg.rank + cfg.rope, dtype=torch.bfloat16, device=q.device)
-        A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, running if positions is None else positions, slots,
-                        cache.pool, q_rope=q[..., cfg.nope:], q_out=ql[..., cfg.rank:])
-        A.head_linear(q[..., :cfg.nope], self.w_uk_t, out=ql[..., :cfg.rank])
-        o = A.latent_attention(ql, cache.pool, cache.pages, cache.lens, cfg.scale, max_len=max(cache.host_lens), tree=tree)
-        return self._finish(A.head_linear(o, self.w_uv), h)
+        with cache.step([count] * len(cache.host_lens)) as (running, slots):
+            h, q, kv = self._queries(delta, residual)
+            ql = torch.empty(q.shape[0], cfg.heads, cfg.rank + cfg.rope, dtype=torch.bfloat16, device=q.device)
+            A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, running if positions is None else positions,
+                            slots, cache.pool, q_rope=q[..., cfg.nope:], q_out=ql[..., cfg.rank:])
+            A.head_linear(q[..., :cfg.nope], self.w_uk_t, out=ql[..., :cfg.rank])
+            o = A.latent_attention(ql, cache.pool, cache.pages, cache.lens, cfg.scale, max_len=max(cache.host_lens), tree=tree)
+            return self._finish(A.head_linear(o, self.w_uv), h)
 
 
 def main() -> None:

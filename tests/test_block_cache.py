@@ -4,7 +4,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from routed_expert_int4_amd.block import BlockConfig, LatentCache  # noqa: E402
+from routed_expert_int4_amd import binding as B  # noqa: E402
+from routed_expert_int4_amd.block import BlockConfig, DecoderBlock, LatentCache, random_weights  # noqa: E402
 
 CFG = BlockConfig(hidden=256, heads=4, q_rank=128, rank=256, rope=64, nope=64, vdim=64, page=16)
 
@@ -43,3 +44,17 @@ def test_a_refused_extend_changes_nothing(counts):
     assert positions.tolist() == [17]
     assert slots.tolist() == [int(cache.pages[0, 1]) * CFG.page + 1]
     check(cache, [18, 16])
+
+
+def test_a_refused_step_counts_no_rows():
+    # on the CPU every kernel call is refused: after the cache has made room
+    block = DecoderBlock(CFG, random_weights(CFG, 1, device="cpu"), max_positions=64, device="cpu")
+    cache = make()
+    x = torch.zeros(21, CFG.hidden)
+    with pytest.raises(B.MoeError):
+        block.prompt(x, x, cache, [21, 0])
+    check(cache, [0, 0])
+    cache.extend([16, 20])
+    with pytest.raises(B.MoeError):
+        block.decode(x[:2], x[:2], cache)
+    check(cache, [16, 20])

@@ -1,0 +1,61 @@
+"""GPU tests of a decoder block and its cache over several steps
+(routed_expert_int4_amd/block.py): refused steps, drafted tokens, sequences
+that come and go.
+
+Two ways to the same tokens run the same kernels on the same rows and differ
+in the order of sums: outputs are compared by norm, 1 % (a bf16 unit in an
+activation is 2^-8, and an 8-bit code that falls the other way is one value
+of many)."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from routed_expert_int4_amd import binding as B  # noqa: E402
+from routed_expert_int4_amd import synth  # noqa: E402
+from routed_expert_int4_amd.block import BlockConfig, DecoderBlock, LatentCache, random_weights  # noqa: E402
+
+DEV = "cuda:0"
+CFG = BlockConfig(hidden=256, heads=4, q_rank=128, rank=256, rope=64, nope=64, vdim=64, page=16)
+
+
+def near(a, b, tol=0.01):
+    a, b = a.double(), b.double()
+    assert a.shape == b.shape and a.isfinite().all()
+    off = ((a - b).norm() / b.norm()).item()
+    assert off < tol, off
+
+
+def make(moe=None, max_positions=256):
+    return DecoderBlock(CFG, random_weights(CFG, 3), moe, max_positions=max_positions)
+
+
+def cache(seqs=2, n_pages=40, max_len=128):
+    return LatentCache(CFG, n_pages=n_pages, max_seqs=seqs, max_len=max_len)
+
+
+def inputs(T, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randn(T, CFG.hidden, generator=g, device=DEV), torch.randn(T, CFG.hidden, generator=g, device=DEV).bfloat16()
+
+
+def test_a_refused_step_can_be_made_again():
+    from routed_expert_int4_amd.layer import DeviceLayer
+    moe = DeviceLayer(synth.gen_layer(synth.TINY, seed=0), max_T=24)
+    block, used, fresh = make(moe), cache(), cache()
+    delta, residual = inputs(40, 1)
+    tree = torch.ones(3, dtype=torch.int64, device=DEV)
+    with pytest.raises(B.MoeError):
+        block.prompt(delta, residual, used, [40, 0])  # the routed layer holds 24 tokens
+    _, first = block.prompt(delta[:20], residual[:20], used, [20, 0])
+    with pytest.raises(B.MoeError):
+        block.decode(delta[:4], residual[:4], used, 2, tree=tree)  # four tokens, three masks
+    assert used.host_lens == [20, 0] and used.lens.tolist() == [20, 0]
+    _, second = block.decode(delta[20:22], residual[20:22], used)
+    _, want = block.prompt(delta[:20], residual[:20], fresh, [20, 0])
+    near(first, want)
+    _, want = block.decode(delta[20:22], residual[20:22], fresh)
+    near(second, want)
+    moe.close()
