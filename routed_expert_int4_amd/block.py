@@ -81,6 +81,7 @@ class LatentCache:
         self.pages = torch.full((max_seqs, -(-max_len // cfg.page)), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=device)
         self.host_lens = [0] * max_seqs
+        self._drafted = [0] * max_seqs  # rows at the end of a sequence that accept() has to decide on
         self._lists = [[] for _ in range(max_seqs)]
         self._free = list(range(n_pages))[::-1]
 
@@ -95,6 +96,8 @@ class LatentCache:
         pages = 0
         for b, n in enumerate(counts):
             rows = self.host_lens[b] + n
+            if n and self._drafted[b]:
+                raise ValueError(f"sequence {b} ends with {self._drafted[b]} drafted tokens: accept() some of them first")
             if n < 0 or rows > self.max_len:
                 raise ValueError(f"sequence {b}: {n} new rows after {self.host_lens[b]}, the cache holds {self.max_len} per "
                                  "sequence")
@@ -102,10 +105,12 @@ class LatentCache:
         if pages > len(self._free):
             raise ValueError(f"{pages} more pages are needed, the latent cache has {len(self._free)} free ones")
 
-    def extend(self, counts):
+    def extend(self, counts, drafted: bool = False):
         """Makes room for counts[b] new rows of sequence b.  Returns their
         positions (int32) and cache rows (int64), sequence after sequence.
-        What does not fit is refused as a whole: nothing has changed then."""
+        What does not fit is refused as a whole: nothing has changed then.
+        drafted: the rows are drafts, on which accept() decides before their
+        sequences go on."""
         self._check(counts)
         positions, slots, dev = [], [], self.pool.device
         for b, n in enumerate(counts):
@@ -118,6 +123,8 @@ class LatentCache:
             positions += range(have, have + n)
             slots += [self._slot(b, p) for p in range(have, have + n)]
             self.host_lens[b] = have + n
+            if drafted:
+                self._drafted[b] += n
         self.lens.copy_(torch.tensor(self.host_lens, dtype=torch.int32))
         return (torch.tensor(positions, dtype=torch.int32).to(dev), torch.tensor(slots, dtype=torch.int64).to(dev))
 
@@ -131,16 +138,50 @@ class LatentCache:
         self.lens.copy_(torch.tensor(self.host_lens, dtype=torch.int32))
 
     @contextmanager
-    def step(self, counts):
+    def step(self, counts, drafted: bool = False):
         """extend() around the calls that fill the rows: if one of them is
         refused, the rows are taken back."""
-        before = list(self.host_lens)
-        rows = self.extend(counts)
+        before, drafts = list(self.host_lens), list(self._drafted)
+        rows = self.extend(counts, drafted)
         try:
             yield rows
         except BaseException:
             self._cut(before)
+            self._drafted = drafts
             raise
+
+    def accept(self, kept) -> None:
+        """Ends a step of drafted tokens.  kept[b] names those of sequence b's
+        drafts that stay (0 the first; a branch is all of its tokens from the
+        root on): their rows move together behind the context, all others go,
+        and their pages are free again.  A sequence past the end of kept keeps
+        none."""
+        kept = [list(k) for k in kept] + [[]] * (len(self.host_lens) - len(kept))
+        if len(kept) > len(self.host_lens):
+            raise ValueError(f"{len(kept)} sequences, the cache holds {len(self.host_lens)}")
+        lens, moved = [], []
+        for b, keep in enumerate(kept):
+            if len(set(keep)) < len(keep) or any(not 0 <= j < self._drafted[b] for j in keep):
+                raise ValueError(f"sequence {b}: {keep} of {self._drafted[b]} drafted tokens")
+            first = self.host_lens[b] - self._drafted[b]
+            moved += [(self._slot(b, first + i), self._slot(b, first + j)) for i, j in enumerate(keep) if i != j]
+            lens.append(first + len(keep))
+        if moved:
+            to, source = torch.tensor(moved, dtype=torch.int64).t().contiguous().to(self.pool.device)
+            rows = self.pool.view(-1, self.pool.shape[2])
+            rows[to] = rows[source]  # read whole before the first is written
+        self._cut(lens)
+        self._drafted = [0] * len(lens)
+
+    def truncate(self, b: int, length: int = 0) -> None:
+        """Shortens sequence b to its first `length` rows (0 ends it); what
+        is left counts as accepted, and pages no longer needed are free."""
+        if not 0 <= length <= self.host_lens[b]:
+            raise ValueError(f"sequence {b}: {length} of {self.host_lens[b]} rows")
+        lens = list(self.host_lens)
+        lens[b] = length
+        self._cut(lens)
+        self._drafted[b] = 0
 
 
 class DecoderBlock:
@@ -200,9 +241,11 @@ class DecoderBlock:
     def decode(self, delta, residual, cache: LatentCache, count: int = 1, tree=None, positions=None):
         """`count` new tokens of every sequence: one decoded token, a causal
         chunk, or with tree (int64 masks [T]) drafted tokens, whose positions
-        in the text the caller gives (int32 [T]; siblings share one)."""
+        in the text the caller gives (int32 [T]; siblings share one).  After
+        drafted tokens cache.accept() says which of them stay; until then
+        their sequences do not go on."""
         cfg = self.cfg
-        with cache.step([count] * len(cache.host_lens)) as (running, slots):
+        with cache.step([count] * len(cache.host_lens), drafted=tree is not None) as (running, slots):
             h, q, kv = self._queries(delta, residual)
             ql = torch.empty(q.shape[0], cfg.heads, cfg.rank + cfg.rope, dtype=torch.bfloat16, device=q.device)
             A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, running if positions is None else positions,
@@ -239,13 +282,14 @@ def main() -> None:
     x, r = inputs(8)
     timed("one token for each of 8 sequences, attention half", lambda: block.decode(x, r, cache), 20)
     x4, r4 = inputs(32)
-    tree = torch.tensor([1, 3, 5, 11] * 8, dtype=torch.int64, device="cuda:0")  # two branches
+    tree = torch.tensor([1, 3, 5, 11] * 8, dtype=torch.int64, device="cuda:0")  # branches 0 1 3 and 0 2
 
     def verify():
         at = torch.tensor([n + d for n in cache.host_lens for d in (0, 1, 1, 2)], dtype=torch.int32).to("cuda:0")
         block.decode(x4, r4, cache, 4, tree=tree, positions=at)
+        cache.accept([[0, 2]] * 8)
 
-    timed("a tree of 4 drafted tokens for each, attention half", verify, 20)
+    timed("a tree of 4 drafted tokens for each, two of them accepted, attention half", verify, 20)
 
 
 if __name__ == "__main__":

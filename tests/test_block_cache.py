@@ -58,3 +58,79 @@ def test_a_refused_step_counts_no_rows():
     with pytest.raises(B.MoeError):
         block.decode(x[:2], x[:2], cache)
     check(cache, [16, 20])
+
+
+def fill(cache, b, n):
+    """Row p of sequence b holds 100 b + p."""
+    for p in range(n):
+        page = int(cache.pages[b, p // CFG.page])
+        cache.pool[page, p % CFG.page] = 100 * b + p
+
+
+def rows(cache, b):
+    return [int(cache.pool[int(cache.pages[b, p // CFG.page]), p % CFG.page, -1]) for p in range(cache.host_lens[b])]
+
+
+@pytest.mark.parametrize("kept", [[], [0], [0, 1], [0, 2, 3], [3, 1], [0, 1, 2, 3]])
+def test_accepted_drafts_move_together(kept):
+    cache = make(n_pages=5)
+    cache.extend([14, 3])
+    cache.extend([4, 1], drafted=True)  # over the end of a page
+    fill(cache, 0, 18)
+    fill(cache, 1, 4)
+    with pytest.raises(ValueError):
+        cache.extend([1, 0])
+    with pytest.raises(ValueError):
+        cache.extend([0, 1])
+    check(cache, [18, 4])
+    cache.accept([kept, [0]])
+    check(cache, [14 + len(kept), 4])
+    assert rows(cache, 0) == [*range(14), *(14 + j for j in kept)] and rows(cache, 1) == [100, 101, 102, 103]
+    positions, _ = cache.extend([1, 1])
+    assert positions.tolist() == [14 + len(kept), 4]
+
+
+def test_accept_refuses_what_was_not_drafted():
+    cache = make()
+    cache.extend([10, 5])
+    cache.extend([3, 0], drafted=True)
+    fill(cache, 0, 13)
+    for kept in ([[3]], [[-1]], [[0, 0]], [[0], [0]], [[0], [], []]):
+        with pytest.raises(ValueError):
+            cache.accept(kept)
+        check(cache, [13, 5])
+    cache.extend([0, 2])  # a sequence without drafts goes on
+    check(cache, [13, 7])
+    cache.accept([[0, 1]])
+    check(cache, [12, 7])
+    with pytest.raises(ValueError):
+        cache.accept([[0]])  # decided already
+
+
+def test_truncate_frees_pages():
+    cache = make(n_pages=4)
+    cache.extend([33, 16])
+    with pytest.raises(ValueError):
+        cache.truncate(0, 34)
+    with pytest.raises(ValueError):
+        cache.truncate(0, -1)
+    cache.truncate(0, 17)
+    check(cache, [17, 16])
+    cache.extend([2, 0], drafted=True)
+    cache.truncate(0, 18)
+    check(cache, [18, 16])
+    cache.truncate(0)
+    check(cache, [0, 16])
+    cache.extend([48, 0])
+    check(cache, [48, 16])
+
+
+def test_a_refused_step_leaves_no_drafts():
+    cache = make()
+    cache.extend([5, 5])
+    with pytest.raises(RuntimeError):
+        with cache.step([3, 3], drafted=True):
+            raise RuntimeError
+    check(cache, [5, 5])
+    cache.extend([1, 1])
+    check(cache, [6, 6])

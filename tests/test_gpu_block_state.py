@@ -59,3 +59,31 @@ def test_a_refused_step_can_be_made_again():
     _, want = block.decode(delta[20:22], residual[20:22], fresh)
     near(second, want)
     moe.close()
+
+
+@pytest.mark.parametrize("branch,depths", [([0, 1], [0, 1, 1, 2]), ([0, 2, 3], [0, 1, 1, 2])])
+def test_decoding_goes_on_from_an_accepted_branch(branch, depths):
+    """A prompt, a tree, one branch accepted, and on: as if only that branch
+    had ever been decoded."""
+    block = make()
+    delta, residual = inputs(60, 5)
+    # draft tokens a, b (after a), c (after a), d (after c)
+    tree = torch.tensor([0b1, 0b11, 0b101, 0b1101] * 2, dtype=torch.int64, device=DEV)
+    drafted, alone = cache(), cache()
+    for used in (drafted, alone):
+        block.prompt(delta[:45], residual[:45], used, [30, 15])
+    at = torch.tensor([first + d for first in (30, 15) for d in depths], dtype=torch.int32, device=DEV)
+    rows = slice(45, 49)
+    both = [torch.cat([t[rows], t[rows]]) for t in (delta, residual)]
+    block.decode(*both, drafted, 4, tree=tree, positions=at)
+    with pytest.raises(ValueError):
+        block.decode(delta[:2], residual[:2], drafted)
+    drafted.accept([branch, branch])
+    for j in branch:
+        block.decode(delta[[45 + j] * 2], residual[[45 + j] * 2], alone)
+    assert drafted.host_lens == alone.host_lens and torch.equal(drafted.lens, alone.lens)
+    for i in range(3):
+        step = [50 + 2 * i, 51 + 2 * i]
+        _, out = block.decode(delta[step], residual[step], drafted)
+        _, want = block.decode(delta[step], residual[step], alone)
+        near(out, want)
