@@ -222,12 +222,18 @@ class DecoderBlock:
         n = A.add_rmsnorm(delta, self.norms["norm_moe"], self.cfg.eps, residual=h, out="bf16", sum_out=h)
         return h, self.moe.forward(n.y)[0]
 
+    def _known(self, last: int) -> None:
+        """Refuses text positions that the table of angles does not hold."""
+        if last >= self.table.shape[0]:
+            raise ValueError(f"position {last}: the block has a table of {self.table.shape[0]} (max_positions)")
+
     def prompt(self, delta, residual, cache: LatentCache, counts):
         """Prompts of counts[b] tokens, one after another in delta and
         residual [T, hidden], for sequences that have no rows yet."""
         cfg = self.cfg
         if any(n and have for n, have in zip(counts, cache.host_lens)):
             raise ValueError("prompt() starts sequences; decode() continues them")
+        self._known(max(counts, default=0) - 1)
         with cache.step(counts) as (positions, slots):
             h, q, kv = self._queries(delta, residual)
             new = A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, positions, slots, cache.pool,
@@ -241,10 +247,18 @@ class DecoderBlock:
     def decode(self, delta, residual, cache: LatentCache, count: int = 1, tree=None, positions=None):
         """`count` new tokens of every sequence: one decoded token, a causal
         chunk, or with tree (int64 masks [T]) drafted tokens, whose positions
-        in the text the caller gives (int32 [T]; siblings share one).  After
-        drafted tokens cache.accept() says which of them stay; until then
-        their sequences do not go on."""
+        in the text the caller gives (a list, or int32 [T] on the device, which
+        is not looked at here: a position outside the table makes NaN of its
+        token; siblings share one).  After drafted tokens cache.accept() says
+        which of them stay; until then their sequences do not go on."""
         cfg = self.cfg
+        if positions is None:
+            self._known(max(cache.host_lens) + count - 1)
+        elif not isinstance(positions, torch.Tensor):
+            if min(positions, default=0) < 0:
+                raise ValueError(f"position {min(positions)}")
+            self._known(max(positions, default=0))
+            positions = torch.tensor(positions, dtype=torch.int32).to(self.table.device)
         with cache.step([count] * len(cache.host_lens), drafted=tree is not None) as (running, slots):
             h, q, kv = self._queries(delta, residual)
             ql = torch.empty(q.shape[0], cfg.heads, cfg.rank + cfg.rope, dtype=torch.bfloat16, device=q.device)
@@ -285,7 +299,7 @@ def main() -> None:
     tree = torch.tensor([1, 3, 5, 11] * 8, dtype=torch.int64, device="cuda:0")  # branches 0 1 3 and 0 2
 
     def verify():
-        at = torch.tensor([n + d for n in cache.host_lens for d in (0, 1, 1, 2)], dtype=torch.int32).to("cuda:0")
+        at = [n + d for n in cache.host_lens for d in (0, 1, 1, 2)]
         block.decode(x4, r4, cache, 4, tree=tree, positions=at)
         cache.accept([[0, 2]] * 8)
 

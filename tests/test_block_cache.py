@@ -134,3 +134,20 @@ def test_a_refused_step_leaves_no_drafts():
     check(cache, [5, 5])
     cache.extend([1, 1])
     check(cache, [6, 6])
+
+
+def test_positions_past_the_table_are_refused():
+    # the refusal comes before the cache changes and before any kernel (which there is none of on the CPU)
+    block = DecoderBlock(CFG, random_weights(CFG, 1, device="cpu"), max_positions=20, device="cpu")
+    cache = make()
+    x = torch.zeros(8, CFG.hidden)
+    with pytest.raises(ValueError):
+        block.prompt(x, x, cache, [21, 0])
+    cache.extend([20, 18])
+    for tokens in (1, 3):
+        with pytest.raises(ValueError):
+            block.decode(x[:2 * tokens], x[:2 * tokens], cache, tokens)
+    for at in ([19, 20], [-1, 3]):
+        with pytest.raises(ValueError):
+            block.decode(x[:2], x[:2], cache, 1, tree=torch.ones(2, dtype=torch.int64), positions=at)
+    check(cache, [20, 18])

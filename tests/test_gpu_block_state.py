@@ -87,3 +87,20 @@ def test_decoding_goes_on_from_an_accepted_branch(branch, depths):
         _, out = block.decode(delta[step], residual[step], drafted)
         _, want = block.decode(delta[step], residual[step], alone)
         near(out, want)
+
+
+def test_the_last_known_position():
+    block, used = make(max_positions=24), cache(seqs=1)
+    delta, residual = inputs(30, 6)
+    block.prompt(delta[:23], residual[:23], used, [23])
+    _, out = block.decode(delta[23:24], residual[23:24], used)
+    assert out.isfinite().all()
+    with pytest.raises(ValueError):
+        block.decode(delta[24:25], residual[24:25], used)
+    used.truncate(0, 21)
+    tree = torch.tensor([1, 3, 5, 11], dtype=torch.int64, device=DEV)
+    _, lists = block.decode(delta[21:25], residual[21:25], used, 4, tree=tree, positions=[21, 22, 22, 23])
+    used.truncate(0, 21)
+    at = torch.tensor([21, 22, 22, 23], dtype=torch.int32, device=DEV)
+    _, tensors = block.decode(delta[21:25], residual[21:25], used, 4, tree=tree, positions=at)
+    assert torch.equal(lists, tensors) and lists.isfinite().all()
