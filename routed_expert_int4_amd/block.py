@@ -25,6 +25,7 @@ from __future__ import annotations
 
 from contextlib import contextmanager
 from dataclasses import dataclass
+from itertools import accumulate
 
 import torch
 
@@ -216,7 +217,7 @@ class DecoderBlock:
     def _finish(self, o, h):
         """Output projection, second norm and the MoE layer: the residual and
         the next delta."""
-        delta = self._linear(A.quantize(o.reshape(o.shape[0], -1)), "o")
+        delta = self._linear(A.quantize(o.flatten(1)), "o")
         if self.moe is None:
             return h, delta
         n = A.add_rmsnorm(delta, self.norms["norm_moe"], self.cfg.eps, residual=h, out="bf16", sum_out=h)
@@ -226,6 +227,10 @@ class DecoderBlock:
         """Refuses text positions that the table of angles does not hold."""
         if last >= self.table.shape[0]:
             raise ValueError(f"position {last}: the block has a table of {self.table.shape[0]} (max_positions)")
+
+    def _starts(self, counts):
+        """Where each sequence's tokens start, and the last one's end."""
+        return torch.tensor([0, *accumulate(counts)], dtype=torch.int32).to(self.table.device)
 
     def prompt(self, delta, residual, cache: LatentCache, counts):
         """Prompts of counts[b] tokens, one after another in delta and
@@ -240,32 +245,41 @@ class DecoderBlock:
                                   q_rope=q[..., cfg.nope:], q_out=q[..., cfg.nope:], want_key=True)
             latents = new.rows[:, None, :cfg.rank].expand(-1, cfg.heads, -1)  # every head reads the same
             k, v = A.head_linear(latents, self.w_uk), A.head_linear(latents, self.w_uv)
-            cu = torch.tensor([sum(counts[:b]) for b in range(len(counts) + 1)], dtype=torch.int32).to(q.device)
+            cu = self._starts(counts)
             o = A.prompt_attention(q, k, new.key, v, cfg.scale, cu_q=cu, cu_k=cu, max_q=max(counts))
             return self._finish(o, h)
 
-    def decode(self, delta, residual, cache: LatentCache, count: int = 1, tree=None, positions=None):
-        """`count` new tokens of every sequence: one decoded token, a causal
-        chunk, or with tree (int64 masks [T]) drafted tokens, whose positions
-        in the text the caller gives (a list, or int32 [T] on the device, which
-        is not looked at here: a position outside the table makes NaN of its
-        token; siblings share one).  After drafted tokens cache.accept() says
-        which of them stay; until then their sequences do not go on."""
-        cfg = self.cfg
+    def decode(self, delta, residual, cache: LatentCache, count=1, tree=None, positions=None):
+        """`count` new tokens of every sequence, or count[b] of sequence b
+        (0: it sits out), one sequence after another in delta and residual
+        [T, hidden]: one decoded token, a causal chunk, or with tree (int64
+        masks [T]) up to 64 drafted tokens, whose positions in the text the
+        caller gives (a list, or int32 [T] on the device, which is not looked
+        at here: a position outside the table makes NaN of its token; siblings
+        share one).  After drafted tokens cache.accept() says which of them
+        stay; until then their sequences do not go on."""
+        cfg, seqs = self.cfg, len(cache.host_lens)
+        counts = [count] * seqs if isinstance(count, int) else [*count, *[0] * (seqs - len(count))]
+        running = [b for b, n in enumerate(counts) if n]
+        most = max(counts)
+        if tree is not None and most > 64:
+            raise ValueError(f"{most} drafted tokens in a sequence: a mask has 64 bits")
         if positions is None:
-            self._known(max(cache.host_lens) + count - 1)
+            self._known(max((have + n - 1 for have, n in zip(cache.host_lens, counts) if n), default=0))
         elif not isinstance(positions, torch.Tensor):
             if min(positions, default=0) < 0:
                 raise ValueError(f"position {min(positions)}")
             self._known(max(positions, default=0))
             positions = torch.tensor(positions, dtype=torch.int32).to(self.table.device)
-        with cache.step([count] * len(cache.host_lens), drafted=tree is not None) as (running, slots):
+        with cache.step(counts, drafted=tree is not None) as (following, slots):
             h, q, kv = self._queries(delta, residual)
             ql = torch.empty(q.shape[0], cfg.heads, cfg.rank + cfg.rope, dtype=torch.bfloat16, device=q.device)
-            A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, running if positions is None else positions,
+            A.latent_append(kv, self.norms["norm_kv"], cfg.eps, self.table, following if positions is None else positions,
                             slots, cache.pool, q_rope=q[..., cfg.nope:], q_out=ql[..., cfg.rank:])
             A.head_linear(q[..., :cfg.nope], self.w_uk_t, out=ql[..., :cfg.rank])
-            o = A.latent_attention(ql, cache.pool, cache.pages, cache.lens, cfg.scale, max_len=max(cache.host_lens), tree=tree)
+            cu = None if min(counts) == most else self._starts(counts)
+            o = A.latent_attention(ql, cache.pool, cache.pages, cache.lens, cfg.scale, cu_q=cu, max_q=most, tree=tree,
+                                   max_len=max((cache.host_lens[b] for b in running), default=0))
             return self._finish(A.head_linear(o, self.w_uv), h)
 
 

@@ -104,3 +104,61 @@ def test_the_last_known_position():
     at = torch.tensor([21, 22, 22, 23], dtype=torch.int32, device=DEV)
     _, tensors = block.decode(delta[21:25], residual[21:25], used, 4, tree=tree, positions=at)
     assert torch.equal(lists, tensors) and lists.isfinite().all()
+
+
+def test_sequences_sit_out_end_and_start_again():
+    block = make()
+    delta, residual = inputs(100, 7)
+    used = cache(seqs=3, n_pages=9)
+    alone = [cache(seqs=1) for _ in range(3)]
+
+    def both(call, *steps):
+        """A step of (sequence, first row, rows) triples, together and each alone."""
+        at = torch.cat([torch.arange(first, first + n) for _, first, n in steps]).to(DEV)
+        counts = [0] * 3
+        for b, _, n in steps:
+            counts[b] = n
+        _, out = getattr(block, call)(delta[at], residual[at], used, counts)
+        done = 0
+        for b, first, n in steps:
+            rows = slice(first, first + n)
+            _, want = getattr(block, call)(delta[rows], residual[rows], alone[b], [n])
+            near(out[done:done + n], want)
+            done += n
+        assert used.lens.tolist() == [c.host_lens[0] for c in alone]
+
+    both("prompt", (0, 0, 30), (2, 30, 17))       # the second sequence is empty
+    both("decode", (0, 60, 1), (2, 61, 1))
+    both("decode", (2, 62, 5))                    # a chunk of one of them
+    both("decode", (0, 67, 2), (2, 69, 1))        # chunks of different lengths
+    both("prompt", (1, 47, 13))
+    both("decode", (0, 70, 1), (1, 71, 1), (2, 72, 1))
+    used.truncate(0)
+    alone[0].truncate(0)
+    both("decode", (1, 73, 1), (2, 74, 1))
+    both("prompt", (0, 75, 20))                   # on pages that were another sequence's
+    both("decode", (0, 95, 1), (1, 96, 1), (2, 97, 1))
+    with pytest.raises(ValueError):
+        block.decode(delta[:1], residual[:1], used, [0, 0, 0, 1])
+    # no token at all
+    for call in (block.prompt, block.decode):
+        _, out = call(delta[:0], residual[:0], cache(seqs=2), [0, 0])
+        assert out.shape == (0, CFG.hidden)
+
+
+def test_trees_of_different_sizes():
+    block, used = make(), cache(seqs=3)
+    delta, residual = inputs(60, 8)
+    block.prompt(delta[:45], residual[:45], used, [20, 20, 5])
+    tree = torch.tensor([0b1, 0b11, 0b101, 0b1, 0b11], dtype=torch.int64, device=DEV)
+    _, out = block.decode(delta[45:50], residual[45:50], used, [3, 0, 2], tree=tree, positions=[20, 21, 21, 5, 6])
+    used.accept([[0, 2], [], [0]])
+    assert used.host_lens == [22, 20, 6]
+    for b, first, have, branch, rows in ((0, 0, 20, [45, 47], [0, 2]), (2, 40, 5, [48, 49], [3, 4])):
+        alone = cache(seqs=1)
+        block.prompt(delta[first:first + have], residual[first:first + have], alone, [have])
+        for at, row in zip(branch, rows):
+            _, want = block.decode(delta[at:at + 1], residual[at:at + 1], alone)
+            near(out[row], want[0])
+    with pytest.raises(ValueError):
+        block.decode(delta, residual, used, [65, 0, 0], tree=torch.ones(65, dtype=torch.int64, device=DEV), positions=[1] * 65)
