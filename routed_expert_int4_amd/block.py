@@ -16,10 +16,12 @@ interleaved rotary positions, one latent vector per token in the cache):
 
 The latents stay in bf16 in both forms (rounding them to 8 bits for the
 prompt's expansion would give a prompt other keys and values than the tokens
-decoded after it), so the expansions W_uk and W_uv are bf16 and per head.
+decoded after it), so the expansions W_uk and W_uv are bf16 and per head, as
+given.
 
-The block holds its weights (8-bit projections, bf16 expansions), the cache pages of its sequences and nothing else; the residual
-stream and the MoE output go from block to block.
+The block holds its weights (8-bit projections, bf16 expansions, the keys' one
+in both orders) and the table of angles; the cache belongs to the caller, and
+the residual stream and the MoE output go from block to block.
 """
 from __future__ import annotations
 
@@ -185,22 +187,35 @@ class LatentCache:
         self._drafted[b] = 0
 
 
+class _Weights(dict):
+    """The block's 8-bit projections by name, each (values, scales per 128 x
+    128 block).  "kv_b" is held per head and in bf16, as its products take it:
+    asked for here, it is put together again, with scales of one."""
+
+    def __init__(self, projections, w_uk, w_uv):
+        super().__init__(projections)
+        self._kv_b = w_uk, w_uv
+
+    def __missing__(self, name):
+        if name != "kv_b":
+            raise KeyError(name)
+        w = torch.cat(self._kv_b, 1).flatten(0, 1)
+        return w, torch.ones(-(-w.shape[0] // A.GROUP), -(-w.shape[1] // A.GROUP), device=w.device)
+
+
 class DecoderBlock:
     """The attention half around a DeviceLayer (or None: attention only)."""
 
     def __init__(self, cfg: BlockConfig, weights: dict, moe=None, max_positions: int = 4096, device: str = "cuda:0"):
         self.cfg, self.moe = cfg, moe
         self.norms = {k: weights[k] for k in ("norm_in", "norm_q", "norm_kv", "norm_moe")}
-        self.lin = {k: A.quantize_weight(weights[k]) for k in ("q_a", "q_b", "kv_a", "o")}
         # the per-head expansions, for the absorbed form with the keys'
         # transposed (queries go the other way)
-        code, s = A.quantize_weight(weights["kv_b"])
-        self.lin["kv_b"] = code, s
-        kb = s.repeat_interleave(128, 0)[:code.shape[0]].repeat_interleave(128, 1)[:, :code.shape[1]]
-        full = (code.float() * kb).view(cfg.heads, cfg.nope + cfg.vdim, cfg.rank)
-        self.w_uk = full[:, :cfg.nope].contiguous().bfloat16()
+        full = weights["kv_b"].reshape(cfg.heads, cfg.nope + cfg.vdim, cfg.rank)
+        self.w_uk = full[:, :cfg.nope].bfloat16().contiguous()
         self.w_uk_t = self.w_uk.transpose(1, 2).contiguous()
-        self.w_uv = full[:, cfg.nope:].contiguous().bfloat16()
+        self.w_uv = full[:, cfg.nope:].bfloat16().contiguous()
+        self.lin = _Weights({k: A.quantize_weight(weights[k]) for k in ("q_a", "q_b", "kv_a", "o")}, self.w_uk, self.w_uv)
         self.table = rope_table(max_positions, cfg.rope, device=device)
 
     def _linear(self, x, name):

@@ -151,3 +151,18 @@ def test_positions_past_the_table_are_refused():
         with pytest.raises(ValueError):
             block.decode(x[:2], x[:2], cache, 1, tree=torch.ones(2, dtype=torch.int64), positions=at)
     check(cache, [20, 18])
+
+
+def test_expansions_keep_the_bits_of_their_weights():
+    weights = random_weights(CFG, 1, device="cpu")
+    block = DecoderBlock(CFG, weights, max_positions=8, device="cpu")
+    full = weights["kv_b"].view(CFG.heads, CFG.nope + CFG.vdim, CFG.rank)
+    assert torch.equal(block.w_uk, full[:, :CFG.nope]) and torch.equal(block.w_uv, full[:, CFG.nope:])
+    assert torch.equal(block.w_uk_t, full[:, :CFG.nope].transpose(1, 2))
+    assert all(w.is_contiguous() for w in (block.w_uk, block.w_uk_t, block.w_uv))
+    # in one piece again, where it is asked for
+    w, scale = block.lin["kv_b"]
+    assert torch.equal(w, weights["kv_b"]) and scale.shape == (4, 2) and (scale == 1).all()
+    assert "kv_b" not in set(block.lin)
+    with pytest.raises(KeyError):
+        block.lin["kv"]
