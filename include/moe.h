@@ -513,8 +513,9 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
  * of the new ones, the i-th and its predecessors for token i, or with d_tree
  * those whose bit is set in the 64-bit d_tree[t] (bit j = the sequence's j-th
  * new token; a token's own bit is not implied; tokens past 64 are unseen).
- * Rows on a page index outside [0, n_pages) or past the table are unseen.  A
- * token that sees nothing gets zeros.  Rows that a token does not see have no
+ * Rows on a page index outside [0, n_pages) or past the table are unseen (a
+ * pool or a table without pages may be NULL).  A token that sees nothing gets
+ * zeros.  Rows that a token does not see have no
  * part in its output, whatever they hold (NaN and infinities included); a
  * seen row with such values may turn all columns of the output to NaN.
  * max_q and max_len bound the new tokens and rows of a sequence (they size

@@ -164,7 +164,8 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
         return fail(MOE_EUNSUPPORTED, "%s: no kernel for rank %d and rope %d", who, rank, rope);
     if (T == 0) return MOE_OK;
     if (B < 1 || max_q < 1) return fail(MOE_EINVAL, "%s: tokens without a sequence", who);
-    if (!d_q || !d_cache || !d_pages || !d_lens || !d_out) return fail(MOE_EINVAL, "%s: NULL pointer", who);
+    if (!d_q || !d_lens || !d_out || (n_pages > 0 && !d_cache) || (pages_per_seq > 0 && !d_pages))
+        return fail(MOE_EINVAL, "%s: NULL pointer", who);
     if (!d_cu_q && (T % B || T / B > max_q))
         return fail(MOE_EINVAL, "%s: T (%d) is not B (%d) times at most max_q (%d) tokens", who, T, B, max_q);
     if (page_stride < (int64_t)page_size * (rank + rope) || pages_stride < pages_per_seq)
