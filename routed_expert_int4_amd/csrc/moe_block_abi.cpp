@@ -181,6 +181,9 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
     if (rows_per_table > ((int64_t)1 << 31) - 128 || B > 65535 || (int64_t)max_q * heads > (int64_t)1 << 30 ||
         (double)(B + (int64_t)T * heads / 32) * (double)(rows_per_table / 64 + 1) > (double)(1 << 30))
         return fail(MOE_EUNSUPPORTED, "%s: too many tiles", who);
+    // the second launch has a wave per row of the longest sequence, and 32-bit grids count lanes
+    if ((int64_t)(max_q < T ? max_q : T) * heads >= (int64_t)1 << 26)
+        return fail(MOE_EUNSUPPORTED, "%s: 2^26 or more rows (tokens times heads) in a sequence", who);
     const size_t need = latent_workspace(B, max_q, heads, rank, max_len);
     if (!d_ws || ws_bytes < need || !on(d_ws, 256))
         return fail(MOE_EINVAL, "%s: workspace of %zu bytes given, %zu needed (256-byte aligned)", who, ws_bytes, need);

@@ -643,7 +643,7 @@ void launch_rows(LatentArgs a, const LatentCut& cut, hipStream_t s) {
     const int grid = (cut.runs + 7) / 8 * 8 * cut.group;
     hipLaunchKernelGGL((latent_attention_kernel<RANK, RG>), dim3(grid), dim3(RG * 256), 0, s, a);
     if (cut.runs > 1) {
-        const int rows = a.max_q * a.heads;
+        const int rows = (a.max_q < a.T ? a.max_q : a.T) * a.heads;
         if ((long)rows * a.B <= kFewRows)
             hipLaunchKernelGGL((latent_join_kernel<RANK, RG * 32, 4>), dim3(rows, a.B), dim3(256), 0, s, a);
         else

@@ -22,3 +22,14 @@ def test_latent_attention_without_pages(heads, nq):
     for cache, table in ((pool[:0], pages), (pool, pages[:, :0].contiguous()), (pool[:0], pages[:, :0].contiguous())):
         out = A.latent_attention(q, cache, table, lens, 0.07)
         assert out.shape == (2 * nq, heads, 256) and (out == 0).all()
+
+
+def test_latent_attention_with_a_loose_bound_of_tokens():
+    # max_q only bounds: the launch that joins the parts of a sequence is sized by the tokens there are
+    g = gen(2)
+    nq, lens = [2, 3], [700, 300]
+    q, cache, pages, dl = latent_case(g, lens, nq, 64, 512, 64)
+    ref, mag = latent_ref(q, cache, pages, lens, nq, 0.07, 512)
+    for max_q in (3, 5, 1 << 24):
+        out = A.latent_attention(q, cache, pages, dl, 0.07, max_len=700, cu_q=cumulative(nq), max_q=max_q)
+        close(out, ref, U * ref.abs() + U * mag, f"max_q {max_q}")
