@@ -519,7 +519,10 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
  * part in its output, whatever they hold (NaN and infinities included); a
  * seen row with such values may turn all columns of the output to NaN.
  * max_q and max_len bound the new tokens and rows of a sequence (they size
- * the launch and the workspace only).  rank 512 or 256 with rope 64; scale
+ * the launch and the workspace only; a longer one is right as far as max_len
+ * goes, but tokens past max_q may be left unwritten).  d_cu_q must not
+ * decrease: bounds that name more than T tokens in all leave d_out as it is.
+ * Rows of d_q that belong to no sequence are not written in d_out.  rank 512 or 256 with rope 64; scale
  * positive.  moe_latent_attention_workspace: device bytes needed, 256-byte
  * aligned; the buffer's contents need not be kept or cleared. */
 size_t moe_latent_attention_workspace(int B, int max_q, int heads, int rank, int max_len);
@@ -540,7 +543,8 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
  * zeros; keys and values that it does not see have no part in its output,
  * whatever they hold.  (nope, rope, vdim) in {(64, 64, 64), (128, 64, 128),
  * (192, 64, 256)}; strides multiples of 8 and pointers 16-byte aligned;
- * scale positive.  max_q bounds the queries of a sequence. */
+ * scale positive.  max_q bounds the queries of a sequence: rows past it, and
+ * rows of d_q that belong to no sequence, are not written in d_out. */
 moe_status_t moe_prompt_attention(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* d_k,
                                   int64_t k_stride_t, int64_t k_stride_h, const uint16_t* d_k_rope,
                                   int64_t kr_stride_t, const uint16_t* d_v, int64_t v_stride_t, int64_t v_stride_h,

@@ -294,8 +294,9 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     q [T, heads, rank + rope] bf16; cache [pages, page_size, rank + rope];
     pages int32 [B, pages per sequence]; lens int32 [B] (rows of each
     sequence, its new tokens included).  New tokens: T / B per sequence, or
-    with cu_q (int32 [B + 1]) rows cu_q[b] .. cu_q[b + 1] of q, at most max_q
-    each.  max_len bounds lens (the page table's reach if None; a tighter
+    with cu_q (int32 [B + 1], not decreasing) rows cu_q[b] .. cu_q[b + 1] of q,
+    at most max_q each (rows of q in no sequence have no output: what out held
+    there stays, and a new one holds anything).  max_len bounds lens (the page table's reach if None; a tighter
     bound makes short calls faster).  A token sees the context and the new
     tokens up to itself, or those set in its mask (tree, int64 [T], bit j for
     the sequence's j-th new token, itself included if set).  Returns
@@ -356,8 +357,8 @@ def prompt_attention(q, k, k_rope, v, scale: float, cu_q=None, cu_k=None, max_q:
     by the heads, v [Tk, heads, vdim], all bf16 (k and v may be views of one
     expansion).  Sequence b has queries cu_q[b] .. cu_q[b + 1] and keys
     cu_k[b] .. cu_k[b + 1] (int32 [B + 1]; None: one sequence); its queries
-    are its last positions.  max_q bounds the queries of a sequence; max_k is
-    not needed.  Returns [Tq, heads, vdim] bf16."""
+    are its last positions.  max_q bounds the queries of a sequence (rows past
+    it or in no sequence have no output); max_k is not needed.  Returns [Tq, heads, vdim] bf16."""
     if stream is not None:
         return _elsewhere(stream, prompt_attention, q, k, k_rope, v, scale, cu_q, cu_k, max_q, max_k, causal, out)
     (Tq, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY)

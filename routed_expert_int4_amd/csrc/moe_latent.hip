@@ -94,10 +94,12 @@ __device__ __forceinline__ int wave_scan_int(int v) {
     return scan_step<0x143, 0xC>(v);  // lane 31 into the upper half
 }
 
-// The whole list: its length, and the tiles before sequence `upto`.
+// The whole list: its length, and the tiles before sequence `upto`.  The host
+// has seen to it that the tiles of T tokens fit 32 bits, so bounds in device
+// memory that name more than T (some of them twice) leave the list empty.
 template <int ROWS>
 __device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int lane, int& before) {
-    int total = 0;
+    int total = 0, tokens = 0;  // this lane's sequences', T + 1 for any number above T
     before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
         const int b = b0 + lane;
@@ -105,11 +107,15 @@ __device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int la
         if (b < a.B) {
             const SeqShape s = seq_shape<ROWS>(a, b);
             mine = s.tiles * s.passes;
+            tokens = tokens + s.count > a.T ? a.T + 1 : tokens + s.count;
         }
         const int scan = wave_scan_int(mine);
         if (upto > b0) before = total + __builtin_amdgcn_readlane(scan, (upto - b0 < 64 ? upto - b0 : 64) - 1);
         total += __builtin_amdgcn_readlane(scan, 63);
     }
+    // (64 lanes of up to T, below 2^26, are below 2^32)
+    if (a.cu_q && (__any(tokens > a.T) || (unsigned)__builtin_amdgcn_readlane(wave_scan_int(tokens), 63) > (unsigned)a.T))
+        return 0;
     return total;
 }
 
@@ -534,6 +540,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
     if (row >= shape.count * a.heads) return;
     int before;
     const int total = count_tiles<ROWS>(a, seq, lane, before), runs = run_count(total, a.runs);
+    if (total == 0) return;  // nor has the first launch done anything
     const int block = row / ROWS, r = row % ROWS, member = block % a.group;
     const int u0 = before + block / a.group * shape.tiles, u1 = u0 + shape.tiles;
     // runs that hold the unit's first and last tile
