@@ -48,27 +48,18 @@ class AppendOut(NamedTuple):
     rows: torch.Tensor | None    # the cache rows, one after another
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _launch(device, call, *args) -> None:
-    """call(*args, stream) on the current stream of `device`, which is the
-    current device for its duration (a launch goes to that one, whatever device
-    the stream belongs to)."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(device, call, *args)
-    stream = _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
-    B.check(call(*args, stream))
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _elsewhere(stream, f, *args):
-    """f(*args) on `stream` (torch's, or a handle) of the first operand's
-    device: what it allocates belongs to that stream, and memory of the inputs
-    is not used again before a stream of torch's has passed the call (a
-    handle's owner sees to that)."""
+    """f(*args) on `stream` (torch's, or a handle; None: the current one) of
+    the first operand's device, as the current device (a launch goes to that
+    one, whatever device its stream belongs to).  What f allocates belongs to
+    that stream, and memory of the inputs is not used again before a stream of
+    torch's has passed the call (a handle's owner sees to that)."""
     device = args[0].device
-    _need(device.type == "cuda", f"a device tensor is needed, got one on {device}")
+    _need(device.type == "cuda", f"a tensor on a GPU is needed, got one on {device}")
     if isinstance(stream, torch.cuda.Stream):
         _need(stream.device == device, f"a stream of {stream.device} and operands on {device}")
         with torch.cuda.stream(stream):
@@ -77,6 +68,9 @@ def _elsewhere(stream, f, *args):
             if isinstance(t, torch.Tensor):
                 t.record_stream(stream)
         return out
+    if stream is None:
+        with torch.cuda.device(device):
+            return f(*args)
     handle = B._stream_handle(stream)
     with torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)):
         return f(*args)
@@ -87,15 +81,14 @@ def _need(ok: bool, what: str) -> None:
         raise B.MoeError(B.MOE_EINVAL, what)
 
 
-def _rows(t: torch.Tensor, name: str, dims: int, dtypes, device=None):
-    """Shape and strides of a device tensor of `dims` dimensions with a
-    contiguous last one, on `device` (that of a call's first operand) if given."""
+def _rows(t: torch.Tensor, name: str, dims: int, dtypes, on: int):
+    """Shape and strides of a tensor of `dims` dimensions with a contiguous
+    last one on GPU `on`, that of the call's first operand."""
     shape, stride = t.shape, t.stride()
-    if (len(stride) == dims and t.dtype in dtypes and (t.is_cuda if device is None else t.device == device)
-            and (stride[-1] == 1 or shape[-1] <= 1)):
+    if len(stride) == dims and t.dtype in dtypes and t.get_device() == on and (stride[-1] == 1 or shape[-1] <= 1):
         return shape, stride
     raise B.MoeError(B.MOE_EINVAL, f"{name}: a tensor of {dims} dimensions, contiguous in the last, of type "
-                                   f"{' or '.join(str(d) for d in dtypes)} on {device or 'a GPU'} is needed, got {t.dtype} "
+                                   f"{' or '.join(str(d) for d in dtypes)} on cuda:{on} is needed, got {t.dtype} "
                                    f"{tuple(shape)} with strides {stride} on {t.device}")
 
 
@@ -119,44 +112,45 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, out: str = "bf16", 
     "fp8" (codes and one scale per 128 columns) or "both".  h is returned in
     the residual's type (sum_out, which may be the residual itself, receives
     it in place; want_sum=False leaves it out)."""
-    if stream is not None:
+    on = x.get_device()
+    if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, add_rmsnorm, x, weight, eps, residual, out, sum_out, want_sum)
-    shape, strides = _rows(x, "x", 2, _WIDE)
-    dev = x.device
+    shape, strides = _rows(x, "x", 2, _WIDE, on)
     T, H = shape
     weight_p, w_type = None, 0
     if weight is not None:
-        wide, _ = _rows(weight, "weight", 1, _WIDE, dev)
+        wide, _ = _rows(weight, "weight", 1, _WIDE, on)
         if wide[0] != H:
             _need(False, f"weight has {wide[0]} values, x {H} columns")
         weight_p, w_type = weight.data_ptr(), _TYPES[weight.dtype]
     x_type = _TYPES[x.dtype]
     residual_p, r_stride, r_type, sum_type = None, 0, 0, x.dtype
     if residual is not None:
-        r_shape, r_strides = _rows(residual, "residual", 2, _WIDE, dev)
+        r_shape, r_strides = _rows(residual, "residual", 2, _WIDE, on)
         if r_shape != shape:
             _need(False, f"residual {tuple(r_shape)}, x {tuple(shape)}")
         residual_p, r_stride, sum_type = residual.data_ptr(), r_strides[0] if T > 1 else H, residual.dtype
         r_type = _TYPES[sum_type]
     sum_p, s_stride = None, H
     if sum_out is not None:
-        s_shape, s_strides = _rows(sum_out, "sum_out", 2, (sum_type,), dev)
+        s_shape, s_strides = _rows(sum_out, "sum_out", 2, (sum_type,), on)
         _need(s_shape == shape, f"sum_out {tuple(s_shape)}, x {tuple(shape)}")
         sum_p, s_stride = sum_out.data_ptr(), s_strides[0] if T > 1 else H
     elif want_sum and residual is not None:
-        sum_out = torch.empty(shape, dtype=sum_type, device=dev)
+        sum_out = torch.empty(shape, dtype=sum_type, device=on)
         sum_p = sum_out.data_ptr()
     y = q = scale = y_p = q_p = scale_p = None
     pad = -(-H // 16) * 16
     if out != "fp8":
         _need(out in ("bf16", "both"), f"out: {out!r}")
-        y = torch.empty(shape, dtype=_BF16, device=dev)
+        y = torch.empty(shape, dtype=_BF16, device=on)
         y_p = y.data_ptr()
     if out != "bf16":
-        q, scale = _codes(T, H, dev), _scales(T, H, dev)
+        q, scale = _codes(T, H, on), _scales(T, H, on)
         q_p, scale_p = q.data_ptr(), scale.data_ptr()
-    _launch(dev, B.lib().moe_add_rmsnorm, x.data_ptr(), x_type, strides[0] if T > 1 else H, residual_p, r_type, r_stride,
-            weight_p, w_type, T, H, eps, sum_p, s_stride, y_p, H, q_p, pad, scale_p, 1, T)
+    B.check(B.lib().moe_add_rmsnorm(x.data_ptr(), x_type, strides[0] if T > 1 else H, residual_p, r_type, r_stride,
+                                    weight_p, w_type, T, H, eps, sum_p, s_stride, y_p, H, q_p, pad,
+                                    scale_p, 1, T, _raw_stream(on)))
     return NormOut(sum_out, y, q, scale)
 
 
@@ -183,28 +177,30 @@ def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -
     w [N, K] 8-bit with w_scale [ceil(N / 128), ceil(K / 128)]: [M, N] in
     out_dtype (bf16 or fp32).  K is a multiple of 16; a_scale may have any
     strides (add_rmsnorm's are the fastest)."""
-    if stream is not None:
+    on = a.get_device()
+    if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, fp8_linear, a, a_scale, w, w_scale, out_dtype, out)
-    (M, K), a_strides = _rows(a, "a", 2, _FP8_ONLY)
-    dev = a.device
-    (N, wk), w_strides = _rows(w, "w", 2, _FP8_ONLY, dev)
-    ws_shape, ws_strides = _rows(w_scale, "w_scale", 2, _F32_ONLY, dev)
+    (M, K), a_strides = _rows(a, "a", 2, _FP8_ONLY, on)
+    (N, wk), w_strides = _rows(w, "w", 2, _FP8_ONLY, on)
+    ws_shape, ws_strides = _rows(w_scale, "w_scale", 2, _F32_ONLY, on)
     kb, nb = (K + GROUP - 1) // GROUP, (N + GROUP - 1) // GROUP
     as_shape, as_strides = a_scale.shape, a_scale.stride()
-    if wk != K or a_scale.dtype is not _F32 or a_scale.device != dev or tuple(as_shape) != (M, kb) or tuple(ws_shape) != (nb, kb):
-        _need(False, f"a {(M, K)} and w {(N, wk)} need scales of fp32 {(M, kb)} and {(nb, kb)} on {dev}, got "
+    if (wk != K or a_scale.dtype is not _F32 or a_scale.get_device() != on or tuple(as_shape) != (M, kb)
+            or tuple(ws_shape) != (nb, kb)):
+        _need(False, f"a {(M, K)} and w {(N, wk)} need scales of fp32 {(M, kb)} and {(nb, kb)} on cuda:{on}, got "
                      f"{a_scale.dtype} {tuple(as_shape)} on {a_scale.device} and {tuple(ws_shape)}, and the same inner width")
     if out is None:
         _need(out_dtype in _TYPES, f"out_dtype {out_dtype}: bf16 or fp32")
-        out, o_stride = torch.empty((M, N), dtype=out_dtype, device=dev), N
+        out, o_stride = torch.empty((M, N), dtype=out_dtype, device=on), N
     else:
-        o_shape, o_strides = _rows(out, "out", 2, _WIDE, dev)
+        o_shape, o_strides = _rows(out, "out", 2, _WIDE, on)
         _need(tuple(o_shape) == (M, N), f"out {tuple(o_shape)}, {(M, N)} is needed")
         out_dtype, o_stride = out.dtype, o_strides[0] if M > 1 else N
     pad = -(-K // 16) * 16  # the stride of a single row says nothing
-    _launch(dev, B.lib().moe_fp8_linear, a.data_ptr(), a_strides[0] if M > 1 else pad, a_scale.data_ptr(), as_strides[0],
-            as_strides[1], w.data_ptr(), w_strides[0] if N > 1 else pad, w_scale.data_ptr(),
-            ws_strides[0] if nb > 1 else kb, M, N, K, out.data_ptr(), _TYPES[out_dtype], o_stride)
+    B.check(B.lib().moe_fp8_linear(a.data_ptr(), a_strides[0] if M > 1 else pad, a_scale.data_ptr(), as_strides[0],
+                                   as_strides[1], w.data_ptr(), w_strides[0] if N > 1 else pad, w_scale.data_ptr(),
+                                   ws_strides[0] if nb > 1 else kb, M, N, K, out.data_ptr(), _TYPES[out_dtype], o_stride,
+                                   _raw_stream(on)))
     return out
 
 
@@ -212,20 +208,21 @@ def head_linear(x, w, out=None, stream=None) -> torch.Tensor:
     """x [T, heads, K] times the transpose of w [heads, N, K], head by head:
     [T, heads, N], all bf16.  x and out may be strided views (of a wider
     query, say)."""
-    if stream is not None:
+    on = x.get_device()
+    if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, head_linear, x, w, out)
-    (T, heads, K), xs = _rows(x, "x", 3, _BF16_ONLY)
-    dev = x.device
-    w_shape, _ = _rows(w, "w", 3, _BF16_ONLY, dev)
+    (T, heads, K), xs = _rows(x, "x", 3, _BF16_ONLY, on)
+    w_shape, _ = _rows(w, "w", 3, _BF16_ONLY, on)
     N = w_shape[1]
     if w_shape[0] != heads or w_shape[2] != K or not w.is_contiguous():
         _need(False, f"w: contiguous {(heads, 'N', K)} is needed, got {tuple(w_shape)} with strides {w.stride()}")
     if out is None:
-        out, os = torch.empty((T, heads, N), dtype=_BF16, device=dev), (heads * N, N)
+        out, os = torch.empty((T, heads, N), dtype=_BF16, device=on), (heads * N, N)
     else:
-        o_shape, os = _rows(out, "out", 3, _BF16_ONLY, dev)
+        o_shape, os = _rows(out, "out", 3, _BF16_ONLY, on)
         _need(tuple(o_shape) == (T, heads, N), f"out {tuple(o_shape)}, {(T, heads, N)} is needed")
-    _launch(dev, B.lib().moe_head_linear, x.data_ptr(), xs[0], xs[1], w.data_ptr(), T, heads, K, N, out.data_ptr(), os[0], os[1])
+    B.check(B.lib().moe_head_linear(x.data_ptr(), xs[0], xs[1], w.data_ptr(), T, heads, K, N, out.data_ptr(), os[0], os[1],
+                                    _raw_stream(on)))
     return out
 
 
@@ -240,50 +237,50 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
     page_size, rank + rope] contiguous.  q_rope [T, heads, rope] is rotated
     into q_out (given, the view itself for in place, or new).  want_fp8: the
     normed latent in 8 bits too; want_key: the rotated key part too."""
-    if stream is not None:
+    on = kv.get_device()
+    if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, latent_append, kv, weight, eps, table, positions, slots, cache, q_rope, q_out,
                           want_fp8, want_key)
-    (T, width), kvs = _rows(kv, "kv", 2, _BF16_ONLY)
-    dev = kv.device
-    (rank,), _ = _rows(weight, "weight", 1, _WIDE, dev)
-    (n_positions, rope), _ = _rows(table, "table", 2, _F32_ONLY, dev)
-    (n,), _ = _rows(positions, "positions", 1, _I32_ONLY, dev)
+    (T, width), kvs = _rows(kv, "kv", 2, _BF16_ONLY, on)
+    (rank,), _ = _rows(weight, "weight", 1, _WIDE, on)
+    (n_positions, rope), _ = _rows(table, "table", 2, _F32_ONLY, on)
+    (n,), _ = _rows(positions, "positions", 1, _I32_ONLY, on)
     if width != rank + rope or n != T or not table.is_contiguous():
         _need(False, f"kv has {width} columns, weight and table {rank} + {rope}; {n} positions for {T} tokens; table "
                      "contiguous")
     cache_p = slots_p = None
     n_slots = 0
     if cache is not None:
-        if cache.dtype is not _BF16 or cache.device != dev or not cache.is_contiguous() or cache.shape[-1] != width:
-            _need(False, f"cache: contiguous bf16 rows of {width} on {dev} are needed, got {cache.dtype} {tuple(cache.shape)} on "
-                         f"{cache.device}")
+        if cache.dtype is not _BF16 or cache.get_device() != on or not cache.is_contiguous() or cache.shape[-1] != width:
+            _need(False, f"cache: contiguous bf16 rows of {width} on cuda:{on} are needed, got {cache.dtype} "
+                         f"{tuple(cache.shape)} on {cache.device}")
         _need(slots is not None, "a cache needs slots")
-        (n,), _ = _rows(slots, "slots", 1, _I64_ONLY, dev)
+        (n,), _ = _rows(slots, "slots", 1, _I64_ONLY, on)
         _need(n == T, f"{n} slots for {T} tokens")
         cache_p, slots_p, n_slots = cache.data_ptr(), slots.data_ptr(), cache.numel() // width
     heads, qs, qo, qp, qop = 0, (0, 0), (0, 0), None, None
     if q_rope is not None:
-        q_shape, qs = _rows(q_rope, "q_rope", 3, _BF16_ONLY, dev)
+        q_shape, qs = _rows(q_rope, "q_rope", 3, _BF16_ONLY, on)
         if q_shape[0] != T or q_shape[2] != rope:
             _need(False, f"q_rope {tuple(q_shape)}, {(T, 'heads', rope)} is needed")
         heads = q_shape[1]
         if q_out is None:
-            q_out, qo = torch.empty(q_shape, dtype=_BF16, device=dev), (heads * rope, rope)
+            q_out, qo = torch.empty(q_shape, dtype=_BF16, device=on), (heads * rope, rope)
         else:
-            qo_shape, qo = _rows(q_out, "q_out", 3, _BF16_ONLY, dev)
+            qo_shape, qo = _rows(q_out, "q_out", 3, _BF16_ONLY, on)
             _need(qo_shape == q_shape, f"q_out {tuple(qo_shape)}, q_rope {tuple(q_shape)}")
         qp, qop = q_rope.data_ptr(), q_out.data_ptr()
     q = scale = rows = q_p = scale_p = rows_p = None
     if want_fp8:
-        q, scale = _codes(T, rank, dev), _scales(T, rank, dev)
+        q, scale = _codes(T, rank, on), _scales(T, rank, on)
         q_p, scale_p = q.data_ptr(), scale.data_ptr()
     if want_key:
-        rows = torch.empty((T, width), dtype=_BF16, device=dev)
+        rows = torch.empty((T, width), dtype=_BF16, device=on)
         rows_p = rows.data_ptr()
-    _launch(
-        dev, B.lib().moe_latent_append, kv.data_ptr(), kvs[0] if T > 1 else width, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
+    B.check(B.lib().moe_latent_append(
+        kv.data_ptr(), kvs[0] if T > 1 else width, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
         table.data_ptr(), n_positions, positions.data_ptr(), slots_p, T, cache_p, n_slots, qp, heads, qs[0], qs[1],
-        qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, rows_p, width)
+        qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, rows_p, width, _raw_stream(on)))
     return AppendOut(q_out if q_rope is not None else None, q, scale, rows[:, rank:] if want_key else None, rows)
 
 
@@ -302,14 +299,14 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     the sequence's j-th new token, itself included if set).  Returns
     [T, heads, rank] bf16.  workspace: uint8 of
     moe_latent_attention_workspace() bytes (allocated per call if None)."""
-    if stream is not None:
+    on = q.get_device()
+    if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, latent_attention, q, cache, pages, lens, scale, max_len, cu_q, max_q, tree, out,
                           workspace)
-    (T, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY)
-    dev = q.device
-    (n_pages, page_size, c_width), cs = _rows(cache, "cache", 3, _BF16_ONLY, dev)
-    (nb, per_seq), ps = _rows(pages, "pages", 2, _I32_ONLY, dev)
-    (n,), _ = _rows(lens, "lens", 1, _I32_ONLY, dev)
+    (T, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY, on)
+    (n_pages, page_size, c_width), cs = _rows(cache, "cache", 3, _BF16_ONLY, on)
+    (nb, per_seq), ps = _rows(pages, "pages", 2, _I32_ONLY, on)
+    (n,), _ = _rows(lens, "lens", 1, _I32_ONLY, on)
     rope = 64
     rank = width - rope
     if c_width != width or (page_size > 1 and cs[1] != width) or n != nb:
@@ -317,7 +314,7 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
                      f"{cs}; {n} lengths for {nb} page rows")
     cu_p = tree_p = None
     if cu_q is not None:
-        (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY, dev)
+        (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY, on)
         _need(n == nb + 1 and max_q is not None, f"cu_q has {n} entries for {nb} sequences; it needs max_q")
         cu_p = cu_q.data_ptr()
     else:
@@ -325,27 +322,28 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     if max_len is None:
         max_len = per_seq * page_size
     if tree is not None:
-        (n,), _ = _rows(tree, "tree", 1, _I64_ONLY, dev)
+        (n,), _ = _rows(tree, "tree", 1, _I64_ONLY, on)
         _need(n == T, f"tree has {n} masks for {T} tokens")
         tree_p = tree.data_ptr()
     if out is None:
-        out, os = torch.empty((T, heads, rank), dtype=_BF16, device=dev), (heads * rank, rank)
+        out, os = torch.empty((T, heads, rank), dtype=_BF16, device=on), (heads * rank, rank)
     else:
-        o_shape, os = _rows(out, "out", 3, _BF16_ONLY, dev)
+        o_shape, os = _rows(out, "out", 3, _BF16_ONLY, on)
         _need(tuple(o_shape) == (T, heads, rank), f"out {tuple(o_shape)}, {(T, heads, rank)} is needed")
     L = B.lib()
     if workspace is None:
         n = L.moe_latent_attention_workspace(nb, max_q, heads, rank, max_len)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(n, dtype=torch.uint8, device=on)
     else:
-        if workspace.device != dev or not workspace.is_contiguous():
-            _need(False, f"workspace: contiguous memory of {dev} is needed, got strides {workspace.stride()} on "
+        if workspace.get_device() != on or not workspace.is_contiguous():
+            _need(False, f"workspace: contiguous memory of cuda:{on} is needed, got strides {workspace.stride()} on "
                          f"{workspace.device}")
         n = workspace.numel() * workspace.element_size()
-    _launch(
-        dev, L.moe_latent_attention, q.data_ptr(), qs[0], qs[1], T, heads, rank, rope, cache.data_ptr(), n_pages, page_size,
+    B.check(L.moe_latent_attention(
+        q.data_ptr(), qs[0], qs[1], T, heads, rank, rope, cache.data_ptr(), n_pages, page_size,
         cs[0] if n_pages > 1 else page_size * width, pages.data_ptr(), ps[0] if nb > 1 else per_seq, per_seq,
-        lens.data_ptr(), nb, cu_p, max_q, max_len, tree_p, scale, out.data_ptr(), os[0], os[1], workspace.data_ptr(), n)
+        lens.data_ptr(), nb, cu_p, max_q, max_len, tree_p, scale, out.data_ptr(), os[0], os[1], workspace.data_ptr(), n,
+        _raw_stream(on)))
     return out
 
 
@@ -359,31 +357,31 @@ def prompt_attention(q, k, k_rope, v, scale: float, cu_q=None, cu_k=None, max_q:
     cu_k[b] .. cu_k[b + 1] (int32 [B + 1]; None: one sequence); its queries
     are its last positions.  max_q bounds the queries of a sequence (rows past
     it or in no sequence have no output); max_k is not needed.  Returns [Tq, heads, vdim] bf16."""
-    if stream is not None:
+    on = q.get_device()
+    if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, prompt_attention, q, k, k_rope, v, scale, cu_q, cu_k, max_q, max_k, causal, out)
-    (Tq, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY)
-    dev = q.device
-    (Tk, k_heads, nope), ks = _rows(k, "k", 3, _BF16_ONLY, dev)
-    (r_rows, rope), rs = _rows(k_rope, "k_rope", 2, _BF16_ONLY, dev)
-    (v_rows, v_heads, vdim), vs = _rows(v, "v", 3, _BF16_ONLY, dev)
+    (Tq, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY, on)
+    (Tk, k_heads, nope), ks = _rows(k, "k", 3, _BF16_ONLY, on)
+    (r_rows, rope), rs = _rows(k_rope, "k_rope", 2, _BF16_ONLY, on)
+    (v_rows, v_heads, vdim), vs = _rows(v, "v", 3, _BF16_ONLY, on)
     if k_heads != heads or v_heads != heads or v_rows != Tk or r_rows != Tk or nope + rope != width:
         _need(False, f"q {tuple(q.shape)}, k {tuple(k.shape)}, k_rope {tuple(k_rope.shape)}, v {tuple(v.shape)} do not go "
                      "together")
     _need((cu_q is None) == (cu_k is None), "cu_q and cu_k go together")
     if cu_q is None:
-        ends = torch.arange(2, dtype=torch.int32, device=dev)
+        ends = torch.arange(2, dtype=torch.int32, device=on)
         cu_q, cu_k = ends * Tq, ends * Tk
         max_q = Tq
-    (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY, dev)
-    (n_k,), _ = _rows(cu_k, "cu_k", 1, _I32_ONLY, dev)
+    (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY, on)
+    (n_k,), _ = _rows(cu_k, "cu_k", 1, _I32_ONLY, on)
     _need(n == n_k and n >= 1 and max_q is not None, "cu_q and cu_k: one more entry than sequences each, and max_q")
     if out is None:
-        out, os = torch.empty((Tq, heads, vdim), dtype=_BF16, device=dev), (heads * vdim, vdim)
+        out, os = torch.empty((Tq, heads, vdim), dtype=_BF16, device=on), (heads * vdim, vdim)
     else:
-        o_shape, os = _rows(out, "out", 3, _BF16_ONLY, dev)
+        o_shape, os = _rows(out, "out", 3, _BF16_ONLY, on)
         _need(tuple(o_shape) == (Tq, heads, vdim), f"out {tuple(o_shape)}, {(Tq, heads, vdim)} is needed")
-    _launch(
-        dev, B.lib().moe_prompt_attention, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], k_rope.data_ptr(), rs[0], v.data_ptr(), vs[0], vs[1], Tq,
+    B.check(B.lib().moe_prompt_attention(
+        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], k_rope.data_ptr(), rs[0], v.data_ptr(), vs[0], vs[1], Tq,
         Tk, heads, nope, rope, vdim, cu_q.data_ptr(), cu_k.data_ptr(), n - 1, max_q, int(causal), scale, out.data_ptr(),
-        os[0], os[1])
+        os[0], os[1], _raw_stream(on)))
     return out

@@ -17,6 +17,9 @@ class On:
     def __init__(self, tensor, device):
         self.tensor, self.device, self.is_cuda = tensor, torch.device(device), device != "cpu"
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
     def __getattr__(self, name):
         return getattr(self.tensor, name)
 
@@ -38,8 +41,8 @@ def heads(p):
 
 
 def append(p):
-    A.latent_append(p(z(2, 320)), p(z(256)), 1e-6, p(z(8, 64, dtype=F32)), p(z(2, dtype=I32)), p(z(2, dtype=I64)), p(z(2, 16, 320)),
-                    q_rope=p(z(2, 4, 64)), q_out=p(z(2, 4, 64)))
+    A.latent_append(p(z(2, 320)), p(z(256)), 1e-6, p(z(8, 64, dtype=F32)), p(z(2, dtype=I32)), p(z(2, dtype=I64)),
+                    p(z(2, 16, 320)), q_rope=p(z(2, 4, 64)), q_out=p(z(2, 4, 64)))
 
 
 def latent(p):
@@ -55,11 +58,34 @@ def prompt(p):
 CALLS = {norm: 4, linear: 5, heads: 3, append: 8, latent: 8, prompt: 7}
 
 
+class Guard:
+    """Stands in for torch.cuda.device."""
+    current = [0]
+
+    def __init__(self, device):
+        self.device = torch.device(device)
+
+    def __enter__(self):
+        Guard.current.append(self.device.index)
+
+    def __exit__(self, *_):
+        Guard.current.pop()
+
+
 @pytest.fixture
 def launched(monkeypatch):
-    """The calls that got as far as a launch, by device."""
-    calls = []
-    monkeypatch.setattr(A, "_launch", lambda device, call, *args: calls.append(device))
+    """The calls that got as far as a launch: (current device, stream)."""
+    calls, empty = [], torch.empty
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: calls.append((Guard.current[-1], args[-1])) or B.MOE_OK
+
+    monkeypatch.setattr(B, "lib", Library)
+    monkeypatch.setattr(torch, "empty", lambda *a, device, **k: empty(*a, **k))
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(A, "_device", lambda: Guard.current[-1])
+    monkeypatch.setattr(A, "_raw_stream", lambda index: 100 + index)
     return calls
 
 
@@ -75,32 +101,10 @@ def test_one_operand_elsewhere(call, other, launched):
 
 
 @pytest.mark.parametrize("call", CALLS, ids=lambda c: c.__name__)
-def test_operands_together(call, launched, monkeypatch):
-    empty = torch.empty
-    monkeypatch.setattr(torch, "empty", lambda *a, device, **k: empty(*a, **k))
-    call(lambda t: On(t, "cuda:1"))
-    assert launched == [torch.device("cuda:1")]
-
-
-def test_launches_go_to_the_operands_device(monkeypatch):
-    seen, current = [], [0]
-
-    class Guard:
-        def __init__(self, device):
-            self.device = device
-
-        def __enter__(self):
-            current.append(self.device.index)
-
-        def __exit__(self, *_):
-            current.pop()
-
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
-    monkeypatch.setattr(torch.cuda, "device", Guard)
-    monkeypatch.setattr(A, "_raw_stream", lambda index: 100 + index)
-    for index in (0, 1):
-        A._launch(torch.device("cuda", index), lambda *a: seen.append((current[-1], *a)) or B.MOE_OK, 7)
-    assert seen == [(0, 7, 100), (1, 7, 101)] and current == [0]
+@pytest.mark.parametrize("device", [0, 1])
+def test_launches_go_to_the_operands_device(call, device, launched):
+    call(lambda t: On(t, f"cuda:{device}"))
+    assert launched == [(device, 100 + device)] and Guard.current == [0]
 
 
 def test_a_stream_for_operands_on_the_cpu(launched):
