@@ -152,8 +152,9 @@ __global__ void __launch_bounds__(512) fp8_rows_kernel(Fp8Args a) {
 
 // --------------------------------------------------------------- many tokens
 // Bound by the issue of matrix instructions and the scaling between them:
-// 4096 x 6144 x 8192 takes 205 us, 2.0 PFLOP/s (a library product of that
-// shape without block scales 2.3; matrix cores 39 % busy).  WN x WT waves, each NT x TT instruction tiles;
+// 4096 x 6144 x 8192 takes 205 to 227 us from one card and run to the next, 1.8
+// to 2.0 PFLOP/s (a library product of that shape without block scales 2.3;
+// matrix cores 39 % busy).  WN x WT waves, each NT x TT instruction tiles;
 // both operands of one block of 128 columns go through LDS, loaded
 // asynchronously two blocks ahead into a ring of three buffers, with the
 // activation scales of each wave's tokens beside them (so that the loop's

@@ -23,12 +23,13 @@
 // workgroup is one or two such fours, 32 or 64 rows.
 //
 // Measured, rank 512, 64 heads: 32 sequences of 16384 rows, one token each,
-// 132 us (4.6 TB/s), four tokens 357 us (0.83 PFLOP/s); trees of four tokens
-// over ragged rows, 10400 on average, 214 us.  One sequence, one token: 1013
-// rows 21 us, 16384 rows 33 us, 65536 rows 40 us.  A tile takes a workgroup
-// 2.6 us, of which matrix instructions are 1.0; the loads stall the waves that
-// issue them for about 0.5 (issued all at once: 4 % slower; some of them after
-// the scores, so that they arrive late: 3 to 9 %).
+// 132 us (4.6 TB/s), four tokens 357 us (0.82 PFLOP/s); trees of four tokens
+// over ragged rows, 10400 on average, 213 to 229 us.  One sequence, one token:
+// 1013 rows 21 us, 16384 rows 34 us, 65536 rows 41 us.  Rank 256: 81, 241, and
+// 16, 29 and 31 us.  A tile takes a workgroup 2.6 us, of which matrix
+// instructions are 1.0; the loads stall the waves that issue them for about 0.5
+// (issued all at once: 4 % slower; some of them after the scores, so that they
+// arrive late: 3 to 9 %).
 //
 // Row blocks of one sequence read the same cache rows, so GS workgroups work
 // as a group: on the same die (one L2), over the same tiles, each on its own
@@ -413,6 +414,8 @@ __global__ void __launch_bounds__(RG * 256, 1) latent_attention_kernel(LatentArg
             for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
             top = half_max(top);
             const bool raise = __any((top - m) * c > kMaxSlack);
+            // the sum takes them before they are rounded to bf16: the roundings
+            // of numerator and denominator do not cancel, but average out
             auto exponentials = [&]() {
                 const float mc = m * c;
                 float sum = 0.0f;
@@ -637,7 +640,7 @@ LatentCut latent_cut(int B, int max_q, int heads, int max_len) {
 }
 
 // Up to this many rows get a workgroup each in the join, so that more of the
-// chip reads the sums: one sequence of 16384 rows 54 to 33 us (64 heads),
+// chip reads the sums: one sequence of 16384 rows 54 to 34 us (64 heads),
 // four tokens of it 37 to 35; at 8 sequences of 4096 a wave per row is
 // better, 30 against 32.
 constexpr long kFewRows = 256;

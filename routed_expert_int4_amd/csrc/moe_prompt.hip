@@ -10,11 +10,12 @@
 // 900 cycles of exponentials and statistics, which the second workgroup on
 // the same CU fills in (half of LDS each).
 //
-// 64 heads of widths 192 and 128, causal: 8192 tokens 1.22 ms, 1.13 PFLOP/s
-// (a large bf16 matrix product reaches 1.50); three sequences of 257 tokens
-// 17 us, where launch and the longest run of tiles count.
-// 4096 tokens, 32 heads: 107 us (64, 64), 163 us (128, 128), 391 us
-// (192, 256; tiles of 64 keys spill: 729).
+// 64 heads of widths 192 and 128, causal: 8192 tokens 1.22 to 1.32 ms from one
+// card and run to the next, 1.05 to 1.13 PFLOP/s (a large bf16 matrix product
+// reaches 1.50); three sequences of 257 tokens 17 us, where launch and the
+// longest run of tiles count.
+// 4096 tokens, 32 heads: 108 us (64, 64), 166 us (128, 128), 387 us (192, 256:
+// 512 registers, of which 10 spill; tiles of 64 keys spill more: 729).
 //
 // A weight of zero times a value that is not finite would still make NaN, so
 // tiles that some query of the wave does not see whole are searched for such
