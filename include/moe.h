@@ -526,9 +526,10 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
  * the launch and the workspace only; a longer one is right as far as max_len
  * goes, but tokens past max_q may be left unwritten).  d_cu_q must not
  * decrease: bounds that name more than T tokens in all leave d_out as it is.
- * Rows of d_q that belong to no sequence are not written in d_out.  rank 512 or 256 with rope 64; scale
- * positive.  moe_latent_attention_workspace: device bytes needed, 256-byte
- * aligned; the buffer's contents need not be kept or cleared. */
+ * Rows of d_q that belong to no sequence are not written in d_out.  At most
+ * 2^26 - 1 rows (tokens times heads) in a sequence; rank 512 or 256 with rope
+ * 64; scale positive.  moe_latent_attention_workspace: device bytes needed,
+ * 256-byte aligned; the buffer's contents need not be kept or cleared. */
 size_t moe_latent_attention_workspace(int B, int max_q, int heads, int rank, int max_len);
 moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, int T, int heads,
                                   int rank, int rope, const uint16_t* d_cache, int n_pages, int page_size,
