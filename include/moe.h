@@ -473,6 +473,22 @@ moe_status_t moe_fp8_linear(const uint8_t* d_a, int64_t a_stride, const float* d
                             int64_t ws_stride, int M, int N, int K, void* d_out, int out_type, int64_t out_stride,
                             void* stream);
 
+/* moe_int4_linear: out[m][n] = sum_g scale[n][g] sum_{k in g} q[n][k] x[m][k]
+ * over groups g of `group` inner columns (32, 64 or 128): a product with 4-bit
+ * weights in the experts' format, for the resident projections of a model
+ * (colibri summary, "Principales fonctionnalites": packed int4 with
+ * dequant-on-use).  x [M][K] bf16; d_w [N][K / 2] two's complement nibbles, the
+ * even column in the low one; d_scale fp16 [N][K / group]; out [M][N] bf16 or
+ * fp32 (out_type).  Weights are used as they are (a code and its scale enter
+ * separately), sums are fp32.  K a multiple of the group; x 16-byte aligned,
+ * its stride a multiple of 8; w 16-byte aligned, its stride (bytes) a multiple
+ * of 16 (else MOE_EUNSUPPORTED); M x N at most 2^38.  Sums hold 1.5 + q / 16
+ * and take the 1.5 away again, so activations above 2^120 may overflow, and a
+ * token with an infinity gives NaN or an infinity. */
+moe_status_t moe_int4_linear(const uint16_t* d_x, int64_t x_stride, const uint8_t* d_w, int64_t w_stride,
+                             const uint16_t* d_scale, int64_t scale_stride, int group, int M, int N, int K, void* d_out,
+                             int out_type, int64_t out_stride, void* stream);
+
 /* moe_head_linear: out[t][h][n] = sum_k x[t][h][k] w[h][n][k], bf16; w is
  * contiguous.  The absorbed form of latent attention applies it to the
  * queries before (w = the key expansion, transposed per head) and to the

@@ -4,6 +4,7 @@ layers of a model with latent attention, as calls on torch tensors.
     add_rmsnorm       residual addition and root-mean-square norm, bf16 and / or 8-bit output
     quantize          8-bit codes and scales alone
     fp8_linear        8-bit product with a scale per 128 columns (activations) and 128 x 128 block (weights)
+    int4_linear       product with 4-bit weights and a scale per group of 32, 64 or 128 columns
     head_linear       one product per head (queries into the latent space, outputs back out)
     latent_append     norm, rotation and write of new rows of the latent cache
     latent_attention  attention over the paged latent cache (single tokens, chunks, trees of drafted tokens)
@@ -27,8 +28,10 @@ from . import binding as B
 _BF16, _F32, _FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _TYPES = {_BF16: 0, _F32: 1}  # MOE_BF16, MOE_F32
 _WIDE, _BF16_ONLY, _FP8_ONLY, _F32_ONLY = (_BF16, _F32), (_BF16,), (_FP8,), (_F32,)
+_U8_ONLY, _F16_ONLY = (torch.uint8,), (torch.float16,)
 _I32_ONLY, _I64_ONLY = (torch.int32,), (torch.int64,)
 GROUP = 128                   # columns (and weight rows) that share a scale
+_GROUPS = (32, 64, 128)       # columns that share a scale of 4-bit weights
 
 
 class NormOut(NamedTuple):
@@ -201,6 +204,49 @@ def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -
                                    as_strides[1], w.data_ptr(), w_strides[0] if N > 1 else pad, w_scale.data_ptr(),
                                    ws_strides[0] if nb > 1 else kb, M, N, K, out.data_ptr(), _TYPES[out_dtype], o_stride,
                                    _raw_stream(on)))
+    return out
+
+
+def quantize_weight_int4(w, group: int = 32):
+    """A weight [N, K] in 4 bits with one fp16 scale per `group` (32, 64 or
+    128) columns of a row, as int4_linear reads it: (codes uint8 [N, K / 2],
+    scales [N, K / group]).  The largest magnitude of a group gets code 7 or
+    -7.  Done once when a model is loaded, in torch."""
+    N, K = w.shape
+    _need(group in _GROUPS and K % group == 0, f"groups of {group} columns (32, 64 or 128) in rows of {K}")
+    blocks = w.float().view(N, K // group, group)
+    scale = (blocks.abs().amax(2) / 7).clamp_(2.0 ** -24, 65504.0).half()  # finite, and not zero
+    q = (blocks / scale.float()[:, :, None]).round_().clamp_(-8, 7).view(N, K).to(torch.int32)
+    return ((q[:, 0::2] & 15) | (q[:, 1::2] & 15) << 4).to(torch.uint8), scale
+
+
+def int4_linear(x, codes, scale, out_dtype=_BF16, out=None, stream=None) -> torch.Tensor:
+    """x [M, K] bf16 times the transpose of a 4-bit weight: codes uint8
+    [N, K / 2] (two's complement nibbles, the even column in the low one) with
+    scale fp16 [N, K / group], group 32, 64 or 128: [M, N] in out_dtype (bf16
+    or fp32).  Rows of x and codes start on 16 bytes."""
+    on = x.get_device()
+    if stream is not None or on < 0 or on != _device():
+        return _elsewhere(stream, int4_linear, x, codes, scale, out_dtype, out)
+    (M, K), x_strides = _rows(x, "x", 2, _BF16_ONLY, on)
+    (N, half), w_strides = _rows(codes, "codes", 2, _U8_ONLY, on)
+    (rows, groups), s_strides = _rows(scale, "scale", 2, _F16_ONLY, on)
+    group = K // groups if groups else 0
+    if half * 2 != K or rows != N or group not in _GROUPS or group * groups != K:
+        _need(False, f"x {(M, K)} needs codes (N, {K // 2}) and scales (N, {K} / 32, 64 or 128), got {(N, half)} and "
+                     f"{(rows, groups)}")
+    if out is None:
+        _need(out_dtype in _TYPES, f"out_dtype {out_dtype}: bf16 or fp32")
+        out, o_stride = torch.empty((M, N), dtype=out_dtype, device=on), N
+    else:
+        o_shape, o_strides = _rows(out, "out", 2, _WIDE, on)
+        _need(tuple(o_shape) == (M, N), f"out {tuple(o_shape)}, {(M, N)} is needed")
+        out_dtype, o_stride = out.dtype, o_strides[0] if M > 1 else N
+    # the stride of a single row says nothing
+    B.check(B.lib().moe_int4_linear(x.data_ptr(), x_strides[0] if M > 1 else K, codes.data_ptr(),
+                                    w_strides[0] if N > 1 else -(-half // 16) * 16, scale.data_ptr(),
+                                    s_strides[0] if N > 1 else groups, group, M, N, K, out.data_ptr(), _TYPES[out_dtype],
+                                    o_stride, _raw_stream(on)))
     return out
 
 

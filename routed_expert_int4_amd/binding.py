@@ -99,6 +99,7 @@ _SIGNATURES = {
     "expert_cache_timeline_read": ([_vp, ctypes.POINTER(MoeCacheTimeline)], _i),
     "moe_add_rmsnorm": ([_vp, _i, _l, _vp, _i, _l, _vp, _i, _i, _i, _f, _vp, _l, _vp, _l, _vp, _l, _vp, _l, _l, _vp], _i),
     "moe_fp8_linear": ([_vp, _l, _vp, _l, _l, _vp, _l, _vp, _l, _i, _i, _i, _vp, _i, _l, _vp], _i),
+    "moe_int4_linear": ([_vp, _l, _vp, _l, _vp, _l, _i, _i, _i, _i, _vp, _i, _l, _vp], _i),
     "moe_head_linear": ([_vp, _l, _l, _vp, _i, _i, _i, _i, _vp, _l, _l, _vp], _i),
     "moe_latent_append": ([_vp, _l, _vp, _i, _f, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _l, _vp, _i, _l, _l, _vp, _l, _l,
                            _vp, _l, _vp, _l, _l, _vp, _l, _vp], _i),

@@ -69,6 +69,17 @@ struct Fp8Args {
 };
 hipError_t launch_fp8_linear(const Fp8Args& a, hipStream_t s);
 
+struct Int4Args {
+    const uint16_t* x;      // [M][K] bf16
+    const uint8_t* w;       // [N][K / 2]
+    const uint16_t* scale;  // [N][K / group] fp16
+    void* out;              // [M][N]
+    long ldx, ldw, lds, ldo;
+    int M, N, K, group;
+    bool out_f32;
+};
+hipError_t launch_int4_linear(const Int4Args& a, hipStream_t s);
+
 struct LatentArgs {
     const uint16_t* q;      // [T][heads][rank + rope]
     const uint16_t* cache;  // [n_pages][page_size][rank + rope]

@@ -83,6 +83,33 @@ moe_status_t moe_fp8_linear(const uint8_t* d_a, int64_t a_stride, const float* d
     return launched(launch_fp8_linear(a, static_cast<hipStream_t>(stream)), who);
 }
 
+moe_status_t moe_int4_linear(const uint16_t* d_x, int64_t x_stride, const uint8_t* d_w, int64_t w_stride,
+                             const uint16_t* d_scale, int64_t scale_stride, int group, int M, int N, int K, void* d_out,
+                             int out_type, int64_t out_stride, void* stream) {
+    const char* who = "moe_int4_linear";
+    if (M < 0 || N < 1 || K < 1) return fail(MOE_EINVAL, "%s: M (%d), N (%d), K (%d)", who, M, N, K);
+    if (group != 32 && group != 64 && group != 128)
+        return fail(MOE_EUNSUPPORTED, "%s: groups of %d columns (32, 64 or 128)", who, group);
+    if (K % group) return fail(MOE_EINVAL, "%s: K (%d) is not a multiple of the group (%d)", who, K, group);
+    if (!type_ok(out_type)) return fail(MOE_EINVAL, "%s: unknown output type %d", who, out_type);
+    if (M == 0) return MOE_OK;
+    if (!d_x || !d_w || !d_scale || !d_out) return fail(MOE_EINVAL, "%s: NULL pointer", who);
+    if (x_stride < K || w_stride < K / 2 || scale_stride < K / group || out_stride < N)
+        return fail(MOE_EINVAL, "%s: a row stride is below its row", who);
+    if (x_stride % 8 || w_stride % 16 || !on(d_x, 16) || !on(d_w, 16))
+        return fail(MOE_EUNSUPPORTED, "%s: the strides of x and w must be multiples of 16 bytes, both 16-byte aligned", who);
+    if (!on(d_scale, 2) || !on(d_out, out_type == MOE_F32 ? 4 : 2))
+        return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
+    // grids count lanes in 32 bits, and the largest tile is 128 x 256
+    if ((int64_t)M * N > (int64_t)1 << 38) return fail(MOE_EUNSUPPORTED, "%s: M x N (%d x %d) is over 2^38", who, M, N);
+    Int4Args a{};
+    a.x = d_x, a.w = d_w, a.scale = d_scale, a.out = d_out;
+    a.ldx = x_stride, a.ldw = w_stride, a.lds = scale_stride, a.ldo = out_stride;
+    a.M = M, a.N = N, a.K = K, a.group = group;
+    a.out_f32 = out_type == MOE_F32;
+    return launched(launch_int4_linear(a, static_cast<hipStream_t>(stream)), who);
+}
+
 moe_status_t moe_head_linear(const uint16_t* d_x, int64_t x_stride_t, int64_t x_stride_h, const uint16_t* d_w, int T,
                              int heads, int K, int N, uint16_t* d_out, int64_t out_stride_t, int64_t out_stride_h,
                              void* stream) {
