@@ -521,6 +521,29 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
                                uint8_t* d_lat_q, int64_t lat_stride, float* d_lat_scale, int64_t ls_stride_t,
                                int64_t ls_stride_g, uint16_t* d_rows, int64_t rows_stride, void* stream);
 
+/* The latent cache in 8 bits: row s of d_cache holds rank E4M3 codes and then
+ * rope bf16 values (rank + 2 rope bytes), d_cache_scale[s] the power of two
+ * that its codes are multiples of: the least that brings the row's largest
+ * finite magnitude to at most 448 (at least 2^-100; 1 for a row of zeros).
+ * Codes are rounded to nearest once, from fp32; what is not finite becomes NaN.
+ * Values code x scale are exact in bf16.  At rank 512 and rope 64 a token
+ * takes 644 bytes with its scale, against 1152 in bf16.
+ *
+ * moe_latent_append_fp8: moe_latent_append into such a cache (d_rows, if
+ * given, receives the rows in bf16 before their rounding to codes).  rank a
+ * multiple of 16.
+ * moe_latent_read_fp8: rows d_slots[t] as bf16, d_out [T][rank + rope]; a slot
+ * outside [0, n_slots) reads as zeros.  What a prompt's key and value
+ * expansion takes for tokens that are cached already. */
+moe_status_t moe_latent_append_fp8(const uint16_t* d_kv, int64_t kv_stride, const void* d_weight, int weight_type,
+                                   float eps, int rank, int rope, const float* d_table, int n_positions,
+                                   const int32_t* d_positions, const int64_t* d_slots, int T, uint8_t* d_cache,
+                                   float* d_cache_scale, int64_t n_slots, const uint16_t* d_q_rope, int heads,
+                                   int64_t q_stride_t, int64_t q_stride_h, uint16_t* d_q_out, int64_t qo_stride_t,
+                                   int64_t qo_stride_h, uint16_t* d_rows, int64_t rows_stride, void* stream);
+moe_status_t moe_latent_read_fp8(const uint8_t* d_cache, const float* d_cache_scale, int64_t n_slots, int rank, int rope,
+                                 const int64_t* d_slots, int T, uint16_t* d_out, int64_t out_stride, void* stream);
+
 /* moe_latent_attention: attention over the paged latent cache, absorbed form.
  * d_q [T][heads][rank + rope] (queries already in the latent space, and their
  * rotated position part); d_cache [n_pages] pages of page_size rows of rank +

@@ -6,7 +6,8 @@ layers of a model with latent attention, as calls on torch tensors.
     fp8_linear        8-bit product with a scale per 128 columns (activations) and 128 x 128 block (weights)
     int4_linear       product with 4-bit weights and a scale per group of 32, 64 or 128 columns
     head_linear       one product per head (queries into the latent space, outputs back out)
-    latent_append     norm, rotation and write of new rows of the latent cache
+    latent_append     norm, rotation and write of new rows of the latent cache (bf16, or 8 bits)
+    latent_read       rows of an 8-bit latent cache as bf16
     latent_attention  attention over the paged latent cache (single tokens, chunks, trees of drafted tokens)
     prompt_attention  the same attention with keys and values expanded per head, for prompts
 
@@ -273,7 +274,7 @@ def head_linear(x, w, out=None, stream=None) -> torch.Tensor:
 
 
 def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_rope=None, q_out=None,
-                  want_fp8: bool = False, want_key: bool = False, stream=None) -> AppendOut:
+                  want_fp8: bool = False, want_key: bool = False, stream=None, cache_scale=None) -> AppendOut:
     """Norms the latents and rotates the position parts of new tokens and
     writes them to their rows of the cache.
 
@@ -282,11 +283,17 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
     cache, page * page_size + place; negative: not written), cache [pages,
     page_size, rank + rope] contiguous.  q_rope [T, heads, rope] is rotated
     into q_out (given, the view itself for in place, or new).  want_fp8: the
-    normed latent in 8 bits too; want_key: the rotated key part too."""
+    normed latent in 8 bits too; want_key: the rotated key part too.
+
+    With cache_scale (fp32, contiguous, one value per row of the cache) the
+    cache holds 8 bits: uint8 [pages, page_size, rank + 2 rope], a row being
+    rank E4M3 codes and the rotated part's bf16 bytes, and cache_scale
+    receives the row's power of two (want_fp8 is not for this cache; want_key's
+    rows are those before their rounding to codes)."""
     on = kv.get_device()
     if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, latent_append, kv, weight, eps, table, positions, slots, cache, q_rope, q_out,
-                          want_fp8, want_key)
+                          want_fp8, want_key, None, cache_scale)
     (T, width), kvs = _rows(kv, "kv", 2, _BF16_ONLY, on)
     (rank,), _ = _rows(weight, "weight", 1, _WIDE, on)
     (n_positions, rope), _ = _rows(table, "table", 2, _F32_ONLY, on)
@@ -296,14 +303,20 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
                      "contiguous")
     cache_p = slots_p = None
     n_slots = 0
-    if cache is not None:
+    if cache_scale is not None:
+        _need(cache is not None and slots is not None and not want_fp8, "cache_scale goes with a cache of 8 bits and slots, "
+              "and without want_fp8")
+        n_slots = _narrow_rows(cache, cache_scale, width + rope, on)
+    elif cache is not None:
         if cache.dtype is not _BF16 or cache.get_device() != on or not cache.is_contiguous() or cache.shape[-1] != width:
             _need(False, f"cache: contiguous bf16 rows of {width} on cuda:{on} are needed, got {cache.dtype} "
                          f"{tuple(cache.shape)} on {cache.device}")
         _need(slots is not None, "a cache needs slots")
+        n_slots = cache.numel() // width
+    if cache is not None:
         (n,), _ = _rows(slots, "slots", 1, _I64_ONLY, on)
         _need(n == T, f"{n} slots for {T} tokens")
-        cache_p, slots_p, n_slots = cache.data_ptr(), slots.data_ptr(), cache.numel() // width
+        cache_p, slots_p = cache.data_ptr(), slots.data_ptr()
     heads, qs, qo, qp, qop = 0, (0, 0), (0, 0), None, None
     if q_rope is not None:
         q_shape, qs = _rows(q_rope, "q_rope", 3, _BF16_ONLY, on)
@@ -323,11 +336,50 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
     if want_key:
         rows = torch.empty((T, width), dtype=_BF16, device=on)
         rows_p = rows.data_ptr()
+    if cache_scale is not None:
+        B.check(B.lib().moe_latent_append_fp8(
+            kv.data_ptr(), kvs[0] if T > 1 else width, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
+            table.data_ptr(), n_positions, positions.data_ptr(), slots_p, T, cache_p, cache_scale.data_ptr(), n_slots, qp,
+            heads, qs[0], qs[1], qop, qo[0], qo[1], rows_p, width, _raw_stream(on)))
+        return AppendOut(q_out if q_rope is not None else None, None, None, rows[:, rank:] if want_key else None, rows)
     B.check(B.lib().moe_latent_append(
         kv.data_ptr(), kvs[0] if T > 1 else width, weight.data_ptr(), _TYPES[weight.dtype], eps, rank, rope,
         table.data_ptr(), n_positions, positions.data_ptr(), slots_p, T, cache_p, n_slots, qp, heads, qs[0], qs[1],
         qop, qo[0], qo[1], q_p, -(-rank // 16) * 16, scale_p, 1, T, rows_p, width, _raw_stream(on)))
     return AppendOut(q_out if q_rope is not None else None, q, scale, rows[:, rank:] if want_key else None, rows)
+
+
+def _narrow_rows(cache, cache_scale, row: int, on: int) -> int:
+    """Rows of a cache of 8 bits with `row` bytes each and its scales."""
+    if (cache.dtype is not torch.uint8 or cache.get_device() != on or not cache.is_contiguous() or cache.shape[-1] != row
+            or cache_scale.dtype is not _F32 or cache_scale.get_device() != on or not cache_scale.is_contiguous()
+            or cache_scale.numel() * row != cache.numel()):
+        _need(False, f"a cache of 8 bits: contiguous uint8 rows of {row} and an fp32 scale for each, on cuda:{on}, are "
+                     f"needed, got {cache.dtype} {tuple(cache.shape)} on {cache.device} and {cache_scale.dtype} "
+                     f"{tuple(cache_scale.shape)} on {cache_scale.device}")
+    return cache_scale.numel()
+
+
+def latent_read(cache, cache_scale, slots, rope: int = 64, out=None, stream=None) -> torch.Tensor:
+    """Rows slots (int64 [T]) of a cache of 8 bits (uint8 [pages, page_size,
+    rank + 2 rope] with cache_scale) as bf16 [T, rank + rope], which holds
+    their values exactly; a slot outside the cache reads as zeros."""
+    on = cache.get_device()
+    if stream is not None or on < 0 or on != _device():
+        return _elsewhere(stream, latent_read, cache, cache_scale, slots, rope, out)
+    n_slots = _narrow_rows(cache, cache_scale, cache.shape[-1], on)
+    (T,), _ = _rows(slots, "slots", 1, _I64_ONLY, on)
+    width = cache.shape[-1] - rope
+    _need(width > rope > 0, f"rows of {cache.shape[-1]} bytes do not hold {rope} position values and codes")
+    if out is None:
+        out, o_stride = torch.empty((T, width), dtype=_BF16, device=on), width
+    else:
+        o_shape, o_strides = _rows(out, "out", 2, _BF16_ONLY, on)
+        _need(tuple(o_shape) == (T, width), f"out {tuple(o_shape)}, {(T, width)} is needed")
+        o_stride = o_strides[0] if T > 1 else width
+    B.check(B.lib().moe_latent_read_fp8(cache.data_ptr(), cache_scale.data_ptr(), n_slots, width - rope, rope, slots.data_ptr(),
+                                        T, out.data_ptr(), o_stride, _raw_stream(on)))
+    return out
 
 
 def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = None, cu_q=None,

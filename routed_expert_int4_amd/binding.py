@@ -103,6 +103,9 @@ _SIGNATURES = {
     "moe_head_linear": ([_vp, _l, _l, _vp, _i, _i, _i, _i, _vp, _l, _l, _vp], _i),
     "moe_latent_append": ([_vp, _l, _vp, _i, _f, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _l, _vp, _i, _l, _l, _vp, _l, _l,
                            _vp, _l, _vp, _l, _l, _vp, _l, _vp], _i),
+    "moe_latent_append_fp8": ([_vp, _l, _vp, _i, _f, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _l, _vp, _i, _l, _l, _vp, _l,
+                               _l, _vp, _l, _vp], _i),
+    "moe_latent_read_fp8": ([_vp, _vp, _l, _i, _i, _vp, _i, _vp, _l, _vp], _i),
     "moe_latent_attention_workspace": ([_i] * 5, _sz),
     "moe_latent_attention": ([_vp, _l, _l, _i, _i, _i, _i, _vp, _i, _i, _l, _vp, _l, _i, _vp, _i, _vp, _i, _i, _vp, _f,
                               _vp, _l, _l, _vp, _sz, _vp], _i),

@@ -33,6 +33,8 @@ struct AppendArgs {
     const int32_t* positions;
     const int64_t* slots;
     uint16_t* cache;           // [n_slots][rank + rope], or nullptr
+    uint8_t* cache8;           // [n_slots] rows of rank codes and rope bf16 values, or nullptr
+    float* cache_scale;        // [n_slots], of cache8
     const uint16_t* q;         // [T][heads][rope] strided, or nullptr
     uint16_t* q_out;
     uint8_t* lat_q;            // [T][rank] E4M3, or nullptr
@@ -46,6 +48,16 @@ struct AppendArgs {
 };
 hipError_t launch_latent_append(const AppendArgs& a, hipStream_t s);
 constexpr int kAppendMaxRank = 2048;
+
+struct ReadArgs {
+    const uint8_t* cache;   // [n_slots] rows of rank codes and rope bf16 values
+    const float* scale;     // [n_slots]
+    const int64_t* slots;   // [T]
+    uint16_t* out;          // [T][rank + rope]
+    long n_slots, o_stride;
+    int T, rank, rope;
+};
+hipError_t launch_latent_read(const ReadArgs& a, hipStream_t s);
 
 struct HeadArgs {
     const uint16_t* x;

@@ -19,6 +19,49 @@ bool stride_fits(int64_t bytes) { return bytes >= 0 && bytes < (int64_t)1 << 23;
 
 moe_status_t launched(hipError_t e, const char* who) { return e == hipSuccess ? MOE_OK : hip_fail(e, who); }
 
+// The bf16 cache or the 8-bit one (with its scales), or neither.
+moe_status_t append(const char* who, uint8_t* d_cache8, float* d_cache_scale, const uint16_t* d_kv, int64_t kv_stride,
+                    const void* d_weight, int weight_type, float eps, int rank, int rope, const float* d_table,
+                    int n_positions, const int32_t* d_positions, const int64_t* d_slots, int T, uint16_t* d_cache,
+                    int64_t n_slots, const uint16_t* d_q_rope, int heads, int64_t q_stride_t, int64_t q_stride_h,
+                    uint16_t* d_q_out, int64_t qo_stride_t, int64_t qo_stride_h, uint8_t* d_lat_q, int64_t lat_stride,
+                    float* d_lat_scale, int64_t ls_stride_t, int64_t ls_stride_g, uint16_t* d_rows, int64_t rows_stride,
+                    void* stream) {
+    if (T < 0 || rank < 1 || rope < 1 || n_positions < 0 || n_slots < 0 || (d_q_rope && heads < 1))
+        return fail(MOE_EINVAL, "%s: T (%d), rank (%d), rope (%d), heads (%d), positions (%d) or slots", who, T, rank,
+                    rope, heads, n_positions);
+    if (!type_ok(weight_type)) return fail(MOE_EINVAL, "%s: unknown weight type %d", who, weight_type);
+    if (!(eps >= 0.0f)) return fail(MOE_EINVAL, "%s: eps must be >= 0", who);
+    if (T == 0) return MOE_OK;
+    if (!d_kv || !d_weight || !d_table || !d_positions) return fail(MOE_EINVAL, "%s: NULL pointer", who);
+    if ((d_cache || d_cache8) && !d_slots) return fail(MOE_EINVAL, "%s: a cache without slots", who);
+    if (!d_q_rope != !d_q_out) return fail(MOE_EINVAL, "%s: queries need both an input and an output", who);
+    if (!d_lat_q != !d_lat_scale) return fail(MOE_EINVAL, "%s: the 8-bit latent needs codes and scales", who);
+    if (!d_cache && !d_cache8 && !d_q_rope && !d_lat_q && !d_rows) return fail(MOE_EINVAL, "%s: no output", who);
+    if (kv_stride < rank + rope || (d_lat_q && lat_stride < rank) || (d_rows && rows_stride < rank + rope))
+        return fail(MOE_EINVAL, "%s: a row stride is below its row", who);
+    if (rank > kAppendMaxRank) return fail(MOE_EUNSUPPORTED, "%s: rank (%d) is over %d", who, rank, kAppendMaxRank);
+    if (rank % 8 || rope % 8 || kv_stride % 8 || q_stride_t % 8 || q_stride_h % 8 || qo_stride_t % 8 ||
+        qo_stride_h % 8 || lat_stride % 8 || rows_stride % 8 || !on(d_kv, 16) || !on(d_weight, 16) ||
+        !on(d_cache, 16) || !on(d_q_rope, 16) || !on(d_q_out, 16) || !on(d_lat_q, 8) || !on(d_rows, 16))
+        return fail(MOE_EUNSUPPORTED, "%s: rank, rope and the strides must be multiples of 8, pointers 16-byte aligned",
+                    who);
+    if (d_cache8 && (rank % 16 || !on(d_cache8, 16)))
+        return fail(MOE_EUNSUPPORTED, "%s: rows of 8 bits need a rank (%d) that is a multiple of 16, 16-byte aligned", who,
+                    rank);
+    if (!on(d_table, 4) || !on(d_positions, 4) || !on(d_slots, 8) || !on(d_lat_scale, 4) || !on(d_cache_scale, 4))
+        return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
+    AppendArgs a{};
+    a.kv = d_kv, a.weight = d_weight, a.table = d_table, a.positions = d_positions, a.slots = d_slots;
+    a.cache = d_cache, a.cache8 = d_cache8, a.cache_scale = d_cache_scale, a.q = d_q_rope, a.q_out = d_q_out, a.lat_q = d_lat_q, a.lat_scale = d_lat_scale, a.rows = d_rows;
+    a.kv_stride = kv_stride, a.n_slots = n_slots, a.q_stride_t = q_stride_t, a.q_stride_h = q_stride_h;
+    a.qo_stride_t = qo_stride_t, a.qo_stride_h = qo_stride_h, a.lat_stride = lat_stride, a.ls_stride_t = ls_stride_t;
+    a.ls_stride_g = ls_stride_g, a.rows_stride = rows_stride;
+    a.T = T, a.rank = rank, a.rope = rope, a.heads = heads, a.n_positions = n_positions, a.eps = eps;
+    a.weight_f32 = weight_type == MOE_F32;
+    return launched(launch_latent_append(a, static_cast<hipStream_t>(stream)), who);
+}
+
 }  // namespace
 
 extern "C" {
@@ -138,37 +181,44 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
                                int64_t q_stride_h, uint16_t* d_q_out, int64_t qo_stride_t, int64_t qo_stride_h,
                                uint8_t* d_lat_q, int64_t lat_stride, float* d_lat_scale, int64_t ls_stride_t,
                                int64_t ls_stride_g, uint16_t* d_rows, int64_t rows_stride, void* stream) {
-    const char* who = "moe_latent_append";
-    if (T < 0 || rank < 1 || rope < 1 || n_positions < 0 || n_slots < 0 || (d_q_rope && heads < 1))
-        return fail(MOE_EINVAL, "%s: T (%d), rank (%d), rope (%d), heads (%d), positions (%d) or slots", who, T, rank,
-                    rope, heads, n_positions);
-    if (!type_ok(weight_type)) return fail(MOE_EINVAL, "%s: unknown weight type %d", who, weight_type);
-    if (!(eps >= 0.0f)) return fail(MOE_EINVAL, "%s: eps must be >= 0", who);
+    return append("moe_latent_append", nullptr, nullptr, d_kv, kv_stride, d_weight, weight_type, eps, rank, rope, d_table,
+                  n_positions, d_positions, d_slots, T, d_cache, n_slots, d_q_rope, heads, q_stride_t, q_stride_h, d_q_out,
+                  qo_stride_t, qo_stride_h, d_lat_q, lat_stride, d_lat_scale, ls_stride_t, ls_stride_g, d_rows, rows_stride,
+                  stream);
+}
+
+moe_status_t moe_latent_append_fp8(const uint16_t* d_kv, int64_t kv_stride, const void* d_weight, int weight_type,
+                                   float eps, int rank, int rope, const float* d_table, int n_positions,
+                                   const int32_t* d_positions, const int64_t* d_slots, int T, uint8_t* d_cache,
+                                   float* d_cache_scale, int64_t n_slots, const uint16_t* d_q_rope, int heads,
+                                   int64_t q_stride_t, int64_t q_stride_h, uint16_t* d_q_out, int64_t qo_stride_t,
+                                   int64_t qo_stride_h, uint16_t* d_rows, int64_t rows_stride, void* stream) {
+    const char* who = "moe_latent_append_fp8";
+    if (T > 0 && (!d_cache || !d_cache_scale)) return fail(MOE_EINVAL, "%s: NULL cache or scales", who);
+    return append(who, d_cache, d_cache_scale, d_kv, kv_stride, d_weight, weight_type, eps, rank, rope, d_table, n_positions,
+                  d_positions, d_slots, T, nullptr, n_slots, d_q_rope, heads, q_stride_t, q_stride_h, d_q_out, qo_stride_t,
+                  qo_stride_h, nullptr, 0, nullptr, 0, 0, d_rows, rows_stride, stream);
+}
+
+moe_status_t moe_latent_read_fp8(const uint8_t* d_cache, const float* d_cache_scale, int64_t n_slots, int rank, int rope,
+                                 const int64_t* d_slots, int T, uint16_t* d_out, int64_t out_stride, void* stream) {
+    const char* who = "moe_latent_read_fp8";
+    if (T < 0 || rank < 1 || rope < 1 || n_slots < 0)
+        return fail(MOE_EINVAL, "%s: T (%d), rank (%d), rope (%d) or slots", who, T, rank, rope);
     if (T == 0) return MOE_OK;
-    if (!d_kv || !d_weight || !d_table || !d_positions) return fail(MOE_EINVAL, "%s: NULL pointer", who);
-    if (d_cache && !d_slots) return fail(MOE_EINVAL, "%s: a cache without slots", who);
-    if (!d_q_rope != !d_q_out) return fail(MOE_EINVAL, "%s: queries need both an input and an output", who);
-    if (!d_lat_q != !d_lat_scale) return fail(MOE_EINVAL, "%s: the 8-bit latent needs codes and scales", who);
-    if (!d_cache && !d_q_rope && !d_lat_q && !d_rows) return fail(MOE_EINVAL, "%s: no output", who);
-    if (kv_stride < rank + rope || (d_lat_q && lat_stride < rank) || (d_rows && rows_stride < rank + rope))
-        return fail(MOE_EINVAL, "%s: a row stride is below its row", who);
-    if (rank > kAppendMaxRank) return fail(MOE_EUNSUPPORTED, "%s: rank (%d) is over %d", who, rank, kAppendMaxRank);
-    if (rank % 8 || rope % 8 || kv_stride % 8 || q_stride_t % 8 || q_stride_h % 8 || qo_stride_t % 8 ||
-        qo_stride_h % 8 || lat_stride % 8 || rows_stride % 8 || !on(d_kv, 16) || !on(d_weight, 16) ||
-        !on(d_cache, 16) || !on(d_q_rope, 16) || !on(d_q_out, 16) || !on(d_lat_q, 8) || !on(d_rows, 16))
-        return fail(MOE_EUNSUPPORTED, "%s: rank, rope and the strides must be multiples of 8, pointers 16-byte aligned",
+    if (!d_slots || !d_out || (n_slots > 0 && (!d_cache || !d_cache_scale))) return fail(MOE_EINVAL, "%s: NULL pointer", who);
+    if (out_stride < rank + rope) return fail(MOE_EINVAL, "%s: a row stride is below its row", who);
+    if (rank % 16 || rope % 8 || out_stride % 8 || !on(d_cache, 16) || !on(d_out, 16))
+        return fail(MOE_EUNSUPPORTED, "%s: rank must be a multiple of 16, rope and the stride of 8, pointers 16-byte aligned",
                     who);
-    if (!on(d_table, 4) || !on(d_positions, 4) || !on(d_slots, 8) || !on(d_lat_scale, 4))
-        return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
-    AppendArgs a{};
-    a.kv = d_kv, a.weight = d_weight, a.table = d_table, a.positions = d_positions, a.slots = d_slots;
-    a.cache = d_cache, a.q = d_q_rope, a.q_out = d_q_out, a.lat_q = d_lat_q, a.lat_scale = d_lat_scale, a.rows = d_rows;
-    a.kv_stride = kv_stride, a.n_slots = n_slots, a.q_stride_t = q_stride_t, a.q_stride_h = q_stride_h;
-    a.qo_stride_t = qo_stride_t, a.qo_stride_h = qo_stride_h, a.lat_stride = lat_stride, a.ls_stride_t = ls_stride_t;
-    a.ls_stride_g = ls_stride_g, a.rows_stride = rows_stride;
-    a.T = T, a.rank = rank, a.rope = rope, a.heads = heads, a.n_positions = n_positions, a.eps = eps;
-    a.weight_f32 = weight_type == MOE_F32;
-    return launched(launch_latent_append(a, static_cast<hipStream_t>(stream)), who);
+    if (!on(d_cache_scale, 4) || !on(d_slots, 8)) return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
+    // grids count lanes in 32 bits, 16 bytes of a row each
+    if (rank > kAppendMaxRank || (int64_t)T * ((rank + 2 * (int64_t)rope) / 16) >= (int64_t)1 << 32)
+        return fail(MOE_EUNSUPPORTED, "%s: rank over %d, or too many rows", who, kAppendMaxRank);
+    ReadArgs a{};
+    a.cache = d_cache, a.scale = d_cache_scale, a.slots = d_slots, a.out = d_out;
+    a.n_slots = n_slots, a.o_stride = out_stride, a.T = T, a.rank = rank, a.rope = rope;
+    return launched(launch_latent_read(a, static_cast<hipStream_t>(stream)), who);
 }
 
 size_t moe_latent_attention_workspace(int B, int max_q, int heads, int rank, int max_len) {

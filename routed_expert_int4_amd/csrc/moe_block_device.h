@@ -58,6 +58,22 @@ __device__ __forceinline__ float group_scale(unsigned top) {
     return s < 1e-12f ? 1e-12f : s;
 }
 
+// 8-bit cache rows: E4M3 codes times a power of two.  A code has 4 bits of
+// significand, so a row's values are exact in bf16.
+// The least power of two that brings magnitudes up to the one with the bits
+// `top` (finite) into the codes' range; 1 for zero.
+__device__ __forceinline__ float row_power(unsigned top) {
+    const int e = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u);  // 448 = 1.75 * 2^8
+    return top == 0 ? 1.0f : __builtin_bit_cast(float, (unsigned)(e < 27 ? 27 : e) << 23);  // 2^-100 and up
+}
+// Eight codes as bf16.
+__device__ __forceinline__ u32x4 codes_to_bf16(unsigned lo, unsigned hi, float scale) {
+    return u32x4{__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false)),
+                 __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true)),
+                 __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false)),
+                 __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
+}
+
 // 16 bytes per lane from global memory straight into LDS: lane l's bytes land
 // at dst + 16 l.  dst is wave-uniform.  Written in assembly because the
 // compiler drains every outstanding one before the next LDS read of any

@@ -185,7 +185,9 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
     const uint16_t* kv = a.kv + t * a.kv_stride;
     // a slot outside the pool writes no row; a position outside the table
     // has no angle and rotates to NaN
-    uint16_t* row = a.cache && slot >= 0 && slot < a.n_slots ? a.cache + slot * (a.rank + a.rope) : nullptr;
+    const bool placed = slot >= 0 && slot < a.n_slots;
+    uint16_t* row = a.cache && placed ? a.cache + slot * (a.rank + a.rope) : nullptr;
+    uint8_t* row8 = a.cache8 && placed ? a.cache8 + slot * (a.rank + 2 * a.rope) : nullptr;
     const bool known = pos >= 0 && pos < a.n_positions;
     const float* angle = a.table + (known ? (long)pos * a.rope : 0);
     const u32x4 nan = {0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
@@ -218,6 +220,34 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
             if (a.lat_q)
                 store_fp8<true>(y, c, a.rank, a.lat_q + t * a.lat_stride, a.lat_scale + t * a.ls_stride_t,
                                 a.ls_stride_g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = y[j];
+        }
+        if (row8) {
+            // one power of two for the row, from its largest finite value;
+            // what is not finite becomes NaN
+            unsigned top = 0;
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const unsigned m = __builtin_bit_cast(unsigned, v[i][j]) & 0x7FFFFFFFu;
+                    if (m >= 0x7F800000u)
+                        v[i][j] = __builtin_nanf("");
+                    else
+                        top = umax(top, m);
+                }
+            const float scale = row_power(wave_max_u32(top)), inverse = 1.0f / scale;  // exact
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                const int c = (threadIdx.x + i * 64) * 8;
+                if (c >= a.rank) break;
+                float u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = v[i][j] * inverse;
+                *reinterpret_cast<u32x2*>(row8 + c) = u32x2{pack_fp8x4(u[0], u[1], u[2], u[3]), pack_fp8x4(u[4], u[5], u[6], u[7])};
+            }
+            if (threadIdx.x == 0) a.cache_scale[slot] = scale;
         }
     }
     const int jobs = rope8 * (1 + (a.q ? a.heads : 0));
@@ -225,15 +255,39 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
     for (int k = blockDim.x - 1 - threadIdx.x; k < jobs; k += blockDim.x) {
         const int h = k / rope8 - 1, c = (k % rope8) * 8;
         if (h < 0) {
-            if (!row && !a.rows) continue;
+            if (!row && !row8 && !a.rows) continue;
             const u32x4 o = known ? rotate8(as_global<u32x4>(kv + a.rank)[c / 8], angle, c, a.rope) : nan;
             if (row) *reinterpret_cast<u32x4*>(row + a.rank + c) = o;
+            if (row8) *reinterpret_cast<u32x4*>(row8 + a.rank + c * 2) = o;
             if (a.rows) *reinterpret_cast<u32x4*>(a.rows + t * a.rows_stride + a.rank + c) = o;
         } else {
             const u32x4 u = *as_global<u32x4>(a.q + t * a.q_stride_t + h * a.q_stride_h + c);
             *reinterpret_cast<u32x4*>(a.q_out + t * a.qo_stride_t + h * a.qo_stride_h + c) =
                 known ? rotate8(u, angle, c, a.rope) : nan;
         }
+    }
+}
+
+// Rows of the 8-bit cache as bf16: 16 bytes of a row per lane.
+__global__ void __launch_bounds__(256) latent_read_kernel(ReadArgs a) {
+    const int chunks = (a.rank + 2 * a.rope) / 16;
+    const long job = (long)blockIdx.x * 256 + threadIdx.x, t = job / chunks;
+    const int c = (int)(job - t * chunks) * 16;
+    if (t >= a.T) return;
+    const int64_t slot = a.slots[t];
+    const bool known = slot >= 0 && slot < a.n_slots;
+    u32x4 v = {0, 0, 0, 0};
+    float scale = 1.0f;
+    if (known) {
+        v = *as_global<u32x4>(a.cache + slot * (a.rank + 2 * a.rope) + c);
+        scale = as_global<float>(a.scale)[slot];
+    }
+    uint16_t* out = a.out + t * a.o_stride;
+    if (c < a.rank) {
+        *reinterpret_cast<u32x4*>(out + c) = codes_to_bf16(v[0], v[1], scale);
+        *reinterpret_cast<u32x4*>(out + c + 8) = codes_to_bf16(v[2], v[3], scale);
+    } else {
+        *reinterpret_cast<u32x4*>(out + a.rank + (c - a.rank) / 2) = v;
     }
 }
 
@@ -284,6 +338,12 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s) {
 
 hipError_t launch_latent_append(const AppendArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(latent_append_kernel, dim3(a.T), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_latent_read(const ReadArgs& a, hipStream_t s) {
+    const long jobs = (long)a.T * ((a.rank + 2 * a.rope) / 16);
+    hipLaunchKernelGGL(latent_read_kernel, dim3((unsigned)((jobs + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
