@@ -578,6 +578,38 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
                                   int64_t out_stride_t, int64_t out_stride_h, void* d_ws, size_t ws_bytes,
                                   void* stream);
 
+/* moe_latent_attention_shared: moe_latent_attention over either cache, and for
+ * sequences that share long prefixes, whose rows are then read once for all
+ * tokens on them.
+ * d_cache_scale NULL: d_cache is the bf16 cache.  Else it is the 8-bit one
+ * above, page_stride counts its bytes, and d_cache_scale [n_pages][page_size]
+ * holds the rows' powers of two (contiguous; anything else is read as the power
+ * of two with its exponent).
+ * n_prefixes > 0: prefix i has d_prefix_lens[i] rows on pages d_prefix_pages[i *
+ * prefix_pages_stride + j], j < pages_per_prefix, of the same pool, and belongs
+ * to sequences d_groups[i] .. d_groups[i + 1] (int32 [n_prefixes + 1], not
+ * decreasing; NULL with one prefix: all sequences; a sequence in no group has
+ * none).  Its rows come before the sequence's own: a token sees all of them and
+ * of its own sequence's rows what moe_latent_attention says; d_lens, d_pages,
+ * max_len and trees are of own rows alone, of which there may be none.
+ * max_prefix_len bounds d_prefix_lens (for the launch's size; a longer one is
+ * right all the same).  Prefixes with d_groups that decrease or overlap are
+ * unseen.  Fewer than 2^26 rows (tokens times heads) in all.
+ * moe_latent_attention_shared_workspace: device bytes needed, as above; with
+ * prefixes they hold fp32 sums of all T x heads rows twice. */
+size_t moe_latent_attention_shared_workspace(int B, int T, int max_q, int heads, int rank, int max_len, int n_prefixes,
+                                             int max_prefix_len);
+moe_status_t moe_latent_attention_shared(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, int T, int heads,
+                                         int rank, int rope, const void* d_cache, const float* d_cache_scale,
+                                         int n_pages, int page_size, int64_t page_stride, const int32_t* d_pages,
+                                         int64_t pages_stride, int pages_per_seq, const int32_t* d_lens, int B,
+                                         const int32_t* d_cu_q, int max_q, int max_len, const int64_t* d_tree,
+                                         const int32_t* d_prefix_pages, int64_t prefix_pages_stride,
+                                         int pages_per_prefix, const int32_t* d_prefix_lens, const int32_t* d_groups,
+                                         int n_prefixes, int max_prefix_len, float scale, uint16_t* d_out,
+                                         int64_t out_stride_t, int64_t out_stride_h, void* d_ws, size_t ws_bytes,
+                                         void* stream);
+
 /* moe_prompt_attention: the expanded form, for prompts.  d_q
  * [Tq][heads][nope + rope], d_k [Tk][heads][nope], d_k_rope [Tk][rope] (shared
  * by the heads), d_v [Tk][heads][vdim], out [Tq][heads][vdim]; sequence b has

@@ -43,6 +43,14 @@ class NormOut(NamedTuple):
     scale: torch.Tensor | None  # fp32 [T, ceil(H / 128)]
 
 
+class SharedPrefix(NamedTuple):
+    """Rows that several sequences have before their own, for latent_attention."""
+    pages: torch.Tensor           # int32 [prefixes, pages per prefix], of the sequences' pool
+    lens: torch.Tensor            # int32 [prefixes], their rows
+    max_len: int | None = None    # bounds lens (the pages' reach if None)
+    groups: torch.Tensor | None = None  # int32 [prefixes + 1]: i belongs to sequences groups[i] .. groups[i + 1] (None: one for all)
+
+
 class AppendOut(NamedTuple):
     """Outputs of latent_append; None where not asked for."""
     q_rope: torch.Tensor | None  # rotated position part of the queries
@@ -68,7 +76,7 @@ def _elsewhere(stream, f, *args):
         _need(stream.device == device, f"a stream of {stream.device} and operands on {device}")
         with torch.cuda.stream(stream):
             out = f(*args)
-        for t in args:
+        for t in (u for arg in args for u in (arg if isinstance(arg, tuple) else (arg,))):
             if isinstance(t, torch.Tensor):
                 t.record_stream(stream)
         return out
@@ -383,7 +391,8 @@ def latent_read(cache, cache_scale, slots, rope: int = 64, out=None, stream=None
 
 
 def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = None, cu_q=None,
-                     max_q: int | None = None, tree=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+                     max_q: int | None = None, tree=None, out=None, workspace=None, stream=None, cache_scale=None,
+                     prefix: SharedPrefix | None = None) -> torch.Tensor:
     """Attention over the paged latent cache, heads absorbed into the queries.
 
     q [T, heads, rank + rope] bf16; cache [pages, page_size, rank + rope];
@@ -396,20 +405,33 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     tokens up to itself, or those set in its mask (tree, int64 [T], bit j for
     the sequence's j-th new token, itself included if set).  Returns
     [T, heads, rank] bf16.  workspace: uint8 of
-    moe_latent_attention_workspace() bytes (allocated per call if None)."""
+    moe_latent_attention_workspace() bytes (allocated per call if None).
+
+    cache_scale (fp32 [pages, page_size], contiguous): the cache holds 8 bits,
+    as latent_append leaves it.  prefix: rows that sequences share, seen by
+    their tokens before all of these (pages, lens, max_len and trees are of
+    each sequence's own rows then); they are read once for all tokens on them
+    (workspace: moe_latent_attention_shared_workspace() bytes)."""
     on = q.get_device()
     if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, latent_attention, q, cache, pages, lens, scale, max_len, cu_q, max_q, tree, out,
-                          workspace)
+                          workspace, None, cache_scale, prefix)
     (T, heads, width), qs = _rows(q, "q", 3, _BF16_ONLY, on)
-    (n_pages, page_size, c_width), cs = _rows(cache, "cache", 3, _BF16_ONLY, on)
+    narrow = cache_scale is not None
+    (n_pages, page_size, c_width), cs = _rows(cache, "cache", 3, _U8_ONLY if narrow else _BF16_ONLY, on)
     (nb, per_seq), ps = _rows(pages, "pages", 2, _I32_ONLY, on)
     (n,), _ = _rows(lens, "lens", 1, _I32_ONLY, on)
     rope = 64
     rank = width - rope
-    if c_width != width or (page_size > 1 and cs[1] != width) or n != nb:
-        _need(False, f"cache: rows of {width} one after another in a page are needed, got {tuple(cache.shape)} with strides "
+    row = width + rope if narrow else width
+    if c_width != row or (page_size > 1 and cs[1] != row) or n != nb:
+        _need(False, f"cache: rows of {row} one after another in a page are needed, got {tuple(cache.shape)} with strides "
                      f"{cs}; {n} lengths for {nb} page rows")
+    if narrow:
+        s_shape, _ = _rows(cache_scale, "cache_scale", 2, _F32_ONLY, on)
+        if tuple(s_shape) != (n_pages, page_size) or not cache_scale.is_contiguous():
+            _need(False, f"cache_scale: contiguous {(n_pages, page_size)} is needed, got {tuple(s_shape)} with strides "
+                         f"{cache_scale.stride()}")
     cu_p = tree_p = None
     if cu_q is not None:
         (n,), _ = _rows(cu_q, "cu_q", 1, _I32_ONLY, on)
@@ -428,15 +450,36 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     else:
         o_shape, os = _rows(out, "out", 3, _BF16_ONLY, on)
         _need(tuple(o_shape) == (T, heads, rank), f"out {tuple(o_shape)}, {(T, heads, rank)} is needed")
+    prefixes = most = per_prefix = p_stride = 0
+    p_pages = p_lens = p_groups = None
+    if prefix is not None:
+        (prefixes, per_prefix), pps = _rows(prefix.pages, "prefix.pages", 2, _I32_ONLY, on)
+        (n,), _ = _rows(prefix.lens, "prefix.lens", 1, _I32_ONLY, on)
+        _need(n == prefixes > 0, f"prefix: {n} lengths for {prefixes} page rows")
+        if prefix.groups is not None:
+            (n,), _ = _rows(prefix.groups, "prefix.groups", 1, _I32_ONLY, on)
+            _need(n == prefixes + 1, f"prefix.groups has {n} entries for {prefixes} prefixes")
+            p_groups = prefix.groups.data_ptr()
+        _need(prefixes == 1 or p_groups, f"{prefixes} prefixes need groups")
+        p_stride = pps[0] if prefixes > 1 else per_prefix
+        p_pages, p_lens = prefix.pages.data_ptr(), prefix.lens.data_ptr()
+        most = per_prefix * page_size if prefix.max_len is None else prefix.max_len
     L = B.lib()
     if workspace is None:
-        n = L.moe_latent_attention_workspace(nb, max_q, heads, rank, max_len)
+        n = L.moe_latent_attention_shared_workspace(nb, T, max_q, heads, rank, max_len, prefixes, most)
         workspace = torch.empty(n, dtype=torch.uint8, device=on)
     else:
         if workspace.get_device() != on or not workspace.is_contiguous():
             _need(False, f"workspace: contiguous memory of cuda:{on} is needed, got strides {workspace.stride()} on "
                          f"{workspace.device}")
         n = workspace.numel() * workspace.element_size()
+    if narrow or prefixes:
+        B.check(L.moe_latent_attention_shared(
+            q.data_ptr(), qs[0], qs[1], T, heads, rank, rope, cache.data_ptr(), cache_scale.data_ptr() if narrow else None,
+            n_pages, page_size, cs[0] if n_pages > 1 else page_size * row, pages.data_ptr(), ps[0] if nb > 1 else per_seq,
+            per_seq, lens.data_ptr(), nb, cu_p, max_q, max_len, tree_p, p_pages, p_stride, per_prefix, p_lens, p_groups,
+            prefixes, most, scale, out.data_ptr(), os[0], os[1], workspace.data_ptr(), n, _raw_stream(on)))
+        return out
     B.check(L.moe_latent_attention(
         q.data_ptr(), qs[0], qs[1], T, heads, rank, rope, cache.data_ptr(), n_pages, page_size,
         cs[0] if n_pages > 1 else page_size * width, pages.data_ptr(), ps[0] if nb > 1 else per_seq, per_seq,

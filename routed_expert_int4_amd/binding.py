@@ -109,6 +109,9 @@ _SIGNATURES = {
     "moe_latent_attention_workspace": ([_i] * 5, _sz),
     "moe_latent_attention": ([_vp, _l, _l, _i, _i, _i, _i, _vp, _i, _i, _l, _vp, _l, _i, _vp, _i, _vp, _i, _i, _vp, _f,
                               _vp, _l, _l, _vp, _sz, _vp], _i),
+    "moe_latent_attention_shared_workspace": ([_i] * 8, _sz),
+    "moe_latent_attention_shared": ([_vp, _l, _l, _i, _i, _i, _i, _vp, _vp, _i, _i, _l, _vp, _l, _i, _vp, _i, _vp, _i, _i, _vp,
+                                     _vp, _l, _i, _vp, _vp, _i, _i, _f, _vp, _l, _l, _vp, _sz, _vp], _i),
     "moe_prompt_attention": ([_vp, _l, _l, _vp, _l, _l, _vp, _l, _vp, _l, _l] + [_i] * 6 + [_vp, _vp, _i, _i, _i, _f,
                               _vp, _l, _l, _vp], _i),
 }

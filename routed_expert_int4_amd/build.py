@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libmoe_int4.so")
 SOURCES = ["moe_decode.hip", "moe_batch.hip", "moe_abi.cpp", "moe_cache.cpp", "moe_static.hip", "moe_probe.hip",
-           "moe_norm.hip", "moe_fp8.hip", "moe_heads.hip", "moe_int4.hip", "moe_latent.hip", "moe_prompt.hip", "moe_block_abi.cpp"]
+           "moe_norm.hip", "moe_fp8.hip", "moe_heads.hip", "moe_int4.hip", "moe_latent.hip", "moe_latent_narrow.hip", "moe_latent_shared.hip", "moe_prompt.hip", "moe_block_abi.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

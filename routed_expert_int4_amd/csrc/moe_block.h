@@ -94,7 +94,8 @@ hipError_t launch_int4_linear(const Int4Args& a, hipStream_t s);
 
 struct LatentArgs {
     const uint16_t* q;      // [T][heads][rank + rope]
-    const uint16_t* cache;  // [n_pages][page_size][rank + rope]
+    const uint16_t* cache;  // [n_pages][page_size][rank + rope], or rows of 8 bits (strides count two bytes)
+    const float* cache_scale;  // [n_pages][page_size], of rows of 8 bits
     const int32_t* pages;   // [B][pages_stride]
     const int32_t* lens;    // [B]
     const int32_t* cu_q;    // [B + 1], or nullptr: T / B tokens each
@@ -105,11 +106,30 @@ struct LatentArgs {
     int T, B, heads, rank, rope, n_pages, page_size, pages_per_seq, max_q, max_len;
     int group, runs, per_seq;  // how the call is cut, filled in by the launcher
     float scale;
+    // The sequences of this list are prefixes: b's rows are seen whole by all
+    // tokens of sequences groups[b] .. groups[b + 1] of seqs (nullptr: of all).
+    bool prefixes;
+    const int32_t* groups;
+    int seqs;
+};
+// What is seen before a sequence's own rows: prefixes of groups of sequences.
+struct PrefixArgs {
+    const int32_t* pages;   // [count][pages_stride]
+    const int32_t* lens;    // [count]
+    const int32_t* groups;  // [count + 1], or nullptr: one prefix for all
+    long pages_stride;
+    int pages_per_seq, count, max_len;
+    int group, per_die;     // how the call is cut, filled in by the launcher
 };
 // Device workspace of a call (partial sums of the split sequences).
 size_t latent_workspace(int B, int max_q, int heads, int rank, int max_len);
 bool latent_shape_supported(int rank, int rope);
 hipError_t launch_latent_attention(const LatentArgs& a, hipStream_t s);
+hipError_t launch_latent_narrow(const LatentArgs& a, hipStream_t s);  // its part for rows of 8 bits
+
+// The same with prefixes, which are read once for all tokens of a group.
+size_t latent_shared_workspace(int B, int T, int max_q, int heads, int rank, int max_len, int prefixes, int max_prefix);
+hipError_t launch_latent_shared(const LatentArgs& a, const PrefixArgs& p, hipStream_t s);
 
 struct PromptArgs {
     const uint16_t* q;       // [Tq][heads][nope + rope]

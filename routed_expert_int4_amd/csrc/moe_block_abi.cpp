@@ -62,6 +62,65 @@ moe_status_t append(const char* who, uint8_t* d_cache8, float* d_cache_scale, co
     return launched(launch_latent_append(a, static_cast<hipStream_t>(stream)), who);
 }
 
+// Over rows of either width (8 bits where there are scales; the page stride
+// counts bytes then), with prefixes if there are any.
+moe_status_t attend(const char* who, const float* d_cache_scale, const PrefixArgs& prefix, const uint16_t* d_q,
+                    int64_t q_stride_t, int64_t q_stride_h, int T, int heads, int rank, int rope, const void* d_cache,
+                    int n_pages, int page_size, int64_t page_stride, const int32_t* d_pages, int64_t pages_stride,
+                    int pages_per_seq, const int32_t* d_lens, int B, const int32_t* d_cu_q, int max_q, int max_len,
+                    const int64_t* d_tree, float scale, uint16_t* d_out, int64_t out_stride_t, int64_t out_stride_h,
+                    void* d_ws, size_t ws_bytes, void* stream) {
+    if (T < 0 || B < 0 || heads < 1 || n_pages < 0 || page_size < 1 || pages_per_seq < 0 || max_q < 0 || max_len < 0)
+        return fail(MOE_EINVAL, "%s: a size is negative (or heads or page_size below 1)", who);
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(MOE_EINVAL, "%s: scale must be positive", who);
+    if (!latent_shape_supported(rank, rope))
+        return fail(MOE_EUNSUPPORTED, "%s: no kernel for rank %d and rope %d", who, rank, rope);
+    if (T == 0) return MOE_OK;
+    if (B < 1 || max_q < 1) return fail(MOE_EINVAL, "%s: tokens without a sequence", who);
+    if (!d_q || !d_lens || !d_out || (n_pages > 0 && !d_cache) || (pages_per_seq > 0 && !d_pages))
+        return fail(MOE_EINVAL, "%s: NULL pointer", who);
+    if (!d_cu_q && (T % B || T / B > max_q))
+        return fail(MOE_EINVAL, "%s: T (%d) is not B (%d) times at most max_q (%d) tokens", who, T, B, max_q);
+    const bool narrow = d_cache_scale != nullptr, shared = prefix.count > 0;
+    if (page_stride < (int64_t)page_size * (narrow ? rank + 2 * rope : rank + rope) || pages_stride < pages_per_seq)
+        return fail(MOE_EINVAL, "%s: a stride is below its row", who);
+    if (q_stride_t % 8 || q_stride_h % 8 || page_stride % (narrow ? 16 : 8) || out_stride_t % 4 || out_stride_h % 4 ||
+        !on(d_q, 16) || !on(d_cache, 16) || !on(d_out, 8))
+        return fail(MOE_EUNSUPPORTED, "%s: strides must be multiples of 8 (out: 4; pages of 8 bits: 16), q and cache "
+                    "16-byte aligned, out 8-byte", who);
+    if (!on(d_pages, 4) || !on(d_lens, 4) || !on(d_cu_q, 4) || !on(d_tree, 8) || !on(d_cache_scale, 4) ||
+        !on(prefix.pages, 4) || !on(prefix.lens, 4) || !on(prefix.groups, 4))
+        return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
+    // tile counts are 32-bit: row blocks of all sequences times tiles of the longest
+    const int64_t rows_per_table = (int64_t)pages_per_seq * page_size;
+    if (rows_per_table > ((int64_t)1 << 31) - 128 || B > 65535 || (int64_t)max_q * heads > (int64_t)1 << 30 ||
+        (double)(B + (int64_t)T * heads / 32) * (double)(rows_per_table / 64 + 1) > (double)(1 << 30))
+        return fail(MOE_EUNSUPPORTED, "%s: too many tiles", who);
+    // the second launch has a wave per row of the longest sequence, and 32-bit grids count lanes
+    if ((int64_t)(max_q < T ? max_q : T) * heads >= (int64_t)1 << 26)
+        return fail(MOE_EUNSUPPORTED, "%s: 2^26 or more rows (tokens times heads) in a sequence", who);
+    if (shared) {
+        const int64_t reach = (int64_t)prefix.pages_per_seq * page_size;
+        if (reach > ((int64_t)1 << 31) - 128 || (int64_t)T * heads >= (int64_t)1 << 26 ||
+            (double)(prefix.count + (int64_t)T * heads / 32) * (double)(reach / 64 + 1) > (double)(1 << 30))
+            return fail(MOE_EUNSUPPORTED, "%s: 2^26 or more rows (tokens times heads) or too many tiles of prefixes", who);
+    }
+    const size_t need = shared ? latent_shared_workspace(B, T, max_q, heads, rank, max_len, prefix.count, prefix.max_len)
+                               : latent_workspace(B, max_q, heads, rank, max_len);
+    if (!d_ws || ws_bytes < need || !on(d_ws, 256))
+        return fail(MOE_EINVAL, "%s: workspace of %zu bytes given, %zu needed (256-byte aligned)", who, ws_bytes, need);
+    LatentArgs a{};
+    a.q = d_q, a.cache = static_cast<const uint16_t*>(d_cache), a.cache_scale = d_cache_scale, a.pages = d_pages;
+    a.lens = d_lens, a.cu_q = d_cu_q, a.tree = d_tree, a.out = d_out;
+    a.ws = static_cast<uint8_t*>(d_ws);
+    a.q_stride_t = q_stride_t, a.q_stride_h = q_stride_h, a.o_stride_t = out_stride_t, a.o_stride_h = out_stride_h;
+    a.pages_stride = pages_stride, a.cache_page_stride = narrow ? page_stride / 2 : page_stride;
+    a.T = T, a.B = B, a.heads = heads, a.rank = rank, a.rope = rope, a.n_pages = n_pages, a.page_size = page_size;
+    a.pages_per_seq = pages_per_seq, a.max_q = max_q, a.max_len = max_len, a.scale = scale;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return launched(shared ? launch_latent_shared(a, prefix, s) : launch_latent_attention(a, s), who);
+}
+
 }  // namespace
 
 extern "C" {
@@ -233,45 +292,43 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
                                   int max_len, const int64_t* d_tree, float scale, uint16_t* d_out,
                                   int64_t out_stride_t, int64_t out_stride_h, void* d_ws, size_t ws_bytes,
                                   void* stream) {
-    const char* who = "moe_latent_attention";
-    if (T < 0 || B < 0 || heads < 1 || n_pages < 0 || page_size < 1 || pages_per_seq < 0 || max_q < 0 || max_len < 0)
-        return fail(MOE_EINVAL, "%s: a size is negative (or heads or page_size below 1)", who);
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(MOE_EINVAL, "%s: scale must be positive", who);
-    if (!latent_shape_supported(rank, rope))
-        return fail(MOE_EUNSUPPORTED, "%s: no kernel for rank %d and rope %d", who, rank, rope);
-    if (T == 0) return MOE_OK;
-    if (B < 1 || max_q < 1) return fail(MOE_EINVAL, "%s: tokens without a sequence", who);
-    if (!d_q || !d_lens || !d_out || (n_pages > 0 && !d_cache) || (pages_per_seq > 0 && !d_pages))
-        return fail(MOE_EINVAL, "%s: NULL pointer", who);
-    if (!d_cu_q && (T % B || T / B > max_q))
-        return fail(MOE_EINVAL, "%s: T (%d) is not B (%d) times at most max_q (%d) tokens", who, T, B, max_q);
-    if (page_stride < (int64_t)page_size * (rank + rope) || pages_stride < pages_per_seq)
-        return fail(MOE_EINVAL, "%s: a stride is below its row", who);
-    if (q_stride_t % 8 || q_stride_h % 8 || page_stride % 8 || out_stride_t % 4 || out_stride_h % 4 || !on(d_q, 16) ||
-        !on(d_cache, 16) || !on(d_out, 8))
-        return fail(MOE_EUNSUPPORTED, "%s: strides must be multiples of 8 (out: 4), q and cache 16-byte aligned, out "
-                    "8-byte", who);
-    if (!on(d_pages, 4) || !on(d_lens, 4) || !on(d_cu_q, 4) || !on(d_tree, 8))
-        return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
-    // tile counts are 32-bit: row blocks of all sequences times tiles of the longest
-    const int64_t rows_per_table = (int64_t)pages_per_seq * page_size;
-    if (rows_per_table > ((int64_t)1 << 31) - 128 || B > 65535 || (int64_t)max_q * heads > (int64_t)1 << 30 ||
-        (double)(B + (int64_t)T * heads / 32) * (double)(rows_per_table / 64 + 1) > (double)(1 << 30))
-        return fail(MOE_EUNSUPPORTED, "%s: too many tiles", who);
-    // the second launch has a wave per row of the longest sequence, and 32-bit grids count lanes
-    if ((int64_t)(max_q < T ? max_q : T) * heads >= (int64_t)1 << 26)
-        return fail(MOE_EUNSUPPORTED, "%s: 2^26 or more rows (tokens times heads) in a sequence", who);
-    const size_t need = latent_workspace(B, max_q, heads, rank, max_len);
-    if (!d_ws || ws_bytes < need || !on(d_ws, 256))
-        return fail(MOE_EINVAL, "%s: workspace of %zu bytes given, %zu needed (256-byte aligned)", who, ws_bytes, need);
-    LatentArgs a{};
-    a.q = d_q, a.cache = d_cache, a.pages = d_pages, a.lens = d_lens, a.cu_q = d_cu_q, a.tree = d_tree, a.out = d_out;
-    a.ws = static_cast<uint8_t*>(d_ws);
-    a.q_stride_t = q_stride_t, a.q_stride_h = q_stride_h, a.o_stride_t = out_stride_t, a.o_stride_h = out_stride_h;
-    a.pages_stride = pages_stride, a.cache_page_stride = page_stride;
-    a.T = T, a.B = B, a.heads = heads, a.rank = rank, a.rope = rope, a.n_pages = n_pages, a.page_size = page_size;
-    a.pages_per_seq = pages_per_seq, a.max_q = max_q, a.max_len = max_len, a.scale = scale;
-    return launched(launch_latent_attention(a, static_cast<hipStream_t>(stream)), who);
+    return attend("moe_latent_attention", nullptr, PrefixArgs{}, d_q, q_stride_t, q_stride_h, T, heads, rank, rope, d_cache,
+                  n_pages, page_size, page_stride, d_pages, pages_stride, pages_per_seq, d_lens, B, d_cu_q, max_q, max_len,
+                  d_tree, scale, d_out, out_stride_t, out_stride_h, d_ws, ws_bytes, stream);
+}
+
+size_t moe_latent_attention_shared_workspace(int B, int T, int max_q, int heads, int rank, int max_len, int n_prefixes,
+                                             int max_prefix_len) {
+    if (n_prefixes < 1) return moe_latent_attention_workspace(B, max_q, heads, rank, max_len);
+    if (B < 1 || T < 1 || max_q < 1 || heads < 1 || rank < 1 || max_len < 0 || max_prefix_len < 0) return 0;
+    return latent_shared_workspace(B, T, max_q, heads, rank, max_len, n_prefixes, max_prefix_len);
+}
+
+moe_status_t moe_latent_attention_shared(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, int T, int heads,
+                                         int rank, int rope, const void* d_cache, const float* d_cache_scale,
+                                         int n_pages, int page_size, int64_t page_stride, const int32_t* d_pages,
+                                         int64_t pages_stride, int pages_per_seq, const int32_t* d_lens, int B,
+                                         const int32_t* d_cu_q, int max_q, int max_len, const int64_t* d_tree,
+                                         const int32_t* d_prefix_pages, int64_t prefix_pages_stride,
+                                         int pages_per_prefix, const int32_t* d_prefix_lens, const int32_t* d_groups,
+                                         int n_prefixes, int max_prefix_len, float scale, uint16_t* d_out,
+                                         int64_t out_stride_t, int64_t out_stride_h, void* d_ws, size_t ws_bytes,
+                                         void* stream) {
+    const char* who = "moe_latent_attention_shared";
+    if (n_prefixes < 0 || pages_per_prefix < 0 || max_prefix_len < 0)
+        return fail(MOE_EINVAL, "%s: a size of the prefixes is negative", who);
+    PrefixArgs p{};
+    if (n_prefixes > 0) {
+        if (T > 0 && (!d_prefix_lens || (pages_per_prefix > 0 && !d_prefix_pages) || (n_prefixes > 1 && !d_groups)))
+            return fail(MOE_EINVAL, "%s: NULL pointer for %d prefixes", who, n_prefixes);
+        if (prefix_pages_stride < pages_per_prefix) return fail(MOE_EINVAL, "%s: a stride is below its row", who);
+        if (n_prefixes > 65535) return fail(MOE_EUNSUPPORTED, "%s: over 65535 prefixes", who);
+        p.pages = d_prefix_pages, p.lens = d_prefix_lens, p.groups = d_groups, p.pages_stride = prefix_pages_stride;
+        p.pages_per_seq = pages_per_prefix, p.count = n_prefixes, p.max_len = max_prefix_len;
+    }
+    return attend(who, d_cache_scale, p, d_q, q_stride_t, q_stride_h, T, heads, rank, rope, d_cache, n_pages, page_size,
+                  page_stride, d_pages, pages_stride, pages_per_seq, d_lens, B, d_cu_q, max_q, max_len, d_tree, scale, d_out,
+                  out_stride_t, out_stride_h, d_ws, ws_bytes, stream);
 }
 
 moe_status_t moe_prompt_attention(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* d_k,

@@ -147,6 +147,14 @@ __device__ __forceinline__ bf16x8 values_transposed(unsigned lo, unsigned hi) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
+// The same of 8-bit codes, one read: 16 columns (by lane) by eight keys, whose
+// rows' first or last eight bytes this lane's address names.
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+__device__ __forceinline__ u32x2 codes_transposed(unsigned addr) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)addr));
+}
+
 __device__ __forceinline__ bf16x8 lds_chunk(unsigned addr) {
     return __builtin_bit_cast(bf16x8, *(lds_u32x4*)addr);
 }
