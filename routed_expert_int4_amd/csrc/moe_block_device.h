@@ -98,6 +98,13 @@ __device__ __forceinline__ void load_to_lds16(const void* base, unsigned offset,
                  "s"(__builtin_amdgcn_readfirstlane(dst))
                  : "memory");
 }
+// The same from a base that lane reads have just made: a vector memory
+// instruction may read such a register five wait states later.
+__device__ __forceinline__ void load_to_lds16_lane(unsigned long long base, unsigned offset, unsigned dst) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base),
+                 "s"(__builtin_amdgcn_readfirstlane(dst))
+                 : "memory");
+}
 // Four bytes per lane into LDS: lane l's bytes land at dst + 4 l.
 __device__ __forceinline__ void load_to_lds4(const void* src, unsigned dst) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src),

@@ -51,6 +51,8 @@ constexpr int kTile = 64;          // cache rows per tile
 constexpr int kMaxGroup = 8;       // workgroups of a group
 constexpr int kMaxWorkgroups = 256;  // one per CU
 constexpr int kRopeWidth = 64;
+// What a load of eight rows of 8 bits reads where there is no page.
+__device__ __attribute__((aligned(16))) const uint8_t kNoPage[8 * (512 + 2 * kRopeWidth)] = {};
 
 __device__ __forceinline__ int seq_len(const LatentArgs& a, int b) {
     const int n = a.lens[b];
@@ -237,12 +239,15 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
     constexpr int kLat = RANK / 32, kRope = kRopeWidth / 32, kSteps = kLat + kRope, kOut = RANK / 128;
     constexpr int kLatRow = RANK * kBytes, kLatBytes = kTile * kLatRow, kTileBytes = kLatBytes + kTile * kRopeWidth * 2;
     constexpr int kRowsPerLoad = 1024 / kLatRow;  // cache rows per asynchronous load
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTileBytes];
+    // Tiles are loaded one ahead, those of 8 bits two ahead.
+    constexpr int kBuffers = NARROW ? 3 : 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kBuffers * kTileBytes];
     // Slots by which the four waves of 32 rows hand over partial scores, then
     // exponentials, maxima and flags.  A wave writes its scores to its own
     // slot, reads those of wave ^ 1, and then owns what it has read.
     __shared__ u32x4 slots[kWaves][2][64];
-    __shared__ float powers[2][NARROW ? kTile : 1];  // of the tile's rows
+    __shared__ float powers[kBuffers][NARROW ? kTile : 1];  // of the tiles' rows
+    __shared__ int pages_ahead[2][NARROW ? kTile : 1];       // of the tile after those
     const int lane = threadIdx.x & 63, wave = wave_in_block(), half = lane >> 5, col = lane & 31;
     const int rg = wave >> 2, quarter = wave & 3, side = quarter >> 1, inner = quarter & 1, other = wave ^ 1;
     float* const my_top = reinterpret_cast<float*>(slots[other][1]);  // 32 maxima (at the end: totals)
@@ -263,7 +268,9 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
     // offset reach every chunk from these.
     unsigned key_at, rope_at, value_at;
     {
-        const int r = side * 32 + col;
+        // (a wave takes its keys so that those it keeps are the first 16
+        // instruction rows, and those its neighbour keeps the others)
+        const int r = side * 32 + (col ^ inner * 16);
         if constexpr (NARROW) {
             // keys: 16 codes, two steps of the inner dimension; values: the
             // first byte of eight keys' 16 columns
@@ -315,7 +322,7 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
         }
         // Page and place of cache row t * 64 + lane (-1 past the end).
         const int32_t* my_pages = a.pages + seq * a.pages_stride;
-        auto page_of = [&](int t, int& off) {
+        auto place_of = [&](int t, int& off) {
             const int pos = t * kTile + lane;
             int p = (int)__umulhi((unsigned)pos, page_magic);
             off = pos - p * a.page_size;
@@ -323,38 +330,73 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                 off -= a.page_size;
                 ++p;
             }
-            return pos < len ? as_global<int32_t>(my_pages)[p] : -1;
+            return pos < len ? p : -1;
+        };
+        auto page_of = [&](int t, int& off) {
+            const int p = place_of(t, off);
+            return p >= 0 ? as_global<int32_t>(my_pages)[p] : -1;
         };
         // Its address; a row past the end or on a page that is not in the
         // pool reads as zero and is masked.
         auto address = [&](int page, int off) {
             const uint16_t* p = a.cache + (long)page * a.cache_page_stride + (long)off * kRow;
-            return (unsigned long long)((unsigned)page < (unsigned)a.n_pages ? static_cast<const void*>(p) : kZeros);
+            return (unsigned long long)((unsigned)page < (unsigned)a.n_pages ? static_cast<const void*>(p)
+                                        : NARROW                             ? kNoPage
+                                                                             : kZeros);
         };
         constexpr int kLatLoads = kTile / kRowsPerLoad / kWaves, kLoads = kLatLoads + kTile / 8 / kWaves;
-        // Asynchronous load i of this wave's kLoads of a tile.
-        auto issue = [&](int i, int buf, unsigned long long addr, int chunk) {
+        // Asynchronous load i of this wave's kLoads of a tile: the cache row
+        // of a lane's 16 bytes, and the load from that row's address.
+        auto row_of = [&](int i, int chunk) {
+            return i < kLatLoads ? (i * kWaves + wave) * kRowsPerLoad + chunk / (kLatRow / 16)
+                                 : ((i - kLatLoads) * kWaves + wave) * 8 + (chunk >> 3);
+        };
+        auto issue_from = [&](int i, int buf, unsigned long long p, int chunk) {
             const unsigned dst = lds0 + buf * kTileBytes;
-            if (i < kLatLoads) {
-                const int r0 = (i * kWaves + wave) * kRowsPerLoad;
-                if constexpr (kRowsPerLoad == 1) {
-                    const unsigned lo = __builtin_amdgcn_readlane((unsigned)addr, r0),
-                                   hi = __builtin_amdgcn_readlane((unsigned)(addr >> 32), r0);
-                    load_to_lds16((const void*)((unsigned long long)hi << 32 | lo),
-                                  (unsigned)(chunk ^ place_mix(r0)) * 16, dst + r0 * kLatRow);
-                } else {
-                    const int r = r0 + chunk / (kLatRow / 16);
-                    const unsigned long long p = __shfl(addr, r);
-                    load_to_lds16((const uint8_t*)p + ((chunk % (kLatRow / 16)) ^ place_mix(r)) * 16, dst + r0 * kLatRow);
-                }
-            } else {
-                const int r0 = ((i - kLatLoads) * kWaves + wave) * 8, r = r0 + (chunk >> 3);
-                const unsigned long long p = __shfl(addr, r);
+            const int r = row_of(i, chunk);
+            if (i < kLatLoads)
+                load_to_lds16((const uint8_t*)p + ((chunk % (kLatRow / 16)) ^ place_mix(r)) * 16,
+                              dst + (i * kWaves + wave) * kRowsPerLoad * kLatRow);
+            else
                 load_to_lds16((const uint8_t*)p + kLatRow + (((chunk & 7) ^ (r >> 1)) & 7) * 16,
-                              dst + kLatBytes + r0 * kRopeWidth * 2);
+                              dst + kLatBytes + ((i - kLatLoads) * kWaves + wave) * 8 * kRopeWidth * 2);
+        };
+        // Rows of 8 bits in pages of a multiple of 8 rows: all of a load's rows
+        // follow its first one's address, rows past the sequence's end and all,
+        // and the lanes' offsets are the same for every tile.
+        const bool in_page = NARROW && a.page_size % 8 == 0;
+        unsigned lat_offset = 0, rope_offset = 0;
+        if constexpr (NARROW) {
+            const int r = row_of(0, lane), u = row_of(kLatLoads, lane);
+            lat_offset = lane / (kLatRow / 16) * (kRow * 2) + ((lane % (kLatRow / 16)) ^ place_mix(r)) * 16;
+            rope_offset = (lane >> 3) * (kRow * 2) + kLatRow + (((lane & 7) ^ (u >> 1)) & 7) * 16;
+        }
+        auto issue_rows = [&](int i, int buf, unsigned long long addr) {
+            const int r0 = i < kLatLoads ? (i * kWaves + wave) * kRowsPerLoad : ((i - kLatLoads) * kWaves + wave) * 8;
+            const unsigned lo = __builtin_amdgcn_readlane((unsigned)addr, r0),
+                           hi = __builtin_amdgcn_readlane((unsigned)(addr >> 32), r0);
+            const unsigned long long base = (unsigned long long)hi << 32 | lo;
+            // (the mixed place goes by the row's low four bits)
+            constexpr int kStep = kWaves * kRowsPerLoad;
+            const int mixed = place_mix(wave * kRowsPerLoad + i * kStep) ^ place_mix(wave * kRowsPerLoad);
+            if (i < kLatLoads)
+                load_to_lds16_lane(base, lat_offset ^ mixed * 16, lds0 + buf * kTileBytes + r0 * kLatRow);
+            else
+                load_to_lds16_lane(base, rope_offset, lds0 + buf * kTileBytes + kLatBytes + r0 * kRopeWidth * 2);
+        };
+        auto issue = [&](int i, int buf, unsigned long long addr, int chunk) {
+            if (in_page) {
+                issue_rows(i, buf, addr);
+            } else if (kRowsPerLoad == 1 && i < kLatLoads) {
+                const int r0 = i * kWaves + wave;
+                const unsigned lo = __builtin_amdgcn_readlane((unsigned)addr, r0),
+                               hi = __builtin_amdgcn_readlane((unsigned)(addr >> 32), r0);
+                load_to_lds16((const void*)((unsigned long long)hi << 32 | lo), (unsigned)(chunk ^ place_mix(r0)) * 16,
+                              lds0 + buf * kTileBytes + r0 * kLatRow);
+            } else {
+                issue_from(i, buf, __shfl(addr, row_of(i, chunk)), chunk);
             }
         };
-
         // A tile's powers of two, by one of the waves.
         auto issue_powers = [&](int buf, int page, int off) {
             if constexpr (NARROW) {
@@ -367,7 +409,8 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
         float m = kNoMax, l = 0.0f;
         f32x16 o[kOut] = {};
         int off, page = page_of(t_first, off);
-        unsigned long long valid = __ballot((unsigned)page < (unsigned)a.n_pages);
+        unsigned long long valid = __ballot((unsigned)page < (unsigned)a.n_pages), valid_next = 0;
+        int place_next = -1;  // of this lane's row of the tile after the next
         // the queries have landed: the compiler must not wait for them inside
         // the loop, where other loads are on their way
 #pragma unroll
@@ -379,21 +422,68 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
             issue_powers(0, page, off);
         }
         page = page_of(t_first + 1, off);
+        // The tile after the next has its page numbers brought to LDS by one
+        // wave: a load into a register would be waited for with all others.
+        auto issue_pages = [&](int t, int slot) {
+            place_next = place_of(t, off);
+            if (wave == 0)
+                load_to_lds4(place_next >= 0 ? static_cast<const void*>(my_pages + place_next) : kZeros, lds_address(pages_ahead[slot]));
+        };
+        int buf = 0;
+        if constexpr (NARROW) {
+            asm volatile("" : "+v"(page));
+            valid_next = __ballot((unsigned)page < (unsigned)a.n_pages);
+            const unsigned long long addr = address(page, off);
+            if (t_first + 1 < t_last) issue_powers(1, page, off);
+            if (t_first + 2 < t_last) issue_pages(t_first + 2, 0);
+            if (t_first + 1 < t_last) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) issue(i, 1, addr, lane);
+            }
+        }
         for (int t = t_first; t < t_last; ++t) {
-            const int buf = (t - t_first) & 1;
-            wait_vmem<0>();
-            asm volatile("" : "+v"(page));  // the next tile's pages have landed: no later wait covers its loads
-            lds_barrier();                  // tile t is in LDS, and every wave is done with the other buffer
-            const unsigned long long now = valid;
-            valid = __ballot((unsigned)page < (unsigned)a.n_pages);
-            const unsigned long long next = address(page, off);
-            const bool more = t + 1 < t_last;
-            if (NARROW && more) issue_powers(buf ^ 1, page, off);
-            page = page_of(t + 2, off);
+            unsigned long long now = valid, next;
+            bool more;
+            int into;  // the buffer that the loads of this turn go to
+            if constexpr (NARROW) {
+                // tile t and the page numbers for t + 2 are in LDS; the loads
+                // of tile t + 1 may be on their way
+                if (t + 1 < t_last)
+                    wait_vmem<kLoads>();
+                else
+                    wait_vmem<0>();
+                lds_barrier();  // every wave is done with the third buffer
+                if (t > t_first) buf = buf == 2 ? 0 : buf + 1;
+                buf = __builtin_amdgcn_readfirstlane(buf);
+                into = buf == 0 ? 2 : buf - 1;
+                more = t + 2 < t_last;
+                valid = valid_next;
+                next = 0;
+            } else {
+                buf = (t - t_first) & 1;
+                into = buf ^ 1;
+                wait_vmem<0>();
+                asm volatile("" : "+v"(page));  // the next tile's pages have landed: no later wait covers its loads
+                lds_barrier();                  // tile t is in LDS, and every wave is done with the other buffer
+                valid = __ballot((unsigned)page < (unsigned)a.n_pages);
+                next = address(page, off);
+                more = t + 1 < t_last;
+                page = page_of(t + 2, off);
+            }
+            // (8 bits) what the loads of tile t + 2 go by, once the first matrix
+            // instructions are on their way
+            auto look_ahead = [&]() {
+                const int got = pages_ahead[(t - t_first) & 1][lane];
+                page = more && place_next >= 0 ? got : -1;
+                valid_next = __ballot((unsigned)page < (unsigned)a.n_pages);
+                next = address(page, off);
+                if (more) issue_powers(into, page, off);
+                if (t + 3 < t_last) issue_pages(t + 3, (t + 1 - t_first) & 1);
+            };
             int chunk = lane;
             asm volatile("" : "+v"(chunk));  // the mixed places are not worth a register each across the loop
             const unsigned tile = buf * kTileBytes;
-            float s[8];  // of the wave's 32 keys, registers inner * 8 on
+            float s[8];  // of the wave's keys, a quarter of the tile's
             {
                 f32x16 sum = {};  // over the wave's half of the inner dimension
                 // operands are read kAhead instructions before their use; the
@@ -403,11 +493,11 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
 #pragma unroll
                 for (int k = 0; k < kRope; ++k) rope_base[k] = (rope_at + tile) ^ k * 32;
                 if constexpr (NARROW) {
-                    // an item is 16 codes, widened for two instructions, or a
+                    // An item is 16 codes, widened for two instructions, or a
                     // chunk of the position part
-                    constexpr int kPairs = kLat / 2, kItems = kPairs + kRope, kAhead = 4;
+                    constexpr int kPairs = kLat / 2, kItems = kPairs + kRope, kAhead = 4, kFirst = 1;
                     u32x4 x[kAhead];
-                    const float power = powers[buf][side * 32 + col];
+                    const float power = powers[buf][side * 32 + (col ^ inner * 16)];
                     auto item = [&](int k) {
                         return __builtin_bit_cast(u32x4, lds_chunk(k < kPairs ? (key_at + tile) ^ k * 32 : rope_base[k - kPairs]));
                     };
@@ -423,9 +513,14 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                             mfma(sum, __builtin_bit_cast(bf16x8, u), qf[kLat + k - kPairs]);
                         }
                         if (k + kAhead < kItems) x[k % kAhead] = item(k + kAhead);
+                        if (k == kFirst) look_ahead();
+                        if (k > kFirst) {
+                            constexpr int kFor = kItems - 1 - kFirst;
+                            const int j = k - 1 - kFirst;
 #pragma unroll
-                        for (int i = k * kLoads / kItems; i < (k + 1) * kLoads / kItems; ++i)
-                            if (more) issue(i, buf ^ 1, next, chunk);
+                            for (int i = j * kLoads / kFor; i < (j + 1) * kLoads / kFor; ++i)
+                                if (more) issue(i, into, next, chunk);
+                        }
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 } else {
@@ -447,15 +542,15 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                         // wave that issues them in one go stalls in the queue)
 #pragma unroll
                         for (int i = k * kLoads / kSteps; i < (k + 1) * kLoads / kSteps; ++i)
-                            if (more) issue(i, buf ^ 1, next, chunk);
+                            if (more) issue(i, into, next, chunk);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
                 f32x4 give[2];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    s[i] = inner ? sum[8 + i] : sum[i];
-                    give[i / 4][i % 4] = inner ? sum[i] : sum[8 + i];
+                    s[i] = sum[i];
+                    give[i / 4][i % 4] = sum[8 + i];
                 }
                 slots[wave][0][lane] = __builtin_bit_cast(u32x4, give[0]);
                 slots[wave][1][lane] = __builtin_bit_cast(u32x4, give[1]);
@@ -488,7 +583,8 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     s[i] = word >> (8 * (i / 4) + i % 4) & 1 ? s[i] : -__builtin_inff();
-                if (before < kTile && (a.tree || count > 1)) {
+                // (rows past the end that a load of whole groups brought count too)
+                if ((NARROW && now != ~0ull) || (before < kTile && (a.tree || count > 1))) {
                     // new tokens that some of them do not see: this wave looks
                     // over its share of the rows
                     unsigned p = lds0 + tile + wave * (kLatBytes / kWaves) + lane * 16;
@@ -514,15 +610,17 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                 else
                     return values_transposed(lo[k] + at_key, hi[k] + at_key);
             };
-            // the wave's keys' exponents, in the order of its scores: what a
-            // code stands for enters through the weights
-            int power_of[NARROW ? 8 : 1];
+            // The powers of two of the wave's keys, in the order of its
+            // scores: what a code stands for enters through the weights.  One
+            // that is not finite counts as another here, for keys whose weight
+            // is zero; a row that sees such a key has it in its score.
+            float power_of[NARROW ? 8 : 1];
             if constexpr (NARROW) {
 #pragma unroll
                 for (int i = 0; i < 8; i += 4) {
-                    const u32x4 u = __builtin_bit_cast(u32x4, *reinterpret_cast<const f32x4*>(&powers[buf][quarter * 16 + half * 4 + i * 2]));
+                    const f32x4 u = *reinterpret_cast<const f32x4*>(&powers[buf][quarter * 16 + half * 4 + i * 2]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) power_of[i + j] = (int)(u[j] >> 23) - 127;
+                    for (int j = 0; j < 4; ++j) power_of[i + j] = __builtin_amdgcn_fmed3f(u[j], 0.0f, 0x1p127f);
                 }
             }
 #pragma unroll
@@ -543,7 +641,7 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                     const float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
                     sum += e;
                     if constexpr (NARROW)
-                        p[i] = (__bf16)__builtin_amdgcn_ldexpf(e, power_of[i]);
+                        p[i] = (__bf16)(e * power_of[i]);
                     else
                         p[i] = (__bf16)e;
                 }
@@ -766,7 +864,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
 struct LatentCut {
     int rows, group, runs;
 };
-[[maybe_unused]] LatentCut latent_cut(int B, int max_q, int heads, int max_len) {
+[[maybe_unused]] LatentCut latent_cut(int B, int max_q, int heads, int max_len, bool narrow) {
     LatentCut c;
     const long rows = (long)max_q * heads;
     c.rows = rows > 32 ? 64 : 32;
@@ -774,7 +872,8 @@ struct LatentCut {
     c.group = (int)(blocks < kMaxGroup ? blocks : kMaxGroup);
     const long passes = (blocks + c.group - 1) / c.group;
     const long tiles = max_len > kTile ? (max_len + kTile - 1) / kTile : 1;
-    const long most = kMaxWorkgroups / c.group, all = B * passes * tiles;
+    // (a group's workgroups lie on one die, which holds 32 at once)
+    const long most = narrow ? kMaxWorkgroups / 8 / c.group * 8 : kMaxWorkgroups / c.group, all = B * passes * tiles;
     c.runs = (int)(all < most ? all : most);
     return c;
 }
@@ -802,7 +901,7 @@ void launch_rows(LatentArgs a, const LatentCut& cut, hipStream_t s) {
 }
 template <int RANK, bool NARROW>
 void launch_rank(const LatentArgs& a, hipStream_t s) {
-    const LatentCut cut = latent_cut(a.B, a.max_q, a.heads, a.max_len);
+    const LatentCut cut = latent_cut(a.B, a.max_q, a.heads, a.max_len, NARROW);
     if (cut.rows == 64)
         launch_rows<RANK, 2, NARROW>(a, cut, s);
     else
