@@ -135,6 +135,16 @@ __device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int la
     return total;
 }
 
+// Pieces of the list: a pass over a sequence's tiles each.  (Bounds that name
+// more than T tokens can make this any number.)
+template <int ROWS>
+__device__ __forceinline__ int count_units(const LatentArgs& a, int lane) {
+    int total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64)
+        total += __builtin_amdgcn_readlane(wave_scan_int(b0 + lane < a.B ? seq_shape<ROWS>(a, b0 + lane).passes : 0), 63);
+    return total;
+}
+
 // The sequence that holds tile `at` of the list (at < its length), and the
 // tile its part starts with.
 template <int ROWS>

@@ -28,29 +28,21 @@ __device__ __forceinline__ void as_prefixes(LatentArgs& a, const PrefixArgs& p) 
 }
 
 // How the workgroups of eight dies, per_die on each, serve lists of total_own
-// and total_prefix tiles: the prefixes' runs are dealt to the dies in turn,
-// p.group workgroups each, and own runs take what is left on each die.  Whole
-// numbers only: both launches have to come to the same.
+// and total_prefix tiles in own_units and prefix_units pieces: the prefixes'
+// runs are dealt to the dies in turn, p.group workgroups each, and own runs
+// take what is left on each die.  Whole numbers only: both launches have to
+// come to the same.
 struct Split {
     int own, prefix;       // runs
     int base, extra;       // prefix runs on each die, and dies that have one more
     int low, high;         // own runs on those dies, and on the others
 };
-__device__ __forceinline__ Split split_runs(int total_own, int total_prefix, int own_group, int prefix_group, int per_die) {
+struct Lists {
+    int own, own_units, prefix, prefix_units;
+};
+__device__ __forceinline__ Split split_at(int prefix, int total_own, int own_group, int prefix_group, int per_die) {
     Split s;
-    s.prefix = 0;
-    if (total_prefix > 0) {
-        unsigned long long p = (unsigned long long)total_prefix * prefix_group, o = (unsigned long long)total_own * own_group;
-        const int bits = 64 - __builtin_clzll(p + o);
-        const int shift = bits > 20 ? bits - 20 : 0;
-        const unsigned part = (unsigned)(p >> shift), whole = (unsigned)((p + o) >> shift) * (unsigned)prefix_group;
-        s.prefix = (int)((per_die * 8 * part + whole / 2) / whole);
-        // at least one die keeps room for an own run
-        const int most = 8 * ((per_die - own_group) / prefix_group) + 7, all = 8 * (per_die / prefix_group);
-        s.prefix = s.prefix > most ? most : s.prefix;
-        s.prefix = s.prefix > all ? all : s.prefix;
-        s.prefix = s.prefix > total_prefix ? total_prefix : s.prefix < 1 ? 1 : s.prefix;
-    }
+    s.prefix = prefix;
     s.base = s.prefix >> 3;
     s.extra = s.prefix & 7;
     s.high = (per_die - s.base * prefix_group) / own_group;
@@ -58,6 +50,48 @@ __device__ __forceinline__ Split split_runs(int total_own, int total_prefix, int
     const int room = s.low * 8 + (s.high - s.low) * (8 - s.extra);
     s.own = total_own < room ? total_own : room;
     return s;
+}
+// What starting and ending a unit costs a run, in tiles (measured: 8 sequences
+// of 5 tiles took a run as long as 60 tiles of one).
+constexpr unsigned kUnitTiles = 2;
+__device__ __forceinline__ Split split_runs(const Lists& n, int own_group, int prefix_group, int per_die) {
+    if (n.prefix == 0) return split_at(0, n.own, own_group, prefix_group, per_die);
+    const unsigned long long p = (unsigned long long)(n.prefix + kUnitTiles * n.prefix_units) * prefix_group,
+                             o = (unsigned long long)(n.own + kUnitTiles * n.own_units) * own_group;
+    const int bits = 64 - __builtin_clzll(p + o), shift = bits > 20 ? bits - 20 : 0;
+    const unsigned part = (unsigned)(p >> shift), whole = (unsigned)((p + o) >> shift) * (unsigned)prefix_group;
+    const int near = (int)(per_die * 8 * part / whole);
+    // at least one die keeps room for an own run
+    const int most = 8 * ((per_die - own_group) / prefix_group) + 7, all = 8 * (per_die / prefix_group);
+    int limit = most < all ? most : all;
+    limit = limit < n.prefix ? limit : n.prefix;
+    // of the numbers next to the even share, the one whose longer list is shortest
+    Split best{};
+    unsigned least = ~0u;
+    for (int i = -1; i <= 1; ++i) {
+        int at = near + i;
+        at = at > limit ? limit : at;
+        at = at < 1 ? 1 : at;
+        const Split s = split_at(at, n.own, own_group, prefix_group, per_die);
+        const unsigned a = (n.prefix + kUnitTiles * n.prefix_units + s.prefix - 1) / s.prefix,
+                       b = (n.own + kUnitTiles * n.own_units + s.own - 1) / s.own, time = a > b ? a : b;
+        if (time < least) {
+            least = time;
+            best = s;
+        }
+    }
+    return best;
+}
+// The lists of both kinds: their tiles and units, and the tiles before
+// sequence `seq` and prefix `g`.
+__device__ __forceinline__ Lists count_lists(const LatentArgs& a, const LatentArgs& q, int seq, int g, int lane, int& before,
+                                             int& before_prefix) {
+    Lists n;
+    n.own = count_tiles<kRows>(a, seq, lane, before);
+    n.prefix = count_tiles<kRows>(q, g, lane, before_prefix);
+    n.own_units = count_units<kRows>(a, lane);
+    n.prefix_units = count_units<kRows>(q, lane);
+    return n;
 }
 
 // Sums of units that one run held whole, by row, after the partial ones.
@@ -72,11 +106,10 @@ __global__ void __launch_bounds__(512, 1) latent_shared_kernel(LatentArgs a, Pre
     const int lane = threadIdx.x & 63, die = blockIdx.x & 7, turn = blockIdx.x >> 3;
     LatentArgs q = a;
     as_prefixes(q, p);
-    int before;
-    const int total_own = count_tiles<kRows>(a, 0, lane, before);
-    if (total_own == 0) return;
-    const int total_prefix = count_tiles<kRows>(q, 0, lane, before);
-    const Split s = split_runs(total_own, total_prefix, a.group, p.group, p.per_die);
+    int before, before_prefix;
+    const Lists n = count_lists(a, q, 0, 0, lane, before, before_prefix);
+    if (n.own == 0) return;
+    const Split s = split_runs(n, a.group, p.group, p.per_die);
     const int prefix_turns = (s.base + (die < s.extra)) * p.group;
     const bool prefix = turn < prefix_turns;
     int run, member;
@@ -93,7 +126,7 @@ __global__ void __launch_bounds__(512, 1) latent_shared_kernel(LatentArgs a, Pre
     const int runs = prefix ? s.prefix : s.own;
     if (run >= runs) return;
     const int slot = run * a.group + member + (prefix ? 0 : s.prefix * p.group);
-    attend<RANK, 2, NARROW, true>(a, prefix ? total_prefix : total_own, runs, run, member, slot, whole_sums<RANK>(a, p, prefix));
+    attend<RANK, 2, NARROW, true>(a, prefix ? n.prefix : n.own, runs, run, member, slot, whole_sums<RANK>(a, p, prefix));
 }
 
 // The runs that hold a unit's sums for one row.
@@ -131,9 +164,6 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(LatentArgs a, P
     if (row >= shape.count * a.heads) return;
     LatentArgs q = a;
     as_prefixes(q, p);
-    int before, before_prefix = 0;
-    const int total_own = count_tiles<kRows>(a, seq, lane, before);
-    if (total_own == 0) return;  // nor has the first launch done anything
     // the sequence's prefix
     int g = p.groups ? -1 : 0;
     if (p.groups)
@@ -145,16 +175,18 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(LatentArgs a, P
                 break;
             }
         }
-    const int total_prefix = count_tiles<kRows>(q, g < 0 ? 0 : g, lane, before_prefix);
-    const Split s = split_runs(total_own, total_prefix, a.group, p.group, p.per_die);
-    const Sources own = sources_of(total_own, s.own, before, shape.tiles, a.group, row, s.prefix * p.group);
+    int before, before_prefix;
+    const Lists n = count_lists(a, q, seq, g < 0 ? 0 : g, lane, before, before_prefix);
+    if (n.own == 0) return;  // nor has the first launch done anything
+    const Split s = split_runs(n, a.group, p.group, p.per_die);
+    const Sources own = sources_of(n.own, s.own, before, shape.tiles, a.group, row, s.prefix * p.group);
     Sources pre{};
-    if (g >= 0 && total_prefix > 0) {
+    if (g >= 0 && n.prefix > 0) {
         const SeqShape of = seq_shape<kRows>(q, g);
         const int r = (shape.first - of.first) * a.heads + row;
         // (bounds in device memory that decrease can put a row outside its group)
         if (r >= 0 && r < of.count * a.heads)
-            pre = sources_of(total_prefix, s.prefix, before_prefix, of.tiles, p.group, r, 0);
+            pre = sources_of(n.prefix, s.prefix, before_prefix, of.tiles, p.group, r, 0);
     }
     const int sources = own.count + pre.count;
     const long rows = (long)a.T * a.heads, at = (long)shape.first * a.heads + row;
