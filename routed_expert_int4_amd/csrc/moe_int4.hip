@@ -46,6 +46,7 @@ __device__ __forceinline__ void swap32(unsigned& a, unsigned& b) {
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
     a = r[0], b = r[1];
 }
+
 __device__ __forceinline__ void swap16(unsigned& a, unsigned& b) {
     const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
     a = r[0], b = r[1];
@@ -59,12 +60,119 @@ __device__ __forceinline__ void store_out(const Int4Args& a, int t, int n, float
         static_cast<uint16_t*>(a.out)[at] = round_bf16(v);
 }
 
-// Few tokens: the weights stream from memory once, straight into operand
-// order.  A workgroup has NT x 16 weight rows and TT x 16 tokens; its waves
+// One or two tokens: a lane takes the 16 bytes, 32 columns, of a weight row
+// that share a scale and multiplies them with two-element dot products: fewer
+// instructions than operands of the matrix cores take for so few rows.  Eight
+// lanes read 128 neighbouring bytes of a row.  The eight waves of a workgroup
+// share the inner columns of 16 weight rows, 256 at a time in turn; all loads
+// of a turn of 8192 columns are on their way before the activations, put in the
+// weights' order, have come to LDS.
+constexpr int kTurnSegs = 4, kFewWaves = 8, kSeg = 256, kTurn = kTurnSegs * kFewWaves * kSeg;
+template <int GROUP, int TOKENS>
+__global__ void __launch_bounds__(kFewWaves * 64) int4_few_kernel(Int4Args a) {
+    // (the 64 bytes that go with a lane's weights: their four chunks are turned
+    // by the upper bit of the lane's place, so that eight lanes cover all banks)
+    __shared__ __attribute__((aligned(16))) u32x4 xs[TOKENS][kTurn / 8];
+    __shared__ float minus[TOKENS][kTurn / 32];  // -1.5 times the sum of 32 activations
+    __shared__ float sums[kFewWaves][TOKENS][16];
+    const int lane = threadIdx.x & 63, place = lane & 7, wave = wave_in_block(), n0 = blockIdx.x * 16;
+    const uint8_t* w_row[2];
+    const uint16_t* s_row[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = n0 + h * 8 + (lane >> 3);
+        w_row[h] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
+        s_row[h] = a.scale + (long)(n < a.N ? n : a.N - 1) * a.lds;
+    }
+    float acc[2][TOKENS] = {};
+    for (int k_turn = 0; k_turn < a.K; k_turn += kTurn) {
+        u32x4 w[kTurnSegs][2];
+        uint16_t s[kTurnSegs][2];
+#pragma unroll
+        for (int i = 0; i < kTurnSegs; ++i) {
+            const int k_seg = k_turn + (i * kFewWaves + wave) * kSeg, k = k_seg + place * 32;
+            if (k_seg >= a.K) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[i][h] = load_stream16(w_row[h] + (k < a.K ? k / 2 : 0));
+                s[i][h] = *as_global<uint16_t>(s_row[h] + (k < a.K ? k / GROUP : 0));
+            }
+        }
+        if (k_turn > 0) __syncthreads();
+        // (zero past the last column, which leaves any weight without effect)
+        for (int i = threadIdx.x; i < TOKENS * (kTurn / 8); i += kFewWaves * 64) {
+            const int t = i / (kTurn / 8), c = i % (kTurn / 8), k = k_turn + c * 8;
+            if (k_turn + c / (kSeg / 8) * kSeg >= a.K) continue;  // (whole segments only)
+            u32x4 x = {0, 0, 0, 0};
+            if (k < a.K && t < a.M) x = *as_global<u32x4>(a.x + (long)t * a.ldx + k);
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += bf16_lo(x[j]) + bf16_hi(x[j]);
+            sum += dpp_f<kDppXor1>(sum);
+            sum += dpp_f<kDppXor2>(sum);
+            xs[t][c ^ ((c >> 4) & 1)] = __builtin_bit_cast(u32x4, in_order(x));
+            if ((c & 3) == 0) minus[t][c / 4] = -1.5f * sum;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTurnSegs; ++i) {
+            const int seg = i * kFewWaves + wave;
+            if (k_turn + seg * kSeg >= a.K) break;
+            float d[2][TOKENS];
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) d[0][t] = d[1][t] = minus[t][seg * 8 + place];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                u32x4 q[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) q[h] = __builtin_bit_cast(u32x4, widen(w[i][h][c]));
+#pragma unroll
+                for (int t = 0; t < TOKENS; ++t) {
+                    const u32x4 x = xs[t][(seg * 32 + place * 4 + c) ^ (place >> 2)];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const unsigned xj = x[j];  // (a bit cast of an element would take the first one's bits)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const unsigned qj = q[h][j];
+                            d[h][t] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(i16x2, qj), __builtin_bit_cast(i16x2, xj), d[h][t], false);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < TOKENS; ++t) acc[h][t] = fmaf(d[h][t], half_bits_to_float(s[i][h]), acc[h][t]);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t) {
+            float sum = acc[h][t];
+            sum += dpp_f<kDppXor1>(sum);
+            sum += dpp_f<kDppXor2>(sum);
+            sum += dpp_f<kDppHalfMirror>(sum);
+            if (place == 0) sums[wave][t][h * 8 + (lane >> 3)] = sum;
+        }
+    __syncthreads();
+    if (threadIdx.x < TOKENS * 16) {
+        const int t = threadIdx.x / 16, n = n0 + (threadIdx.x & 15);
+        if (n >= a.N || t >= a.M) return;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) sum += sums[w][t][threadIdx.x & 15];
+        store_out(a, t, n, sum * kCodeUnit);
+    }
+}
+
+// Up to sixteen tokens: one matrix tile of them and the weights streamed from memory
+// once, straight into operand order.  A workgroup has NT x 16 weight rows and TT x 16 tokens; its waves
 // share the inner columns, 128 (a segment) at a time in turn, U segments
 // loaded one batch ahead, and join their sums through LDS in wave order.
-template <int GROUP, int NT, int TT, int WAVES, int U>
-__global__ void __launch_bounds__(WAVES * 64) int4_rows_kernel(Int4Args a) {
+template <int GROUP, int NT, int TT, int WAVES, int U, int PER_SIMD>
+__global__ void __launch_bounds__(WAVES * 64, PER_SIMD) int4_rows_kernel(Int4Args a) {
     constexpr int kPer = GROUP > 32 ? GROUP / 32 : 1, kGroups = 4 / kPer;  // blocks of 32 per group, groups per segment
     __shared__ float sums[WAVES][NT * TT * 4][64];
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = wave_in_block();
@@ -191,16 +299,18 @@ __global__ void __launch_bounds__(WAVES * 64) int4_rows_kernel(Int4Args a) {
     }
 }
 
-// Many tokens: the activations of a tile pass through LDS, 64 WK inner
-// columns (a stage) loaded asynchronously one stage ahead; weights go from
-// memory into the registers of the waves that own their rows, one stage ahead
-// too.  WT x WN waves lie along tokens and weight rows, TT x NT matrix tiles of
-// 32 x 32 each; WK waves share the inner columns of a stage and join their
-// sums at the end.
+// More tokens: tiles on the matrix cores.  A stage is 64 WK inner columns; the
+// loads of AHEAD stages are on their way into registers, activations going on
+// to one of two LDS buffers (in the weights' order), weights staying with the
+// waves that own their rows.  WT x WN waves lie along tokens and weight rows,
+// TT x NT matrix tiles of 32 x 32 each; WK waves share the inner columns of a
+// stage and join their sums at the end.
+// A weight row's 16 bytes of a lane half hold four dwords of 8 columns; swapped
+// with the other half's they are the four steps of 16, in dwords 0 2 1 3.
 __device__ __forceinline__ constexpr int at_step(int e) { return e == 1 ? 2 : e == 2 ? 1 : e; }
 
-template <int GROUP, int TT, int NT, int WT, int WN, int WK>
-__global__ void __launch_bounds__(WT * WN * WK * 64, 1) int4_tile_kernel(Int4Args a) {
+template <int GROUP, int TT, int NT, int WT, int WN, int WK, int AHEAD, int PER_SIMD>
+__global__ void __launch_bounds__(WT * WN * WK * 64, PER_SIMD) int4_tile_kernel(Int4Args a) {
     constexpr int kWaves = WT * WN * WK, kTokens = WT * TT * 32, kChunks = 8 * WK;  // 16-byte chunks of a row of a stage
     constexpr int kStageBytes = kTokens * kChunks * 16, kLoads = kStageBytes / 1024 / kWaves;
     constexpr int kScales = GROUP == 32 ? 2 : 1, kSteps = 4 / kScales;  // scales of a wave's 64 columns, steps of 16 for each
@@ -218,17 +328,17 @@ __global__ void __launch_bounds__(WT * WN * WK * 64, 1) int4_tile_kernel(Int4Arg
     const int t0 = tile % t_tiles * kTokens, n0 = (tile / t_tiles * WN + wn) * NT * 32;
     const int stages = (a.K + 64 * WK - 1) / (64 * WK);
     const unsigned lds0 = lds_address(lds);
-    // chunk c of row r lies at place c ^ (r & 7): the rows of an operand read cover all banks
-    auto issue = [&](int stage, int buf) {
+    const uint16_t* x_row[kLoads];
+    unsigned x_at[kLoads];
+    int x_k[kLoads];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = (i * kWaves + wave) * 64 + lane, r = at / kChunks, c = (at % kChunks) ^ (r & 7);
-            const int t = t0 + r, k = (stage * kChunks + c) * 8;
-            const uint16_t* p = a.x + (long)t * a.ldx + k;
-            load_to_lds16(t < a.M && k < a.K ? static_cast<const void*>(p) : kZeros,
-                          lds0 + buf * kStageBytes + (i * kWaves + wave) * 1024);
-        }
-    };
+    for (int i = 0; i < kLoads; ++i) {
+        // chunk c of row r lies at place c ^ (r & 7): the rows of an operand read cover all banks
+        const int at = (i * kWaves + wave) * 64 + lane, r = at / kChunks, c = at % kChunks, t = t0 + r;
+        x_row[i] = a.x + (long)(t < a.M ? t : a.M - 1) * a.ldx;
+        x_k[i] = c * 8;
+        x_at[i] = lds0 + (r * kChunks + (c ^ (r & 7))) * 16;
+    }
     const uint8_t* w_row[NT];
     const uint16_t* s_row[NT];
 #pragma unroll
@@ -237,73 +347,90 @@ __global__ void __launch_bounds__(WT * WN * WK * 64, 1) int4_tile_kernel(Int4Arg
         w_row[i] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
         s_row[i] = a.scale + (long)(n < a.N ? n : a.N - 1) * a.lds;
     }
-    u32x4 w_next[NT];
-    uint16_t s_next[NT][kScales];
-    auto load_weights = [&](int stage) {
+    struct Stage {
+        u32x4 x[kLoads], w[NT];
+        uint16_t s[NT][kScales];
+    } ring[AHEAD];
+    // (columns past the last one read the row's first and count as zero)
+    auto load = [&](Stage& v, int stage) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int k = stage * 64 * WK + x_k[i];
+            v.x[i] = *as_global<u32x4>(x_row[i] + (k < a.K ? k : 0));
+        }
         const int k0 = (stage * WK + wk) * 64, k = k0 + half * 32;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            w_next[i] = *as_global<u32x4>(w_row[i] + (k < a.K ? k / 2 : 0));
+            v.w[i] = *as_global<u32x4>(w_row[i] + (k < a.K ? k / 2 : 0));
 #pragma unroll
             for (int g = 0; g < kScales; ++g) {
                 const int kg = k0 + g * 32;
-                s_next[i][g] = *as_global<uint16_t>(s_row[i] + (kg < a.K ? kg / GROUP : 0));
+                v.s[i][g] = *as_global<uint16_t>(s_row[i] + (kg < a.K ? kg / GROUP : 0));
             }
         }
     };
+    auto put = [&](const Stage& v, int stage) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            u32x4 x = v.x[i];
+            if (stage * 64 * WK + x_k[i] >= a.K) x = u32x4{0, 0, 0, 0};
+            lds_store(x_at[i] + (stage & 1) * kStageBytes, __builtin_bit_cast(u32x4, in_order(x)));
+        }
+    };
     f32x16 acc[NT][TT] = {};
-    issue(0, 0);
-    load_weights(0);
-    for (int stage = 0; stage < stages; ++stage) {
-        const int buf = stage & 1;
-        wait_vmem<0>();
-        unsigned w[NT][4];
-        float s[NT][kScales];
+    // Nothing in the loop hangs on the stage (one past the last loads anything
+    // and counts as zero): where loads may or may not have been issued, the
+    // compiler waits for more than it has to.
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            asm volatile("" : "+v"(w_next[i]));
+    for (int d = 0; d < AHEAD; ++d) load(ring[d], d);
+    put(ring[0], 0);
+    for (int stage0 = 0; stage0 < stages; stage0 += AHEAD) {
 #pragma unroll
-            for (int d = 0; d < 4; ++d) w[i][d] = w_next[i][d];
-            // lane halves hold 32 columns each: to halves of 8 columns of the
-            // same 16, which leaves the four steps in dwords 0 2 1 3
-            swap32(w[i][0], w[i][1]);
-            swap32(w[i][2], w[i][3]);
-#pragma unroll
-            for (int g = 0; g < kScales; ++g) s[i][g] = half_bits_to_float(s_next[i][g]);
-        }
-        lds_barrier();  // the stage is in LDS, and every wave is done with the other buffer
-        if (stage + 1 < stages) {
-            issue(stage + 1, buf ^ 1);
-            load_weights(stage + 1);
-        }
-#pragma unroll
-        for (int g = 0; g < kScales; ++g) {
-            f32x16 start[TT];
-            bf16x8 x[TT][kSteps];
-#pragma unroll
-            for (int j = 0; j < TT; ++j)
-#pragma unroll
-                for (int e = 0; e < kSteps; ++e) {
-                    const int r = (wt * TT + j) * 32 + col, c = wk * 8 + (g * kSteps + e) * 2 + half;
-                    x[j][e] = in_order(__builtin_bit_cast(
-                        u32x4, lds_chunk(lds0 + buf * kStageBytes + (r * kChunks + (c ^ (r & 7))) * 16)));
-                    const f32x16 zero = {};
-                    start[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][e], minus_one_and_half(), e ? start[j] : zero, 0, 0, 0);
-                }
+        for (int r = 0; r < AHEAD; ++r) {
+            const int stage = stage0 + r;
+            lds_barrier();  // the stage is in LDS, and every wave is done with the other buffer
+            unsigned w[NT][4];
+            float s[NT][kScales];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                bf16x8 q[kSteps];
 #pragma unroll
-                for (int e = 0; e < kSteps; ++e) q[e] = widen(w[i][at_step(g * kSteps + e)]);
+                for (int d = 0; d < 4; ++d) w[i][d] = ring[r].w[i][d];
+                swap32(w[i][0], w[i][1]);
+                swap32(w[i][2], w[i][3]);
 #pragma unroll
-                for (int j = 0; j < TT; ++j) {
-                    f32x16 d = start[j];
+                for (int g = 0; g < kScales; ++g) s[i][g] = half_bits_to_float(ring[r].s[i][g]);
+            }
+            load(ring[r], stage + AHEAD);
+            const unsigned from = lds0 + (stage & 1) * kStageBytes;
 #pragma unroll
-                    for (int e = 0; e < kSteps; ++e) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][e], q[e], d, 0, 0, 0);
+            for (int g = 0; g < kScales; ++g) {
+                f32x16 start[TT];
+                bf16x8 x[TT][kSteps];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(d[e], s[i][g], acc[i][j][e]);
+                for (int j = 0; j < TT; ++j)
+#pragma unroll
+                    for (int e = 0; e < kSteps; ++e) {
+                        const int row = (wt * TT + j) * 32 + col, c = wk * 8 + (g * kSteps + e) * 2 + half;
+                        x[j][e] = lds_chunk(from + (row * kChunks + (c ^ (row & 7))) * 16);
+                        const f32x16 zero = {};
+                        start[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][e], minus_one_and_half(), e ? start[j] : zero, 0, 0, 0);
+                    }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    bf16x8 q[kSteps];
+#pragma unroll
+                    for (int e = 0; e < kSteps; ++e) q[e] = widen(w[i][at_step(g * kSteps + e)]);
+#pragma unroll
+                    for (int j = 0; j < TT; ++j) {
+                        f32x16 d = start[j];
+#pragma unroll
+                        for (int e = 0; e < kSteps; ++e) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][e], q[e], d, 0, 0, 0);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(d[e], s[i][g], acc[i][j][e]);
+                    }
                 }
             }
+            put(ring[(r + 1) % AHEAD], stage + 1);
         }
     }
     if constexpr (WK > 1) {
@@ -344,28 +471,216 @@ __global__ void __launch_bounds__(WT * WN * WK * 64, 1) int4_tile_kernel(Int4Arg
     }
 }
 
-template <int GROUP, int NT, int TT, int WAVES, int U>
-void launch_few(const Int4Args& a, hipStream_t s) {
-    const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.M + 16 * TT - 1) / (16 * TT));
-    hipLaunchKernelGGL((int4_rows_kernel<GROUP, NT, TT, WAVES, U>), grid, dim3(WAVES * 64), 0, s, a);
+// Many tokens: one wave to the whole inner dimension of its TT x NT matrix
+// tiles, WT x WN waves along tokens and weight rows.  Of a stage of 64 columns
+// the activations come to LDS asynchronously, a stage ahead, and are put in
+// order as they are read: two waves fit a SIMD, and what counts is
+// what instructions cost.
+template <int GROUP, int TT, int NT, int WT, int WN, int PER_SIMD>
+__global__ void __launch_bounds__(WT * WN * 64, PER_SIMD) int4_many_kernel(Int4Args a) {
+    constexpr int kWaves = WT * WN, kTokens = WT * TT * 32, kChunks = 8;  // 16-byte chunks of a row of a stage
+    constexpr int kStageBytes = kTokens * kChunks * 16, kLoads = kStageBytes / 1024 / kWaves;
+    constexpr int kScales = GROUP == 32 ? 2 : 1, kSteps = 4 / kScales;  // scales of a wave's 64 columns, steps of 16 for each
+    static_assert(kLoads * kWaves * 1024 == kStageBytes, "stage");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
+    const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31, wave = wave_in_block();
+    const int wn = wave % WN, wt = wave / WN;
+    // workgroups of one die (they are dealt in turn) take neighbouring tiles
+    // of the same weight rows
+    const int n_tiles = (a.N + WN * NT * 32 - 1) / (WN * NT * 32), t_tiles = (a.M + kTokens - 1) / kTokens;
+    const int per_die = (n_tiles * t_tiles + 7) / 8, tile = (blockIdx.x & 7) * per_die + (blockIdx.x >> 3);
+    if (tile >= n_tiles * t_tiles) return;
+    const int t0 = tile % t_tiles * kTokens, n_tile = tile / t_tiles * WN * NT * 32, n0 = n_tile + wn * NT * 32;
+    const int stages = (a.K + 63) / 64;
+    const unsigned lds0 = lds_address(lds);
+    // Addresses are a base for the tile and the stage and an offset that a lane
+    // keeps; rows past the last one repeat it.  Chunk c of row r lies at place
+    // c ^ (r & 7): the rows of an operand read cover all banks.
+    unsigned x_off[kLoads], w_off[NT], s_off[NT];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int at = (i * kWaves + wave) * 64 + lane, r = at / kChunks, c = (at % kChunks) ^ (r & 7);
+        const int last = a.M - 1 - t0;
+        x_off[i] = (unsigned)(r < last ? r : last) * (unsigned)(a.ldx * 2) + c * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int r = n0 - n_tile + i * 32 + col, last = a.N - 1 - n_tile, row = r < last ? r : last;
+        w_off[i] = (unsigned)row * (unsigned)a.ldw + half * 16;
+        s_off[i] = (unsigned)row * (unsigned)(a.lds * 2);
+    }
+    const uint8_t* const x_base = reinterpret_cast<const uint8_t*>(a.x + (long)t0 * a.ldx);
+    const uint8_t* const w_base = a.w + (long)n_tile * a.ldw;
+    const uint8_t* const s_base = reinterpret_cast<const uint8_t*>(a.scale + (long)n_tile * a.lds);
+    u32x4 w_next[NT];
+    typedef uint16_t scales_t __attribute__((ext_vector_type(kScales), aligned(2)));  // (a row of scales starts on two bytes)
+    scales_t s_next[NT];
+    auto issue = [&](int stage, int buf) {
+        const bool whole = stage * 64 + 64 <= a.K;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const unsigned dst = lds0 + buf * kStageBytes + (i * kWaves + wave) * 1024;
+            if (whole) {
+                load_to_lds16(x_base + (long)stage * 128, x_off[i], dst);
+            } else {  // columns past the last one count as zero
+                const int at = (i * kWaves + wave) * 64 + lane, c = (at % kChunks) ^ ((at / kChunks) & 7);
+                const uint8_t* p = x_base + (long)stage * 128 + x_off[i];
+                load_to_lds16(stage * 64 + c * 8 < a.K ? p : kZeros, dst);
+            }
+        }
+        const uint8_t *w = w_base + (long)stage * 32, *s = s_base + (long)(stage * 64 / GROUP) * 2;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                w_next[i] = *as_global<u32x4>(w + w_off[i]);
+                s_next[i] = *as_global<scales_t>(s + s_off[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                w_next[i] = *as_global<u32x4>(w + w_off[i] - half * 16);
+                s_next[i] = scales_t(*as_global<uint16_t>(s + s_off[i]));
+            }
+        }
+    };
+    f32x16 acc[NT][TT] = {};
+    issue(0, 0);
+    for (int stage = 0; stage < stages; ++stage) {
+        const int buf = stage & 1;
+        wait_vmem<0>();
+        unsigned w[NT][4];
+        float s[NT][kScales];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            asm volatile("" : "+v"(w_next[i]));
+#pragma unroll
+            for (int d = 0; d < 4; ++d) w[i][d] = w_next[i][d];
+            // lane halves hold 32 columns each: to halves of 8 columns of the
+            // same 16, which leaves the four steps in dwords 0 2 1 3
+            swap32(w[i][0], w[i][1]);
+            swap32(w[i][2], w[i][3]);
+#pragma unroll
+            for (int g = 0; g < kScales; ++g) {
+                const uint16_t bits = s_next[i][g];
+                s[i][g] = half_bits_to_float(bits);
+                asm("" : "+v"(s[i][g]));  // (or every product would convert it again)
+            }
+        }
+        lds_barrier();  // the stage is in LDS, and every wave is done with the other buffer
+        if (stage + 1 < stages) issue(stage + 1, buf ^ 1);
+#pragma unroll
+        for (int g = 0; g < kScales; ++g) {
+            f32x16 start[TT];
+            bf16x8 x[TT][kSteps];
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e) {
+                    const int r = (wt * TT + j) * 32 + col, c = (g * kSteps + e) * 2 + half;
+                    x[j][e] = in_order(__builtin_bit_cast(
+                        u32x4, lds_chunk(lds0 + buf * kStageBytes + (r * kChunks + (c ^ (r & 7))) * 16)));
+                    const f32x16 zero = {};
+                    start[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][e], minus_one_and_half(), e ? start[j] : zero, 0, 0, 0);
+                }
+            // a tile's sums are scaled while the next one's are computed: the
+            // barriers keep the compiler from waiting for each in turn
+            f32x16 d[2];
+            auto scale = [&](int p) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[p / TT][p % TT][e] = fmaf(d[p & 1][e], s[p / TT][g], acc[p / TT][p % TT][e]);
+            };
+            bf16x8 q[kSteps];
+#pragma unroll
+            for (int p = 0; p < NT * TT; ++p) {
+                if (p % TT == 0) {
+#pragma unroll
+                    for (int e = 0; e < kSteps; ++e) q[e] = widen(w[p / TT][at_step(g * kSteps + e)]);
+                }
+                d[p & 1] = start[p % TT];
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e)
+                    d[p & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[p % TT][e], q[e], d[p & 1], 0, 0, 0);
+                if (p > 0) scale(p - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            scale(NT * TT - 1);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int n = n0 + i * 32 + col;
+        if (n >= a.N) continue;
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int t = t0 + (wt * TT + j) * 32 + 8 * (e / 4) + 4 * half + e % 4;
+                if (t < a.M) store_out(a, t, n, acc[i][j][e] * kCodeUnit);
+            }
+    }
 }
-template <int GROUP, int TT, int NT, int WT, int WN, int WK>
+
+template <int GROUP, int TOKENS>
+void launch_few(const Int4Args& a, hipStream_t s) {
+    hipLaunchKernelGGL((int4_few_kernel<GROUP, TOKENS>), dim3((a.N + 15) / 16), dim3(kFewWaves * 64), 0, s, a);
+}
+template <int GROUP, int NT, int TT, int WAVES, int U, int PER_SIMD>
+void launch_rows(const Int4Args& a, hipStream_t s) {
+    const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.M + 16 * TT - 1) / (16 * TT));
+    hipLaunchKernelGGL((int4_rows_kernel<GROUP, NT, TT, WAVES, U, PER_SIMD>), grid, dim3(WAVES * 64), 0, s, a);
+}
+template <int GROUP, int TT, int NT, int WT, int WN, int WK, int AHEAD, int PER_SIMD>
 void launch_tiles(const Int4Args& a, hipStream_t s) {
     const long tiles = (long)((a.N + WN * NT * 32 - 1) / (WN * NT * 32)) * ((a.M + WT * TT * 32 - 1) / (WT * TT * 32));
-    hipLaunchKernelGGL((int4_tile_kernel<GROUP, TT, NT, WT, WN, WK>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+    hipLaunchKernelGGL((int4_tile_kernel<GROUP, TT, NT, WT, WN, WK, AHEAD, PER_SIMD>), dim3((unsigned)((tiles + 7) / 8 * 8)),
                        dim3(WT * WN * WK * 64), 0, s, a);
+}
+template <int GROUP, int TT, int NT, int WT, int WN, int PER_SIMD>
+void launch_many(const Int4Args& a, hipStream_t s) {
+    const long tiles = (long)((a.N + WN * NT * 32 - 1) / (WN * NT * 32)) * ((a.M + WT * TT * 32 - 1) / (WT * TT * 32));
+    hipLaunchKernelGGL((int4_many_kernel<GROUP, TT, NT, WT, WN, PER_SIMD>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                       dim3(WT * WN * 64), 0, s, a);
+}
+
+// Shapes of tiles and what a stage of inner columns takes them, in
+// nanoseconds: alone on a compute unit, and with as many as fit (measured; a
+// stage is a chain of latencies for the small ones, instructions for the large).
+struct Shape {
+    int tokens, rows, columns, alone, together, fit;
+};
+constexpr Shape kShapes[] = {{32, 32, 512, 1000, 1000, 1}, {32, 64, 256, 800, 800, 1},   {64, 64, 256, 1230, 1230, 1},
+                             {64, 128, 128, 1050, 1050, 1}, {128, 128, 64, 1150, 1650, 2}, {128, 192, 64, 1500, 2550, 2}};
+// The shape that takes least time over the rounds it needs on the chip.
+int best_shape(const Int4Args& a, int count) {
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < count; ++i) {
+        const Shape& s = kShapes[i];
+        auto up = [](long n, long d) { return (n + d - 1) / d; };
+        const long per_cu = up(up(a.M, s.tokens) * up(a.N, s.rows), 256), full = per_cu / s.fit, rest = per_cu % s.fit;
+        const double time = (double)up(a.K, s.columns) * (double)(full * s.together + rest * s.alone);
+        if (i == 0 || time < least) least = time, best = i;
+    }
+    return best;
 }
 
 template <int GROUP>
 void launch_group(const Int4Args& a, hipStream_t s) {
-    if (a.M <= 16)
-        launch_few<GROUP, 1, 1, 8, 2>(a, s);
-    else if (a.M <= 32)
-        launch_few<GROUP, 1, 2, 8, 1>(a, s);
-    else if ((long)a.M * a.N < 128l * 256 * 128)
-        launch_tiles<GROUP, 2, 2, 1, 1, 4>(a, s);
-    else
-        launch_tiles<GROUP, 2, 4, 2, 2, 1>(a, s);
+    if (a.M == 1) return launch_few<GROUP, 1>(a, s);
+    if (a.M == 2) return launch_few<GROUP, 2>(a, s);
+    // two tiles of weight rows share a wave's activations where there are rows
+    // enough (16 x 6144 x 8192: 21 us, 25 with one; 16 x 2048 x 6144: 15 and 11)
+    if (a.M <= 16) return a.N < 4096 ? launch_rows<GROUP, 1, 1, 8, 1, 4>(a, s) : launch_rows<GROUP, 2, 1, 8, 1, 3>(a, s);
+    // (with larger groups the last shape needs more registers than there are)
+    switch (best_shape(a, GROUP == 32 ? 6 : 5)) {
+        case 0: return launch_tiles<GROUP, 1, 1, 1, 1, 8, 3, 2>(a, s);
+        case 1: return launch_tiles<GROUP, 1, 1, 1, 2, 4, 3, 2>(a, s);
+        case 2: return launch_tiles<GROUP, 2, 1, 1, 2, 4, 4, 2>(a, s);
+        case 3: return launch_tiles<GROUP, 2, 1, 1, 4, 2, 4, 2>(a, s);
+        case 4: return launch_many<GROUP, 2, 2, 2, 2, 2>(a, s);
+        default:
+            if constexpr (GROUP == 32) launch_many<GROUP, 2, 3, 2, 2, 2>(a, s);
+    }
 }
 
 }  // namespace
