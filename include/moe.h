@@ -482,7 +482,8 @@ moe_status_t moe_fp8_linear(const uint8_t* d_a, int64_t a_stride, const float* d
  * fp32 (out_type).  Weights are used as they are (a code and its scale enter
  * separately), sums are fp32.  K a multiple of the group; x 16-byte aligned,
  * its stride a multiple of 8; w 16-byte aligned, its stride (bytes) a multiple
- * of 16 (else MOE_EUNSUPPORTED); M x N at most 2^38.  Sums hold 1.5 + q / 16
+ * of 16, rows under 8 MiB apart (else MOE_EUNSUPPORTED); M and N at
+ * most 2^26 and M x N 2^36.  Sums hold 1.5 + q / 16
  * and take the 1.5 away again, so activations above 2^120 may overflow, and a
  * token with an infinity gives NaN or an infinity. */
 moe_status_t moe_int4_linear(const uint16_t* d_x, int64_t x_stride, const uint8_t* d_w, int64_t w_stride,

@@ -202,8 +202,11 @@ moe_status_t moe_int4_linear(const uint16_t* d_x, int64_t x_stride, const uint8_
         return fail(MOE_EUNSUPPORTED, "%s: the strides of x and w must be multiples of 16 bytes, both 16-byte aligned", who);
     if (!on(d_scale, 2) || !on(d_out, out_type == MOE_F32 ? 4 : 2))
         return fail(MOE_EINVAL, "%s: a pointer is not aligned to its type", who);
-    // grids count lanes in 32 bits, and the largest tile is 128 x 256
-    if ((int64_t)M * N > (int64_t)1 << 38) return fail(MOE_EUNSUPPORTED, "%s: M x N (%d x %d) is over 2^38", who, M, N);
+    if (!stride_fits(x_stride * 2) || !stride_fits(w_stride) || !stride_fits(scale_stride * 2))
+        return fail(MOE_EUNSUPPORTED, "%s: rows over 8 MiB apart", who);
+    // grids count lanes in 32 bits
+    if (M > 1 << 26 || N > 1 << 26 || (int64_t)M * N > (int64_t)1 << 36)
+        return fail(MOE_EUNSUPPORTED, "%s: M (%d) or N (%d) over 2^26, or M x N over 2^36", who, M, N);
     Int4Args a{};
     a.x = d_x, a.w = d_w, a.scale = d_scale, a.out = d_out;
     a.ldx = x_stride, a.ldw = w_stride, a.lds = scale_stride, a.ldo = out_stride;
