@@ -7,6 +7,19 @@
 namespace moe {
 namespace {
 
+// One load from every 64 bytes of a kernel's arguments, so that those that are
+// first used late are in the scalar cache by then (each line is a trip to
+// memory, one after the other where they are used).
+template <int BYTES>
+__device__ __forceinline__ void touch_arguments() {
+    const auto* p = (const __attribute__((address_space(4))) int*)__builtin_amdgcn_kernarg_segment_ptr();
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < BYTES; i += 64) all ^= p[i / 4];
+    asm volatile("" ::"s"(all));
+}
+
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

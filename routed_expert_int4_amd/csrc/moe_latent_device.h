@@ -110,12 +110,14 @@ __device__ __forceinline__ int wave_scan_int(int v) {
     return scan_step<0x143, 0xC>(v);  // lane 31 into the upper half
 }
 
-// The whole list: its length, and the tiles before sequence `upto`.  The host
+// The whole list: its length, the tiles before sequence `upto`, and its
+// pieces, a pass over a sequence's tiles each.  The host
 // has seen to it that the tiles of T tokens fit 32 bits, so bounds in device
 // memory that name more than T (some of them twice) leave the list empty.
 template <int ROWS>
-__device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int lane, int& before) {
+__device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int lane, int& before, int* units = nullptr) {
     int total = 0, tokens = 0;  // this lane's sequences', T + 1 for any number above T
+    int passes = 0;
     before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
         const int b = b0 + lane;
@@ -123,6 +125,7 @@ __device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int la
         if (b < a.B) {
             const SeqShape s = seq_shape<ROWS>(a, b);
             mine = s.tiles * s.passes;
+            passes += s.passes;
             tokens = tokens + s.count > a.T ? a.T + 1 : tokens + s.count;
         }
         const int scan = wave_scan_int(mine);
@@ -132,29 +135,21 @@ __device__ __forceinline__ int count_tiles(const LatentArgs& a, int upto, int la
     // (64 lanes of up to T, below 2^26, are below 2^32)
     if ((a.cu_q || a.prefixes) && (__any(tokens > a.T) || (unsigned)__builtin_amdgcn_readlane(wave_scan_int(tokens), 63) > (unsigned)a.T))
         return 0;
+    if (units) *units = __builtin_amdgcn_readlane(wave_scan_int(passes), 63);
     return total;
 }
 
-// Pieces of the list: a pass over a sequence's tiles each.  (Bounds that name
-// more than T tokens can make this any number.)
+// The sequence that holds tile `at` of the list (at < its length), its part,
+// and the tile that starts with.
 template <int ROWS>
-__device__ __forceinline__ int count_units(const LatentArgs& a, int lane) {
-    int total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64)
-        total += __builtin_amdgcn_readlane(wave_scan_int(b0 + lane < a.B ? seq_shape<ROWS>(a, b0 + lane).passes : 0), 63);
-    return total;
-}
-
-// The sequence that holds tile `at` of the list (at < its length), and the
-// tile its part starts with.
-template <int ROWS>
-__device__ __forceinline__ void find_tile(const LatentArgs& a, int at, int lane, int& seq, int& start) {
+__device__ __forceinline__ SeqShape find_tile(const LatentArgs& a, int at, int lane, int& seq, int& start) {
     int before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
         const int b = b0 + lane;
         int mine = 0;
+        SeqShape s{};
         if (b < a.B) {
-            const SeqShape s = seq_shape<ROWS>(a, b);
+            s = seq_shape<ROWS>(a, b);
             mine = s.tiles * s.passes;
         }
         const int upto = wave_scan_int(mine) + before;
@@ -163,12 +158,14 @@ __device__ __forceinline__ void find_tile(const LatentArgs& a, int at, int lane,
             const int w = __builtin_ctzll(hit);
             seq = b0 + w;
             start = __builtin_amdgcn_readlane(upto - mine, w);
-            return;
+            auto of = [&](int v) { return __builtin_amdgcn_readlane(v, w); };
+            return {of(s.len), of(s.first), of(s.count), of(s.tiles), of(s.blocks), of(s.passes)};
         }
         before = __builtin_amdgcn_readlane(upto, 63);
     }
     seq = a.B - 1;
     start = at;
+    return seq_shape<ROWS>(a, seq);
 }
 
 // Runs the list is cut into, and where run g starts.
@@ -265,7 +262,7 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
     const int run_end = run_start(total, runs, run + 1);
     int at = run_start(total, runs, run);
     int seq, seq_at;
-    find_tile<ROWS>(a, at, lane, seq, seq_at);
+    SeqShape shape = find_tile<ROWS>(a, at, lane, seq, seq_at);
 
     const unsigned lds0 = lds_address(lds);
     const float c = a.scale * 1.44269504088896340736f;
@@ -300,11 +297,10 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
     }
 
     while (at < run_end) {
-        const SeqShape shape = seq_shape<ROWS>(a, seq);
         const int len = shape.len, first = shape.first, count = shape.count, tiles = shape.tiles;
         if (at >= seq_at + tiles * shape.passes) {
             seq_at += tiles * shape.passes;
-            ++seq;
+            shape = seq_shape<ROWS>(a, ++seq);
             continue;
         }
         const int pass = (at - seq_at) / tiles, t_first = (at - seq_at) % tiles;
@@ -763,12 +759,13 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
             }
         }
         at += t_last - t_first;
-        __syncthreads();  // the buffers are free for the next part's first tile
+        lds_barrier();  // the buffers are free for the next part's first tile
     }
 }
 
 template <int RANK, int RG, bool NARROW>
 __global__ void __launch_bounds__(RG * 256, 1) latent_attention_kernel(LatentArgs a) {
+    touch_arguments<sizeof(a)>();
     // workgroups are dealt to the eight dies in turn: group g lies on die g % 8
     const int turn = blockIdx.x >> 3, run = (blockIdx.x & 7) + 8 * (turn / a.group), member = turn % a.group;
     int before;
@@ -782,6 +779,7 @@ __global__ void __launch_bounds__(RG * 256, 1) latent_attention_kernel(LatentArg
 // runs each in turn, and are joined in wave order.
 template <int RANK, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(256) latent_join_kernel(LatentArgs a) {
+    touch_arguments<sizeof(a)>();
     constexpr int V = RANK / 64, kAtOnce = SPLIT > 1 ? 16 : 64;
     __shared__ float shared_o[SPLIT > 1 ? 4 : 1][V][64];
     __shared__ float shared_ml[4][2];

@@ -87,10 +87,9 @@ __device__ __forceinline__ Split split_runs(const Lists& n, int own_group, int p
 __device__ __forceinline__ Lists count_lists(const LatentArgs& a, const LatentArgs& q, int seq, int g, int lane, int& before,
                                              int& before_prefix) {
     Lists n;
-    n.own = count_tiles<kRows>(a, seq, lane, before);
-    n.prefix = count_tiles<kRows>(q, g, lane, before_prefix);
-    n.own_units = count_units<kRows>(a, lane);
-    n.prefix_units = count_units<kRows>(q, lane);
+    n.own_units = n.prefix_units = 0;
+    n.own = count_tiles<kRows>(a, seq, lane, before, &n.own_units);
+    n.prefix = count_tiles<kRows>(q, g, lane, before_prefix, &n.prefix_units);
     return n;
 }
 
@@ -103,6 +102,7 @@ __device__ __forceinline__ float* whole_sums(const LatentArgs& a, const PrefixAr
 
 template <int RANK, bool NARROW>
 __global__ void __launch_bounds__(512, 1) latent_shared_kernel(LatentArgs a, PrefixArgs p) {
+    touch_arguments<sizeof(a) + sizeof(p)>();
     const int lane = threadIdx.x & 63, die = blockIdx.x & 7, turn = blockIdx.x >> 3;
     LatentArgs q = a;
     as_prefixes(q, p);
@@ -154,6 +154,7 @@ __device__ __forceinline__ Sources sources_of(int total, int runs, int before, i
 // wave takes 64 at once; RANK / 64 columns per lane.
 template <int RANK, int SPLIT>
 __global__ void __launch_bounds__(256) latent_shared_join_kernel(LatentArgs a, PrefixArgs p) {
+    touch_arguments<sizeof(a) + sizeof(p)>();
     constexpr int V = RANK / 64, kAtOnce = SPLIT > 1 ? 16 : 64;
     __shared__ float shared_o[SPLIT > 1 ? 4 : 1][V][64];
     __shared__ float shared_ml[4][2];
