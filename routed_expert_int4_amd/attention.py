@@ -245,11 +245,13 @@ def int4_linear(x, codes, scale, out_dtype=_BF16, out=None, stream=None) -> torc
         _need(False, f"x {(M, K)} needs codes (N, {K // 2}) and scales (N, {K} / 32, 64 or 128), got {(N, half)} and "
                      f"{(rows, groups)}")
     if out is None:
-        _need(out_dtype in _TYPES, f"out_dtype {out_dtype}: bf16 or fp32")
-        out, o_stride = torch.empty((M, N), dtype=out_dtype, device=on), N
+        if out_dtype not in _TYPES:
+            _need(False, f"out_dtype {out_dtype}: bf16 or fp32")
+        out, o_stride = torch.empty_strided((M, N), (N, 1), dtype=out_dtype, device=on), N  # (0.4 us quicker than empty)
     else:
         o_shape, o_strides = _rows(out, "out", 2, _WIDE, on)
-        _need(tuple(o_shape) == (M, N), f"out {tuple(o_shape)}, {(M, N)} is needed")
+        if tuple(o_shape) != (M, N):
+            _need(False, f"out {tuple(o_shape)}, {(M, N)} is needed")
         out_dtype, o_stride = out.dtype, o_strides[0] if M > 1 else N
     # the stride of a single row says nothing
     B.check(B.lib().moe_int4_linear(x.data_ptr(), x_strides[0] if M > 1 else K, codes.data_ptr(),
@@ -323,7 +325,8 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
         n_slots = cache.numel() // width
     if cache is not None:
         (n,), _ = _rows(slots, "slots", 1, _I64_ONLY, on)
-        _need(n == T, f"{n} slots for {T} tokens")
+        if n != T:
+            _need(False, f"{n} slots for {T} tokens")
         cache_p, slots_p = cache.data_ptr(), slots.data_ptr()
     heads, qs, qo, qp, qop = 0, (0, 0), (0, 0), None, None
     if q_rope is not None:
@@ -332,7 +335,8 @@ def latent_append(kv, weight, eps, table, positions, slots=None, cache=None, q_r
             _need(False, f"q_rope {tuple(q_shape)}, {(T, 'heads', rope)} is needed")
         heads = q_shape[1]
         if q_out is None:
-            q_out, qo = torch.empty(q_shape, dtype=_BF16, device=on), (heads * rope, rope)
+            qo = (heads * rope, rope)
+            q_out = torch.empty_strided(q_shape, (*qo, 1), dtype=_BF16, device=on)
         else:
             qo_shape, qo = _rows(q_out, "q_out", 3, _BF16_ONLY, on)
             _need(qo_shape == q_shape, f"q_out {tuple(qo_shape)}, q_rope {tuple(q_shape)}")
@@ -378,12 +382,14 @@ def latent_read(cache, cache_scale, slots, rope: int = 64, out=None, stream=None
     n_slots = _narrow_rows(cache, cache_scale, cache.shape[-1], on)
     (T,), _ = _rows(slots, "slots", 1, _I64_ONLY, on)
     width = cache.shape[-1] - rope
-    _need(width > rope > 0, f"rows of {cache.shape[-1]} bytes do not hold {rope} position values and codes")
+    if not width > rope > 0:
+        _need(False, f"rows of {cache.shape[-1]} bytes do not hold {rope} position values and codes")
     if out is None:
-        out, o_stride = torch.empty((T, width), dtype=_BF16, device=on), width
+        out, o_stride = torch.empty_strided((T, width), (width, 1), dtype=_BF16, device=on), width
     else:
         o_shape, o_strides = _rows(out, "out", 2, _BF16_ONLY, on)
-        _need(tuple(o_shape) == (T, width), f"out {tuple(o_shape)}, {(T, width)} is needed")
+        if tuple(o_shape) != (T, width):
+            _need(False, f"out {tuple(o_shape)}, {(T, width)} is needed")
         o_stride = o_strides[0] if T > 1 else width
     B.check(B.lib().moe_latent_read_fp8(cache.data_ptr(), cache_scale.data_ptr(), n_slots, width - rope, rope, slots.data_ptr(),
                                         T, out.data_ptr(), o_stride, _raw_stream(on)))
