@@ -54,26 +54,25 @@ constexpr int kRopeWidth = 64;
 // What a load of eight rows of 8 bits reads where there is no page.
 __device__ __attribute__((aligned(16))) const uint8_t kNoPage[8 * (512 + 2 * kRopeWidth)] = {};
 
-__device__ __forceinline__ int seq_len(const LatentArgs& a, int b) {
-    const int n = a.lens[b];
-    const long most = (long)a.pages_per_seq * a.page_size;
-    return n < 0 ? 0 : (n > most ? (int)most : n);
-}
 __device__ __forceinline__ void seq_tokens(const LatentArgs& a, int b, int& first, int& count) {
+    auto within = [](int v, int most) { return v < 0 ? 0 : (v > most ? most : v); };
     if (a.prefixes && !a.groups) {  // one prefix for all
         first = 0;
         count = a.T;
-    } else if (a.prefixes) {
-        auto start = [&](int g) {
-            const int s = a.groups[g], in = s < 0 ? 0 : (s > a.seqs ? a.seqs : s), t = a.cu_q ? a.cu_q[in] : in * a.per_seq;
-            return t < 0 ? 0 : (t > a.T ? a.T : t);
-        };
-        first = start(b);
-        count = start(b + 1) - first;
-        if (count < 0) count = 0;
-    } else if (a.cu_q) {
-        const int u = a.cu_q[b], v = a.cu_q[b + 1];
-        first = u < 0 ? 0 : (u > a.T ? a.T : u);
+    } else if (a.cu_q || a.prefixes) {
+        int s = b, e = b + 1;
+        if (a.prefixes) {
+            s = a.groups[b];
+            e = a.groups[b + 1];
+            s = within(s, a.seqs);
+            e = within(e, a.seqs);
+        }
+        int u = s * a.per_seq, v = e * a.per_seq;
+        if (a.cu_q) {
+            u = a.cu_q[s];
+            v = a.cu_q[e];
+        }
+        first = within(u, a.T);
         count = (v > a.T ? a.T : v) - first;
         if (count < 0) count = 0;
     } else {
@@ -88,8 +87,10 @@ struct SeqShape {
 template <int ROWS>
 __device__ __forceinline__ SeqShape seq_shape(const LatentArgs& a, int b) {
     SeqShape s;
-    s.len = seq_len(a, b);
+    const int n = a.lens[b];
     seq_tokens(a, b, s.first, s.count);
+    const long most = (long)a.pages_per_seq * a.page_size;
+    s.len = n < 0 ? 0 : (n > most ? (int)most : n);
     s.tiles = s.len > kTile ? (s.len + kTile - 1) / kTile : 1;  // an empty sequence still writes its zeros
     s.blocks = (s.count * a.heads + ROWS - 1) / ROWS;
     s.passes = (s.blocks + a.group - 1) / a.group;
@@ -311,21 +312,6 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
             continue;
         }
         const int context = a.prefixes ? len : len - count;  // keys before the first new token
-        const int row = block * ROWS + rg * 32 + col;
-        const bool row_ok = row < count * a.heads;
-        const int token = row_ok ? row / a.heads : 0, head = row_ok ? row % a.heads : 0;
-        const long long mask = a.tree && row_ok ? a.tree[first + token] : 0;
-        bf16x8 qf[kSteps];
-        {
-            const uint16_t* p = a.q + (first + token) * a.q_stride_t + head * a.q_stride_h;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int at_inner = k >= kLat ? RANK + inner * 32 + (k - kLat) * 16 + half * 8
-                                     : NARROW  ? inner * (RANK / 2) + (k >> 1) * 32 + half * 16 + (k & 1) * 8
-                                               : inner * (RANK / 2) + k * 16 + half * 8;
-                qf[k] = __builtin_bit_cast(bf16x8, *as_global<u32x4>(p + at_inner));
-            }
-        }
         // Page and place of cache row t * 64 + lane (-1 past the end).
         const int32_t* my_pages = a.pages + seq * a.pages_stride;
         auto place_of = [&](int t, int& off) {
@@ -342,6 +328,27 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
             const int p = place_of(t, off);
             return p >= 0 ? as_global<int32_t>(my_pages)[p] : -1;
         };
+        // The loads that the others hang on come first: page numbers, then the
+        // queries, whose many rows take a while to ask for.
+        int off, page = page_of(t_first, off), off_next;
+        const int page_next = page_of(t_first + 1, off_next);
+        __builtin_amdgcn_sched_barrier(0);
+        const int row = block * ROWS + rg * 32 + col;
+        const bool row_ok = row < count * a.heads;
+        const int token = row_ok ? row / a.heads : 0, head = row_ok ? row % a.heads : 0;
+        const long long mask = a.tree && row_ok ? a.tree[first + token] : 0;
+        bf16x8 qf[kSteps];
+        {
+            const uint16_t* p = a.q + (first + token) * a.q_stride_t + head * a.q_stride_h;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const int at_inner = k >= kLat ? RANK + inner * 32 + (k - kLat) * 16 + half * 8
+                                     : NARROW  ? inner * (RANK / 2) + (k >> 1) * 32 + half * 16 + (k & 1) * 8
+                                               : inner * (RANK / 2) + k * 16 + half * 8;
+                qf[k] = __builtin_bit_cast(bf16x8, *as_global<u32x4>(p + at_inner));
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
         // Its address; a row past the end or on a page that is not in the
         // pool reads as zero and is masked.
         auto address = [&](int page, int off) {
@@ -414,20 +421,20 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
 
         float m = kNoMax, l = 0.0f;
         f32x16 o[kOut] = {};
-        int off, page = page_of(t_first, off);
         unsigned long long valid = __ballot((unsigned)page < (unsigned)a.n_pages), valid_next = 0;
         int place_next = -1;  // of this lane's row of the tile after the next
-        // the queries have landed: the compiler must not wait for them inside
-        // the loop, where other loads are on their way
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) asm volatile("" : "+v"(qf[k]));
         {
             const unsigned long long addr = address(page, off);
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) issue(i, 0, addr, lane);
             issue_powers(0, page, off);
         }
-        page = page_of(t_first + 1, off);
+        // the queries have landed, and the first tile: the compiler must not
+        // wait for them inside the loop, where other loads are on their way
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) asm volatile("" : "+v"(qf[k]));
+        page = page_next;
+        off = off_next;
         // The tile after the next has its page numbers brought to LDS by one
         // wave: a load into a register would be waited for with all others.
         auto issue_pages = [&](int t, int slot) {
