@@ -178,6 +178,7 @@ __device__ __forceinline__ u32x2 codes_transposed(unsigned addr) {
 __device__ __forceinline__ bf16x8 lds_chunk(unsigned addr) {
     return __builtin_bit_cast(bf16x8, *(lds_u32x4*)addr);
 }
+__device__ __forceinline__ unsigned lds_dword(unsigned addr) { return *(__attribute__((address_space(3))) unsigned*)addr; }
 __device__ __forceinline__ void lds_store(unsigned addr, u32x4 v) { *(lds_u32x4*)addr = v; }
 #pragma clang diagnostic pop
 

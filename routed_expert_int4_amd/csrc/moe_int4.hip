@@ -47,11 +47,6 @@ __device__ __forceinline__ void swap32(unsigned& a, unsigned& b) {
     a = r[0], b = r[1];
 }
 
-__device__ __forceinline__ void swap16(unsigned& a, unsigned& b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0], b = r[1];
-}
-
 __device__ __forceinline__ void store_out(const Int4Args& a, int t, int n, float v) {
     const long at = (long)t * a.ldo + n;
     if (a.out_f32)
@@ -167,134 +162,182 @@ __global__ void __launch_bounds__(kFewWaves * 64) int4_few_kernel(Int4Args a) {
     }
 }
 
-// Up to sixteen tokens: one matrix tile of them and the weights streamed from memory
-// once, straight into operand order.  A workgroup has NT x 16 weight rows and TT x 16 tokens; its waves
-// share the inner columns, 128 (a segment) at a time in turn, U segments
-// loaded one batch ahead, and join their sums through LDS in wave order.
-template <int GROUP, int NT, int TT, int WAVES, int U, int PER_SIMD>
-__global__ void __launch_bounds__(WAVES * 64, PER_SIMD) int4_rows_kernel(Int4Args a) {
-    constexpr int kPer = GROUP > 32 ? GROUP / 32 : 1, kGroups = 4 / kPer;  // blocks of 32 per group, groups per segment
-    __shared__ float sums[WAVES][NT * TT * 4][64];
+// Up to 32 tokens: one or two matrix tiles of them, and the weights streamed
+// from memory once.  A workgroup has NT x 16 weight rows; its eight waves share
+// the inner columns, 256 (a chunk) at a time in turn, and join their sums in
+// wave order.  What bounds a load is the number of lines that it touches, so
+// all go to LDS asynchronously, eight lanes to 128 bytes of a weight row and as
+// many or twice as many to a row of activations, and are read from there in
+// operand order; a wave waits for nothing but its own loads.  Activations come
+// 128 columns (a stage; 64 of two tiles) at a time.  The scales of a turn of
+// 8192 columns lie in LDS too.
+constexpr int kChunk = 256;
+template <int GROUP, int NT, int TT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, 2) int4_rows_kernel(Int4Args a) {
+    constexpr int kTurnColumns = WAVES * kChunk * 4;
+    constexpr int kStage = 128 / TT, kStages = kChunk / kStage, kSteps = kStage / 32;  // columns, stages per chunk, steps per stage
+    constexpr int kGroups = GROUP < kStage ? kStage / GROUP : 1, kPer = kSteps / kGroups;  // scales per stage, steps per scale
+    constexpr int kRows = NT * 16, kTurnGroups = kTurnColumns / GROUP, kScaleRow = kTurnGroups * 2 + 8;  // bytes; rows apart by two banks
+    constexpr int kWeights = kRows * kChunk / 2, kActs = TT * 16 * kStage * 2, kWave = 2 * (kWeights + kActs);
+    constexpr int kWeightLoads = kWeights / 1024, kActLoads = kActs / 1024;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * kWave];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[kRows * kScaleRow];
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = wave_in_block();
-    const int n0 = blockIdx.x * NT * 16, t0 = blockIdx.y * TT * 16;
-    const int segs = (a.K + 127) / 128;
-    const uint8_t* w_row[NT];
-    const uint16_t* s_row[NT];
-    const uint16_t* x_row[TT];
+    const int n0 = blockIdx.x * kRows;
+    const unsigned weights_at = lds_address(lds) + wave * kWave, acts_at = weights_at + 2 * kWeights;
+    // Piece p (16 bytes) of row r lies at place p ^ (r / 2 % 8) of 128 bytes,
+    // or p ^ (r % 16) of 256: a step's operand reads cover all banks.
+    constexpr int kActPieces = kStage / 8;
+    auto act_place = [](int piece, int r) { return (kActPieces == 16 ? piece ^ r : piece ^ (r / 2)) & (kActPieces - 1); };
+    const uint8_t* w_from[kWeightLoads];
+    int w_piece[kWeightLoads];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int n = n0 + i * 16 + col;
-        w_row[i] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
-        s_row[i] = a.scale + (long)(n < a.N ? n : a.N - 1) * a.lds;
+    for (int j = 0; j < kWeightLoads; ++j) {
+        const int r = j * 8 + (lane >> 3), n = n0 + r;
+        w_from[j] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
+        w_piece[j] = (lane & 7) ^ (r / 2 & 7);
     }
+    const uint16_t* x_from[kActLoads];
+    int x_piece[kActLoads];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        const int t = t0 + j * 16 + col;
-        x_row[j] = a.x + (long)(t < a.M ? t : a.M - 1) * a.ldx;
+    for (int j = 0; j < kActLoads; ++j) {
+        const int r = j * (64 / kActPieces) + lane / kActPieces;
+        x_from[j] = a.x + (long)(r < a.M ? r : a.M - 1) * a.ldx;
+        x_piece[j] = act_place(lane % kActPieces, r);
     }
     f32x4 acc[NT][TT] = {};
-    struct Batch {
-        u32x4 w[U][NT], x[U][TT][4];
-        uint16_t s[U][NT][kGroups];
-    } b[2];
-    auto load = [&](Batch& v, int batch) {
+    for (int k_turn = 0; k_turn < a.K; k_turn += kTurnColumns) {
+        const int columns = a.K - k_turn < kTurnColumns ? a.K - k_turn : kTurnColumns;
+        const int chunks = (columns + WAVES * kChunk - 1) / (WAVES * kChunk), stages = chunks * kStages;
+        auto first_column = [&](int chunk) { return k_turn + (chunk * WAVES + wave) * kChunk; };
+        // (columns past the last one: weights read others, activations zeros)
+        auto load_weights = [&](int chunk) {
+            const int k0 = first_column(chunk);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int seg = (batch * U + u) * WAVES + wave;
-            if (seg >= segs) return;
-            const int k0 = seg * 128;
-            const bool whole = k0 + 128 <= a.K;
+            for (int j = 0; j < kWeightLoads; ++j) {
+                const int k = k0 + w_piece[j] * 32;
+                load_to_lds16(w_from[j] + (k < a.K ? k / 2 : 0), weights_at + (chunk & 1) * kWeights + j * 1024);
+            }
+        };
+        auto load_acts = [&](int stage) {
+            const int k0 = first_column(stage / kStages) + stage % kStages * kStage;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int k = k0 + quad * 32;
-                v.w[u][i] = load_stream16(w_row[i] + (k < a.K ? k / 2 : 0));
-                if (whole) {
-                    // (a row of scales starts on two bytes)
-                    typedef uint16_t scales __attribute__((ext_vector_type(kGroups), aligned(2)));
-                    const scales s = *as_global<scales>(s_row[i] + seg * kGroups);
+            for (int j = 0; j < kActLoads; ++j) {
+                const int k = k0 + x_piece[j] * 8;
+                load_to_lds16(k < a.K ? static_cast<const void*>(x_from[j] + k) : kZeros, acts_at + (stage & 1) * kActs + j * 1024);
+            }
+        };
+        // a part of a row's scales per thread, zero past the last one
+        constexpr int kThreads = WAVES * 64 / kRows, kEach = kTurnGroups / kThreads;  // threads per row, scales of a thread
+        typedef uint16_t part __attribute__((ext_vector_type(kEach < 8 ? kEach : 8), aligned(2)));  // (a row of scales starts on two bytes)
+        constexpr int kPart = kEach < 8 ? kEach : 8, kParts = kEach / kPart;
+        part s_part[kParts];
+        const int s_row = threadIdx.x / kThreads, s_first = threadIdx.x % kThreads * kEach, groups = columns / GROUP;
+        {
+            const uint16_t* p = a.scale + (long)(n0 + s_row < a.N ? n0 + s_row : a.N - 1) * a.lds + k_turn / GROUP;
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) v.s[u][i][g] = s[g];
+            for (int i = 0; i < kParts; ++i) {
+                const int g = s_first + i * kPart;
+                if (g + kPart <= groups) {
+                    s_part[i] = *as_global<part>(p + g);
                 } else {
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
-                        v.s[u][i][g] = k0 + g * GROUP < a.K ? *as_global<uint16_t>(s_row[i] + seg * kGroups + g) : 0;
+                    for (int j = 0; j < kPart; ++j) s_part[i][j] = g + j < groups ? *as_global<uint16_t>(p + g + j) : (uint16_t)0;
                 }
             }
+        }
+        if (k_turn > 0) __syncthreads();  // the last turn's scales have served
+        load_weights(0);
+        load_acts(0);
+        if (chunks > 1) load_weights(1);
+        load_acts(1);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+            for (int j = 0; j < kPart; ++j)
+                *reinterpret_cast<uint16_t*>(scales + s_row * kScaleRow + (s_first + i * kPart + j) * 2) = s_part[i][j];
+        lds_barrier();
+        for (int stage = 0; stage < stages; ++stage) {
+            const int chunk = stage / kStages, in_chunk = stage % kStages;
+            // the loads behind this stage's: the next stage's activations, if
+            // any, and before them the next chunk's weights, if any
+            if (stage + 1 == stages)
+                wait_vmem<0>();
+            else if (in_chunk == 0 && chunk + 1 < chunks)
+                wait_vmem<kWeightLoads + kActLoads>();
+            else
+                wait_vmem<kActLoads>();
+            const unsigned w_at = weights_at + (chunk & 1) * kWeights, x_at = acts_at + (stage & 1) * kActs;
+            bf16x8 x[TT][kSteps];
+            unsigned w[NT][kSteps];
+            typedef uint16_t stage_scales __attribute__((ext_vector_type(kGroups)));
+            stage_scales s[NT];
 #pragma unroll
             for (int j = 0; j < TT; ++j)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int k = k0 + c * 32 + quad * 8;
-                    v.x[u][j][c] = *as_global<u32x4>(x_row[j] + (k < a.K ? k : 0));
-                    if (!whole && k >= a.K) v.x[u][j][c] = u32x4{0, 0, 0, 0};
+                for (int e = 0; e < kSteps; ++e) {
+                    const int r = j * 16 + col;
+                    x[j][e] = lds_chunk(x_at + r * (kStage * 2) + act_place(e * 4 + quad, r) * 16);
                 }
-        }
-    };
-    auto multiply = [&](Batch& v, int batch) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if ((batch * U + u) * WAVES + wave >= segs) return;
-            bf16x8 x[TT][4];
+            for (int i = 0; i < NT; ++i) {
+                const int r = i * 16 + col;
+#pragma unroll
+                for (int e = 0; e < kSteps; ++e)
+                    w[i][e] = lds_dword(w_at + r * (kChunk / 2) + (((in_chunk * kSteps + e) ^ (r / 2)) & 7) * 16 + quad * 4);
+                s[i] = *reinterpret_cast<const stage_scales*>(scales + r * kScaleRow +
+                                                              (first_column(chunk) - k_turn + in_chunk * kStage) / GROUP * 2);
+            }
             f32x4 start[TT][kGroups];
 #pragma unroll
             for (int j = 0; j < TT; ++j)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    x[j][c] = in_order(v.x[u][j][c]);
+                for (int e = 0; e < kSteps; ++e) {
+                    x[j][e] = in_order(__builtin_bit_cast(u32x4, x[j][e]));
                     const f32x4 zero = {};
-                    start[j][c / kPer] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        x[j][c], minus_one_and_half(), c % kPer ? start[j][c / kPer] : zero, 0, 0, 0);
+                    start[j][e / kPer] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        x[j][e], minus_one_and_half(), e % kPer ? start[j][e / kPer] : zero, 0, 0, 0);
                 }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                // from four blocks of 8 columns of a lane row's own 32 to the same block of each lane row
-                unsigned w[4] = {v.w[u][i][0], v.w[u][i][1], v.w[u][i][2], v.w[u][i][3]};
-                swap32(w[0], w[2]);
-                swap32(w[1], w[3]);
-                swap16(w[0], w[1]);
-                swap16(w[2], w[3]);
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    const float s = half_bits_to_float(v.s[u][i][g]);
                     f32x4 d[TT];
 #pragma unroll
-                    for (int c = g * kPer; c < (g + 1) * kPer; ++c) {
-                        const bf16x8 q = widen(w[c]);
+                    for (int e = g * kPer; e < (g + 1) * kPer; ++e) {
+                        const bf16x8 q = widen(w[i][e]);
 #pragma unroll
                         for (int j = 0; j < TT; ++j)
-                            d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j][c], q, c % kPer ? d[j] : start[j][g], 0, 0, 0);
+                            d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j][e], q, e % kPer ? d[j] : start[j][g], 0, 0, 0);
                     }
+                    const uint16_t bits = s[i][g];
+                    const float f = half_bits_to_float(bits);
 #pragma unroll
                     for (int j = 0; j < TT; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], s, acc[i][j][e]);
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], f, acc[i][j][e]);
                 }
-            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this stage's reads, before what is loaded over it
+            if (in_chunk + 1 == kStages && chunk + 2 < chunks) load_weights(chunk + 2);
+            if (stage + 2 < stages) load_acts(stage + 2);
         }
-    };
-    const int batches = (segs + U * WAVES - 1) / (U * WAVES);
-    load(b[0], 0);
-    for (int k = 0; k < batches; k += 2) {
-        if (k + 1 < batches) load(b[1], k + 1);
-        multiply(b[0], k);
-        if (k + 1 >= batches) break;
-        if (k + 2 < batches) load(b[0], k + 2);
-        multiply(b[1], k + 1);
     }
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(lds);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < TT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sums[wave][(i * TT + j) * 4 + e][lane] = acc[i][j][e];
+            for (int e = 0; e < 4; ++e) sums[((wave * NT * TT + i * TT + j) * 4 + e) * 64 + lane] = acc[i][j][e];
     __syncthreads();
     for (int at = threadIdx.x; at < NT * TT * 4 * 64; at += WAVES * 64) {
         const int v = at >> 6, l = at & 63;
-        const int n = n0 + (v / (TT * 4)) * 16 + (l & 15), t = t0 + (v / 4 % TT) * 16 + (l >> 4) * 4 + (v & 3);
+        const int n = n0 + v / (TT * 4) * 16 + (l & 15), t = v / 4 % TT * 16 + (l >> 4) * 4 + (v & 3);
         if (n >= a.N || t >= a.M) continue;
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) sum += sums[w][v][l];
+        for (int w = 0; w < WAVES; ++w) sum += sums[(w * NT * TT * 4 + v) * 64 + l];
         store_out(a, t, n, sum * kCodeUnit);
     }
 }
@@ -624,10 +667,23 @@ template <int GROUP, int TOKENS>
 void launch_few(const Int4Args& a, hipStream_t s) {
     hipLaunchKernelGGL((int4_few_kernel<GROUP, TOKENS>), dim3((a.N + 15) / 16), dim3(kFewWaves * 64), 0, s, a);
 }
-template <int GROUP, int NT, int TT, int WAVES, int U, int PER_SIMD>
+template <int GROUP, int NT, int TT, int WAVES>
 void launch_rows(const Int4Args& a, hipStream_t s) {
-    const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.M + 16 * TT - 1) / (16 * TT));
-    hipLaunchKernelGGL((int4_rows_kernel<GROUP, NT, TT, WAVES, U, PER_SIMD>), grid, dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((int4_rows_kernel<GROUP, NT, TT, WAVES>), dim3((a.N + 16 * NT - 1) / (16 * NT)), dim3(WAVES * 64), 0, s, a);
+}
+// A compute unit holds one workgroup of eight waves, or three of four with 16
+// weight rows: the shortest form that takes one round over the chip, and where
+// there are more, 32 rows to four waves (16 tokens; us; 8 and 4 waves with 16
+// rows, 8 and 4 with 32):
+//   2048 x 6144    7.2   9.3   9.1  11.7      12288 x 2048  11.7   7.9  10.8   8.9
+//   6144 x 8192   17.7  15.8  12.6  16.2      49152 x 8192   108    85    80    72
+template <int GROUP, int TT>
+void launch_rows_of(const Int4Args& a, hipStream_t s) {
+    const int rows = (a.N + 15) / 16;
+    if (rows <= 256 && a.K > 2048) return launch_rows<GROUP, 1, TT, 8>(a, s);
+    if (rows <= 512 && a.K > 2048) return launch_rows<GROUP, 2, TT, 8>(a, s);
+    if (rows <= 768) return launch_rows<GROUP, 1, TT, 4>(a, s);
+    launch_rows<GROUP, 2, TT, 4>(a, s);
 }
 template <int GROUP, int TT, int NT, int WT, int WN, int WK, int AHEAD, int PER_SIMD>
 void launch_tiles(const Int4Args& a, hipStream_t s) {
@@ -668,9 +724,8 @@ template <int GROUP>
 void launch_group(const Int4Args& a, hipStream_t s) {
     if (a.M == 1) return launch_few<GROUP, 1>(a, s);
     if (a.M == 2) return launch_few<GROUP, 2>(a, s);
-    // two tiles of weight rows share a wave's activations where there are rows
-    // enough (16 x 6144 x 8192: 21 us, 25 with one; 16 x 2048 x 6144: 15 and 11)
-    if (a.M <= 16) return a.N < 4096 ? launch_rows<GROUP, 1, 1, 8, 1, 4>(a, s) : launch_rows<GROUP, 2, 1, 8, 1, 3>(a, s);
+    if (a.M <= 16) return launch_rows_of<GROUP, 1>(a, s);
+    if (a.M <= 32) return launch_rows_of<GROUP, 2>(a, s);
     // (with larger groups the last shape needs more registers than there are)
     switch (best_shape(a, GROUP == 32 ? 6 : 5)) {
         case 0: return launch_tiles<GROUP, 1, 1, 1, 1, 8, 3, 2>(a, s);

@@ -146,3 +146,37 @@ def test_quantized_weights(A, group):
     step = scale.double().repeat_interleave(group, 1)
     assert bool(((back - w.double()).abs() <= step * (0.5 + 7 * 2.0 ** -10)).all())
     assert bool((back[5] == 0).all())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("N,K", [(4000, 2176), (4090, 8448), (4100, 2304), (8192, 8320), (8200, 2432), (1000, 2048), (12288, 256), (12290, 4224),
+                                 (7, 16512)])
+@pytest.mark.parametrize("M", [3, 16, 17, 32])
+def test_forms_for_up_to_32_tokens(A, M, N, K, group):
+    """Weight rows that fit one round over the chip in each form, and more;
+    inner columns of one turn of a workgroup and of several."""
+    codes, scale = weight(N, K, group, M + N + K)
+    x = inputs(M, K, M + K)
+    check(A.int4_linear(x, codes, scale), x, codes, scale)
+
+
+@pytest.mark.parametrize("M", [3, 29])
+@pytest.mark.parametrize("K,group", [(32, 32), (96, 32), (160, 32), (2080, 32), (4128, 32), (8224, 32), (2112, 64), (8256, 64)])
+def test_short_last_stages(A, M, K, group):
+    codes, scale = weight(70, K, group, K + M)
+    x = inputs(M, K, M)
+    check(A.int4_linear(x, codes, scale, out_dtype=torch.float32), x, codes, scale)
+
+
+@pytest.mark.parametrize("M", [2, 9, 32, 64])
+def test_what_lies_behind_the_columns_does_not_count(A, M):
+    """Strided operands whose rows go on with values that are not finite."""
+    N, K = 100, 544
+    codes, scale = weight(N, K, 32, M)
+    x = inputs(M, K, M)
+    wide_x = torch.full((M, K + 64), float("nan"), device=DEV).bfloat16()
+    wide_codes = torch.full((N, K // 2 + 48), 0x77, dtype=torch.uint8, device=DEV)
+    wide_scale = torch.full((N, K // 32 + 3), float("inf"), device=DEV).half()
+    wide_x[:, :K], wide_codes[:, :K // 2], wide_scale[:, :K // 32] = x, codes, scale
+    out = A.int4_linear(wide_x[:, :K], wide_codes[:, :K // 2], wide_scale[:, :K // 32], out_dtype=torch.float32)
+    check(out, x, codes, scale)
