@@ -342,109 +342,125 @@ __global__ void __launch_bounds__(WAVES * 64, 2) int4_rows_kernel(Int4Args a) {
     }
 }
 
-// More tokens: tiles on the matrix cores.  A stage is 64 WK inner columns; the
-// loads of AHEAD stages are on their way into registers, activations going on
-// to one of two LDS buffers (in the weights' order), weights staying with the
-// waves that own their rows.  WT x WN waves lie along tokens and weight rows,
-// TT x NT matrix tiles of 32 x 32 each; WK waves share the inner columns of a
-// stage and join their sums at the end.
+// More tokens: tiles on the matrix cores.  WT x WN waves lie along tokens and
+// weight rows, TT x NT matrix tiles of 32 x 32 each; WK waves share the inner
+// columns of a stage, 64 each, and join their sums at the end.  Everything goes
+// to LDS asynchronously, RING - 1 stages ahead, as it lies in memory (what
+// bounds a load is the number of lines that it touches), the scales of a turn
+// of 8192 columns at its beginning.
 // A weight row's 16 bytes of a lane half hold four dwords of 8 columns; swapped
 // with the other half's they are the four steps of 16, in dwords 0 2 1 3.
 __device__ __forceinline__ constexpr int at_step(int e) { return e == 1 ? 2 : e == 2 ? 1 : e; }
 
-template <int GROUP, int TT, int NT, int WT, int WN, int WK, int AHEAD, int PER_SIMD>
-__global__ void __launch_bounds__(WT * WN * WK * 64, PER_SIMD) int4_tile_kernel(Int4Args a) {
-    constexpr int kWaves = WT * WN * WK, kTokens = WT * TT * 32, kChunks = 8 * WK;  // 16-byte chunks of a row of a stage
-    constexpr int kStageBytes = kTokens * kChunks * 16, kLoads = kStageBytes / 1024 / kWaves;
+template <int GROUP, int TT, int NT, int WT, int WN, int WK, int RING>
+__global__ void __launch_bounds__(WT * WN * WK * 64, 2) int4_tile_kernel(Int4Args a) {
+    constexpr int kWaves = WT * WN * WK, kTokens = WT * TT * 32, kRows = WN * NT * 32, kColumns = 64 * WK, kTurnColumns = 8192;
+    constexpr int kActRow = kColumns * 2, kWeightRow = kColumns / 2, kActs = kTokens * kActRow, kWeights = kRows * kWeightRow;
+    constexpr int kActLoads = kActs / 1024 / kWaves, kWeightLoads = kWeights / 1024 / kWaves, kLoads = kActLoads + kWeightLoads;
     constexpr int kScales = GROUP == 32 ? 2 : 1, kSteps = 4 / kScales;  // scales of a wave's 64 columns, steps of 16 for each
-    constexpr int kSumBytes = WK > 1 ? (WK - 1) * WT * WN * TT * NT * 16 * 64 * 4 : 0;
-    constexpr int kLds = 2 * kStageBytes > kSumBytes ? 2 * kStageBytes : kSumBytes;
-    static_assert(kLoads * kWaves * 1024 == kStageBytes && kLds <= 160 * 1024, "stage");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+    constexpr int kSumBytes = WK > 1 ? (WK - 1) * WT * WN * TT * NT * 16 * 64 * 4 : 0, kRing = RING * (kActs + kWeights);
+    constexpr int kTurnGroups = kTurnColumns / GROUP, kScaleRow = kTurnGroups * 2 + 8;  // bytes; rows apart by two banks
+    static_assert(kActLoads * kWaves * 1024 == kActs && kWeightLoads * kWaves * 1024 == kWeights && kSumBytes <= kRing, "stage");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[kRows * kScaleRow];
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31, wave = wave_in_block();
     const int wk = wave % WK, wn = wave / WK % WN, wt = wave / (WK * WN);
     // workgroups of one die (they are dealt in turn) take neighbouring tiles
     // of the same weight rows
-    const int n_tiles = (a.N + WN * NT * 32 - 1) / (WN * NT * 32), t_tiles = (a.M + kTokens - 1) / kTokens;
+    const int n_tiles = (a.N + kRows - 1) / kRows, t_tiles = (a.M + kTokens - 1) / kTokens;
     const int per_die = (n_tiles * t_tiles + 7) / 8, tile = (blockIdx.x & 7) * per_die + (blockIdx.x >> 3);
     if (tile >= n_tiles * t_tiles) return;
-    const int t0 = tile % t_tiles * kTokens, n0 = (tile / t_tiles * WN + wn) * NT * 32;
-    const int stages = (a.K + 64 * WK - 1) / (64 * WK);
+    const int t0 = tile % t_tiles * kTokens, n_tile = tile / t_tiles * kRows, n0 = n_tile + wn * NT * 32;
     const unsigned lds0 = lds_address(lds);
-    const uint16_t* x_row[kLoads];
-    unsigned x_at[kLoads];
-    int x_k[kLoads];
+    // Piece c (16 bytes) of row r lies at place c mixed with the row so that
+    // the rows of an operand read cover all banks.
+    auto act_place = [](int r, int c) { return c ^ (r & 15); };
+    auto weight_place = [](int r, int c) { return c ^ (r / (8 / WK) & (2 * WK - 1)); };
+    const uint16_t* x_from[kActLoads];
+    int x_column[kActLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        // chunk c of row r lies at place c ^ (r & 7): the rows of an operand read cover all banks
-        const int at = (i * kWaves + wave) * 64 + lane, r = at / kChunks, c = at % kChunks, t = t0 + r;
-        x_row[i] = a.x + (long)(t < a.M ? t : a.M - 1) * a.ldx;
-        x_k[i] = c * 8;
-        x_at[i] = lds0 + (r * kChunks + (c ^ (r & 7))) * 16;
+    for (int i = 0; i < kActLoads; ++i) {
+        const int at = ((i * kWaves + wave) * 64 + lane) * 16, r = at / kActRow, t = t0 + r;
+        x_from[i] = a.x + (long)(t < a.M ? t : a.M - 1) * a.ldx;
+        x_column[i] = act_place(r, at % kActRow / 16) * 8;
     }
-    const uint8_t* w_row[NT];
-    const uint16_t* s_row[NT];
+    const uint8_t* w_from[kWeightLoads];
+    int w_column[kWeightLoads];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int n = n0 + i * 32 + col;
-        w_row[i] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
-        s_row[i] = a.scale + (long)(n < a.N ? n : a.N - 1) * a.lds;
+    for (int i = 0; i < kWeightLoads; ++i) {
+        const int at = ((i * kWaves + wave) * 64 + lane) * 16, r = at / kWeightRow, n = n_tile + r;
+        w_from[i] = a.w + (long)(n < a.N ? n : a.N - 1) * a.ldw;
+        w_column[i] = weight_place(r, at % kWeightRow / 16) * 32;
     }
-    struct Stage {
-        u32x4 x[kLoads], w[NT];
-        uint16_t s[NT][kScales];
-    } ring[AHEAD];
-    // (columns past the last one read the row's first and count as zero)
-    auto load = [&](Stage& v, int stage) {
+    f32x16 acc[NT][TT] = {};
+    for (int k_turn = 0; k_turn < a.K; k_turn += kTurnColumns) {
+        const int columns = a.K - k_turn < kTurnColumns ? a.K - k_turn : kTurnColumns, stages = (columns + kColumns - 1) / kColumns;
+        // (columns past the last one: weights read others, activations zeros)
+        auto issue = [&](int stage, int buf) {
+            const int k0 = k_turn + stage * kColumns;
+            const unsigned dst = lds0 + buf * (kActs + kWeights) + wave * 1024;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int k = stage * 64 * WK + x_k[i];
-            v.x[i] = *as_global<u32x4>(x_row[i] + (k < a.K ? k : 0));
-        }
-        const int k0 = (stage * WK + wk) * 64, k = k0 + half * 32;
+            for (int i = 0; i < kActLoads; ++i) {
+                const int k = k0 + x_column[i];
+                load_to_lds16(k < a.K ? static_cast<const void*>(x_from[i] + k) : kZeros, dst + i * kWaves * 1024);
+            }
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            v.w[i] = *as_global<u32x4>(w_row[i] + (k < a.K ? k / 2 : 0));
+            for (int i = 0; i < kWeightLoads; ++i) {
+                const int k = k0 + w_column[i];
+                load_to_lds16(w_from[i] + (k < a.K ? k / 2 : 0), dst + kActs + i * kWaves * 1024);
+            }
+        };
+        // a part of a row's scales per thread, zero past the last one
+        constexpr int kThreads = kWaves * 64 / kRows, kEach = kTurnGroups / kThreads, kPart = kEach < 8 ? kEach : 8, kParts = kEach / kPart;
+        typedef uint16_t part __attribute__((ext_vector_type(kPart), aligned(2)));  // (a row of scales starts on two bytes)
+        part s_part[kParts];
+        const int s_row = threadIdx.x / kThreads, s_first = threadIdx.x % kThreads * kEach, groups = columns / GROUP;
+        const uint16_t* p = a.scale + (long)(n_tile + s_row < a.N ? n_tile + s_row : a.N - 1) * a.lds + k_turn / GROUP;
 #pragma unroll
-            for (int g = 0; g < kScales; ++g) {
-                const int kg = k0 + g * 32;
-                v.s[i][g] = *as_global<uint16_t>(s_row[i] + (kg < a.K ? kg / GROUP : 0));
+        for (int i = 0; i < kParts; ++i) {
+            const int g = s_first + i * kPart;
+            if (g + kPart <= groups) {
+                s_part[i] = *as_global<part>(p + g);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPart; ++j) s_part[i][j] = g + j < groups ? *as_global<uint16_t>(p + g + j) : (uint16_t)0;
             }
         }
-    };
-    auto put = [&](const Stage& v, int stage) {
+        if (k_turn > 0) __syncthreads();  // the last turn's scales and stages have served
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            u32x4 x = v.x[i];
-            if (stage * 64 * WK + x_k[i] >= a.K) x = u32x4{0, 0, 0, 0};
-            lds_store(x_at[i] + (stage & 1) * kStageBytes, __builtin_bit_cast(u32x4, in_order(x)));
-        }
-    };
-    f32x16 acc[NT][TT] = {};
-    // Nothing in the loop hangs on the stage (one past the last loads anything
-    // and counts as zero): where loads may or may not have been issued, the
-    // compiler waits for more than it has to.
+        for (int i = 0; i < RING - 1; ++i)
+            if (i < stages) issue(i, i);
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) load(ring[d], d);
-    put(ring[0], 0);
-    for (int stage0 = 0; stage0 < stages; stage0 += AHEAD) {
+        for (int i = 0; i < kParts; ++i)
 #pragma unroll
-        for (int r = 0; r < AHEAD; ++r) {
-            const int stage = stage0 + r;
-            lds_barrier();  // the stage is in LDS, and every wave is done with the other buffer
+            for (int j = 0; j < kPart; ++j)
+                *reinterpret_cast<uint16_t*>(scales + s_row * kScaleRow + (s_first + i * kPart + j) * 2) = s_part[i][j];
+        int buf = 0;
+        for (int stage = 0; stage < stages; ++stage) {
+            if (stage + RING - 2 < stages)
+                wait_vmem<(RING - 2) * kLoads>();
+            else
+                wait_vmem<0>();
+            lds_barrier();  // the stage is in LDS, and every wave is done with the one before
+            if (stage + RING - 1 < stages) issue(stage + RING - 1, buf == 0 ? RING - 1 : buf - 1);
+            const unsigned from = lds0 + buf * (kActs + kWeights);
+            buf = buf == RING - 1 ? 0 : buf + 1;
             unsigned w[NT][4];
             float s[NT][kScales];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
+                const int r = (wn * NT + i) * 32 + col;
+                const u32x4 v = __builtin_bit_cast(u32x4, lds_chunk(from + kActs + r * kWeightRow + weight_place(r, wk * 2 + half) * 16));
 #pragma unroll
-                for (int d = 0; d < 4; ++d) w[i][d] = ring[r].w[i][d];
+                for (int d = 0; d < 4; ++d) w[i][d] = v[d];
                 swap32(w[i][0], w[i][1]);
                 swap32(w[i][2], w[i][3]);
 #pragma unroll
-                for (int g = 0; g < kScales; ++g) s[i][g] = half_bits_to_float(ring[r].s[i][g]);
+                for (int g = 0; g < kScales; ++g) {
+                    const uint16_t bits = *reinterpret_cast<const uint16_t*>(scales + r * kScaleRow + (stage * kColumns + wk * 64 + g * 32) / GROUP * 2);
+                    s[i][g] = half_bits_to_float(bits);
+                }
             }
-            load(ring[r], stage + AHEAD);
-            const unsigned from = lds0 + (stage & 1) * kStageBytes;
 #pragma unroll
             for (int g = 0; g < kScales; ++g) {
                 f32x16 start[TT];
@@ -453,8 +469,8 @@ __global__ void __launch_bounds__(WT * WN * WK * 64, PER_SIMD) int4_tile_kernel(
                 for (int j = 0; j < TT; ++j)
 #pragma unroll
                     for (int e = 0; e < kSteps; ++e) {
-                        const int row = (wt * TT + j) * 32 + col, c = wk * 8 + (g * kSteps + e) * 2 + half;
-                        x[j][e] = lds_chunk(from + (row * kChunks + (c ^ (row & 7))) * 16);
+                        const int r = (wt * TT + j) * 32 + col, c = wk * 8 + (g * kSteps + e) * 2 + half;
+                        x[j][e] = in_order(__builtin_bit_cast(u32x4, lds_chunk(from + r * kActRow + act_place(r, c) * 16)));
                         const f32x16 zero = {};
                         start[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][e], minus_one_and_half(), e ? start[j] : zero, 0, 0, 0);
                     }
@@ -473,7 +489,6 @@ __global__ void __launch_bounds__(WT * WN * WK * 64, PER_SIMD) int4_tile_kernel(
                     }
                 }
             }
-            put(ring[(r + 1) % AHEAD], stage + 1);
         }
     }
     if constexpr (WK > 1) {
@@ -525,7 +540,12 @@ __global__ void __launch_bounds__(WT * WN * 64, PER_SIMD) int4_many_kernel(Int4A
     constexpr int kStageBytes = kTokens * kChunks * 16, kLoads = kStageBytes / 1024 / kWaves;
     constexpr int kScales = GROUP == 32 ? 2 : 1, kSteps = 4 / kScales;  // scales of a wave's 64 columns, steps of 16 for each
     static_assert(kLoads * kWaves * 1024 == kStageBytes, "stage");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStageBytes];
+    // Weights come 128 columns (a chunk, two stages) at a time, scales 256.
+    constexpr int kRows = WN * NT * 32, kChunkBytes = kRows * 64, kChunkLoads = kChunkBytes / 1024 / kWaves, kPart = 256 / GROUP;
+    static_assert(kChunkLoads * kWaves * 1024 == kChunkBytes && kRows <= kWaves * 64, "chunk");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (kStageBytes + kChunkBytes)];
+    typedef uint16_t part __attribute__((ext_vector_type(kPart), aligned(2)));  // (a row of scales starts on two bytes)
+    __shared__ __attribute__((aligned(16))) uint16_t scales[2][kRows][kPart];
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31, wave = wave_in_block();
     const int wn = wave % WN, wt = wave / WN;
     // workgroups of one die (they are dealt in turn) take neighbouring tiles
@@ -537,28 +557,32 @@ __global__ void __launch_bounds__(WT * WN * 64, PER_SIMD) int4_many_kernel(Int4A
     const int stages = (a.K + 63) / 64;
     const unsigned lds0 = lds_address(lds);
     // Addresses are a base for the tile and the stage and an offset that a lane
-    // keeps; rows past the last one repeat it.  Chunk c of row r lies at place
-    // c ^ (r & 7): the rows of an operand read cover all banks.
-    unsigned x_off[kLoads], w_off[NT], s_off[NT];
+    // keeps; rows past the last one repeat it.  Chunk c of row r of the
+    // activations lies at place c ^ (r & 7), of the weights at c ^ (r / 4 & 3):
+    // the rows of an operand read cover all banks.  (What bounds loads is the
+    // number of lines that they touch: weights straight into operand order
+    // would be 32 lines to a load of 1 KB.)
+    unsigned x_off[kLoads], w_off[kChunkLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int at = (i * kWaves + wave) * 64 + lane, r = at / kChunks, c = (at % kChunks) ^ (r & 7);
         const int last = a.M - 1 - t0;
         x_off[i] = (unsigned)(r < last ? r : last) * (unsigned)(a.ldx * 2) + c * 16;
     }
+    const int last_row = a.N - 1 - n_tile;
+    auto weight_place = [](int r, int c) { return c ^ (r >> 2 & 3); };
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int r = n0 - n_tile + i * 32 + col, last = a.N - 1 - n_tile, row = r < last ? r : last;
-        w_off[i] = (unsigned)row * (unsigned)a.ldw + half * 16;
-        s_off[i] = (unsigned)row * (unsigned)(a.lds * 2);
+    for (int i = 0; i < kChunkLoads; ++i) {
+        const int r = (i * kWaves + wave) * 16 + (lane >> 2);
+        w_off[i] = (unsigned)(r < last_row ? r : last_row) * (unsigned)a.ldw + weight_place(r, lane & 3) * 16;
     }
     const uint8_t* const x_base = reinterpret_cast<const uint8_t*>(a.x + (long)t0 * a.ldx);
     const uint8_t* const w_base = a.w + (long)n_tile * a.ldw;
-    const uint8_t* const s_base = reinterpret_cast<const uint8_t*>(a.scale + (long)n_tile * a.lds);
-    u32x4 w_next[NT];
-    typedef uint16_t scales_t __attribute__((ext_vector_type(kScales), aligned(2)));  // (a row of scales starts on two bytes)
-    scales_t s_next[NT];
-    auto issue = [&](int stage, int buf) {
+    const int s_row = threadIdx.x < last_row ? threadIdx.x : last_row;
+    const uint16_t* const s_base = a.scale + (long)(n_tile + s_row) * a.lds;
+    const int groups = a.K / GROUP;
+    part s_next;
+    auto issue_acts = [&](int stage, int buf) {
         const bool whole = stage * 64 + 64 <= a.K;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -571,46 +595,66 @@ __global__ void __launch_bounds__(WT * WN * 64, PER_SIMD) int4_many_kernel(Int4A
                 load_to_lds16(stage * 64 + c * 8 < a.K ? p : kZeros, dst);
             }
         }
-        const uint8_t *w = w_base + (long)stage * 32, *s = s_base + (long)(stage * 64 / GROUP) * 2;
-        if (whole) {
+    };
+    auto issue_weights = [&](int chunk) {
+        const bool whole = chunk * 128 + 128 <= a.K;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                w_next[i] = *as_global<u32x4>(w + w_off[i]);
-                s_next[i] = *as_global<scales_t>(s + s_off[i]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                w_next[i] = *as_global<u32x4>(w + w_off[i] - half * 16);
-                s_next[i] = scales_t(*as_global<uint16_t>(s + s_off[i]));
+        for (int i = 0; i < kChunkLoads; ++i) {
+            const unsigned dst = lds0 + 2 * kStageBytes + (chunk & 1) * kChunkBytes + (i * kWaves + wave) * 1024;
+            if (whole) {
+                load_to_lds16(w_base + (long)chunk * 64, w_off[i], dst);
+            } else {  // (the product with zero)
+                const int c = weight_place((i * kWaves + wave) * 16 + (lane >> 2), lane & 3);
+                load_to_lds16(w_base + w_off[i] + (chunk * 128 + c * 32 < a.K ? (long)chunk * 64 : -(long)c * 16), dst);
             }
         }
     };
+    auto load_scales = [&](int turn) {  // of 256 columns, a row per thread; zero past the last one
+        const int first = turn * kPart;
+        if (first + kPart <= groups) {
+            s_next = *as_global<part>(s_base + first);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) s_next[i] = first + i < groups ? *as_global<uint16_t>(s_base + first + i) : (uint16_t)0;
+        }
+    };
     f32x16 acc[NT][TT] = {};
-    issue(0, 0);
+    load_scales(0);
+    issue_acts(0, 0);
+    issue_weights(0);
     for (int stage = 0; stage < stages; ++stage) {
         const int buf = stage & 1;
         wait_vmem<0>();
+        if (stage % 4 == 0 && (int)threadIdx.x < kRows) {
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) scales[stage >> 2 & 1][threadIdx.x][i] = s_next[i];
+        }
+        lds_barrier();  // the stage is in LDS, and every wave is done with the other buffer
+        if (stage + 1 < stages) {
+            if (stage % 4 == 3) load_scales((stage + 1) / 4);
+            issue_acts(stage + 1, buf ^ 1);
+            if (stage & 1) issue_weights((stage + 1) / 2);
+        }
         unsigned w[NT][4];
         float s[NT][kScales];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            asm volatile("" : "+v"(w_next[i]));
+            const int r = (wn * NT + i) * 32 + col;
+            const u32x4 v = __builtin_bit_cast(u32x4, lds_chunk(lds0 + 2 * kStageBytes + (stage >> 1 & 1) * kChunkBytes + r * 64 +
+                                                                weight_place(r, (stage & 1) * 2 + half) * 16));
 #pragma unroll
-            for (int d = 0; d < 4; ++d) w[i][d] = w_next[i][d];
+            for (int d = 0; d < 4; ++d) w[i][d] = v[d];
             // lane halves hold 32 columns each: to halves of 8 columns of the
             // same 16, which leaves the four steps in dwords 0 2 1 3
             swap32(w[i][0], w[i][1]);
             swap32(w[i][2], w[i][3]);
 #pragma unroll
             for (int g = 0; g < kScales; ++g) {
-                const uint16_t bits = s_next[i][g];
+                const uint16_t bits = scales[stage >> 2 & 1][r][(stage % 4 * 64 + g * 32) / GROUP];
                 s[i][g] = half_bits_to_float(bits);
                 asm("" : "+v"(s[i][g]));  // (or every product would convert it again)
             }
         }
-        lds_barrier();  // the stage is in LDS, and every wave is done with the other buffer
-        if (stage + 1 < stages) issue(stage + 1, buf ^ 1);
 #pragma unroll
         for (int g = 0; g < kScales; ++g) {
             f32x16 start[TT];
@@ -685,10 +729,10 @@ void launch_rows_of(const Int4Args& a, hipStream_t s) {
     if (rows <= 768) return launch_rows<GROUP, 1, TT, 4>(a, s);
     launch_rows<GROUP, 2, TT, 4>(a, s);
 }
-template <int GROUP, int TT, int NT, int WT, int WN, int WK, int AHEAD, int PER_SIMD>
+template <int GROUP, int TT, int NT, int WT, int WN, int WK, int RING>
 void launch_tiles(const Int4Args& a, hipStream_t s) {
     const long tiles = (long)((a.N + WN * NT * 32 - 1) / (WN * NT * 32)) * ((a.M + WT * TT * 32 - 1) / (WT * TT * 32));
-    hipLaunchKernelGGL((int4_tile_kernel<GROUP, TT, NT, WT, WN, WK, AHEAD, PER_SIMD>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+    hipLaunchKernelGGL((int4_tile_kernel<GROUP, TT, NT, WT, WN, WK, RING>), dim3((unsigned)((tiles + 7) / 8 * 8)),
                        dim3(WT * WN * WK * 64), 0, s, a);
 }
 template <int GROUP, int TT, int NT, int WT, int WN, int PER_SIMD>
@@ -699,22 +743,27 @@ void launch_many(const Int4Args& a, hipStream_t s) {
 }
 
 // Shapes of tiles and what a stage of inner columns takes them, in
-// nanoseconds: alone on a compute unit, and with as many as fit (measured; a
-// stage is a chain of latencies for the small ones, instructions for the large).
+// nanoseconds: alone on a compute unit, and with as many as fit (measured; the
+// large ones are bound by instructions, the small ones by one step after the
+// other), with kBegin for a tile's beginning and end.
 struct Shape {
     int tokens, rows, columns, alone, together, fit;
 };
-constexpr Shape kShapes[] = {{32, 32, 512, 1000, 1000, 1}, {32, 64, 256, 800, 800, 1},   {64, 64, 256, 1230, 1230, 1},
-                             {64, 128, 128, 1050, 1050, 1}, {128, 128, 64, 1150, 1650, 2}, {128, 192, 64, 1500, 2550, 2}};
-// The shape that takes least time over the rounds it needs on the chip.
-int best_shape(const Int4Args& a, int count) {
+constexpr Shape kShapes[] = {{32, 32, 512, 900, 900, 1},    {32, 64, 256, 770, 770, 1},    {64, 64, 256, 1250, 1250, 1},
+                             {64, 128, 128, 1050, 1050, 1}, {128, 128, 64, 1200, 1750, 2}, {128, 192, 64, 1560, 2330, 2}};
+constexpr double kBegin = 3000.0;
+// The shape that takes least time over the rounds it needs on the chip (us at
+// K = 8192; 64 x 6144: 35, 29, 44, 72 in the first four; 512 x 6144: 198, 155,
+// 131, 144, 159, 200; 1024 x 6144: 442, 313, 260, 232, 207, 203).
+int best_shape(const Int4Args& a) {
     int best = 0;
     double least = 0.0;
-    for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
         const Shape& s = kShapes[i];
         auto up = [](long n, long d) { return (n + d - 1) / d; };
         const long per_cu = up(up(a.M, s.tokens) * up(a.N, s.rows), 256), full = per_cu / s.fit, rest = per_cu % s.fit;
-        const double time = (double)up(a.K, s.columns) * (double)(full * s.together + rest * s.alone);
+        const double stages = (double)up(a.K, s.columns);
+        const double time = (double)full * (stages * s.together + kBegin) + (rest ? stages * s.alone + kBegin : 0.0);
         if (i == 0 || time < least) least = time, best = i;
     }
     return best;
@@ -726,15 +775,14 @@ void launch_group(const Int4Args& a, hipStream_t s) {
     if (a.M == 2) return launch_few<GROUP, 2>(a, s);
     if (a.M <= 16) return launch_rows_of<GROUP, 1>(a, s);
     if (a.M <= 32) return launch_rows_of<GROUP, 2>(a, s);
-    // (with larger groups the last shape needs more registers than there are)
-    switch (best_shape(a, GROUP == 32 ? 6 : 5)) {
-        case 0: return launch_tiles<GROUP, 1, 1, 1, 1, 8, 3, 2>(a, s);
-        case 1: return launch_tiles<GROUP, 1, 1, 1, 2, 4, 3, 2>(a, s);
-        case 2: return launch_tiles<GROUP, 2, 1, 1, 2, 4, 4, 2>(a, s);
-        case 3: return launch_tiles<GROUP, 2, 1, 1, 4, 2, 4, 2>(a, s);
+    switch (best_shape(a)) {
+        case 0: return launch_tiles<GROUP, 1, 1, 1, 1, 8, 3>(a, s);
+        case 1: return launch_tiles<GROUP, 1, 1, 1, 2, 4, 4>(a, s);
+        case 2: return launch_tiles<GROUP, 2, 1, 1, 2, 4, 3>(a, s);
+        case 3: return launch_tiles<GROUP, 2, 1, 1, 4, 2, 3>(a, s);
         case 4: return launch_many<GROUP, 2, 2, 2, 2, 2>(a, s);
         default:
-            if constexpr (GROUP == 32) launch_many<GROUP, 2, 3, 2, 2, 2>(a, s);
+            launch_many<GROUP, 2, 3, 2, 2, 2>(a, s);
     }
 }
 

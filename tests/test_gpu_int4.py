@@ -180,3 +180,14 @@ def test_what_lies_behind_the_columns_does_not_count(A, M):
     wide_x[:, :K], wide_codes[:, :K // 2], wide_scale[:, :K // 32] = x, codes, scale
     out = A.int4_linear(wide_x[:, :K], wide_codes[:, :K // 2], wide_scale[:, :K // 32], out_dtype=torch.float32)
     check(out, x, codes, scale)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(40, 200, 8320), (64, 6200, 8448), (130, 4100, 8320), (256, 6144, 8448), (300, 7000, 640), (1025, 6150, 384),
+                                   (640, 12300, 128)])
+def test_forms_for_more_tokens(A, M, N, K, group):
+    """Each shape of tiles, its last tiles cut by either edge, and inner
+    columns of one turn of a workgroup and of two."""
+    codes, scale = weight(N, K, group, M + N + K)
+    x = inputs(M, K, M + K)
+    check(A.int4_linear(x, codes, scale), x, codes, scale)
