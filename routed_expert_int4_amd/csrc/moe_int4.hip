@@ -12,10 +12,19 @@
 // sum q x / 16, with no rounding but fp32's.
 //
 // Activations are the matrix instruction's rows, weights its columns: a lane
-// then holds one weight row's results and needs one scale per group.  A
-// weight row's 16 bytes per lane hold four blocks of 8 columns of one group of
-// 32; the swaps between the lane rows of a wave turn them into operands whose
-// lanes share a group.
+// then holds one weight row's results and needs one scale per group.
+//
+// Few tokens are bound by reading the weights, and a load by the lines that it
+// touches, some two cycles each: 32 bytes of 32 rows cost four times what 128
+// bytes of eight do.  Many are bound by what the vector unit does beside the
+// matrix cores, and the two overlap only in part: 64 columns of a wave's 64 x 96
+// results are 32 matrix instructions and 370 others, 192 of them the scaling of
+// the groups' sums (for every result and group, whatever the tile).
+//
+// Measured, 6144 x 8192, group 32 (25 MB of codes, 3 of scales): 1 token 9.6 us
+// (3.0 TB/s, a quarter of it launch and first latency; 49152 rows 51 us, 4.4
+// TB/s), 16 tokens 12.5, 32 17.6, 64 28, 128 45, 512 135, 2048 290 (0.71
+// PFLOP/s; group 128 265, 0.78).
 #include "moe_block.h"
 #include "moe_block_device.h"
 
@@ -61,7 +70,8 @@ __device__ __forceinline__ void store_out(const Int4Args& a, int t, int n, float
 // lanes read 128 neighbouring bytes of a row.  The eight waves of a workgroup
 // share the inner columns of 16 weight rows, 256 at a time in turn; all loads
 // of a turn of 8192 columns are on their way before the activations, put in the
-// weights' order, have come to LDS.
+// weights' order, have come to LDS.  (1 x 6144 x 8192: 9.6 us; four lanes to a
+// row 13.8, matrix instructions 22.9.)
 constexpr int kTurnSegs = 4, kFewWaves = 8, kSeg = 256, kTurn = kTurnSegs * kFewWaves * kSeg;
 template <int GROUP, int TOKENS>
 __global__ void __launch_bounds__(kFewWaves * 64) int4_few_kernel(Int4Args a) {
@@ -170,7 +180,9 @@ __global__ void __launch_bounds__(kFewWaves * 64) int4_few_kernel(Int4Args a) {
 // many or twice as many to a row of activations, and are read from there in
 // operand order; a wave waits for nothing but its own loads.  Activations come
 // 128 columns (a stage; 64 of two tiles) at a time.  The scales of a turn of
-// 8192 columns lie in LDS too.
+// 4096 or 8192 columns lie in LDS too.  (16 x 6144 x 8192: 12.5 us; everything
+// straight into registers in operand order, 64 bytes of 16 rows to a load, 21.4
+// and, with more of it on its way, 24 and 27.)
 constexpr int kChunk = 256;
 template <int GROUP, int NT, int TT, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2) int4_rows_kernel(Int4Args a) {
@@ -347,7 +359,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) int4_rows_kernel(Int4Args a) {
 // columns of a stage, 64 each, and join their sums at the end.  Everything goes
 // to LDS asynchronously, RING - 1 stages ahead, as it lies in memory (what
 // bounds a load is the number of lines that it touches), the scales of a turn
-// of 8192 columns at its beginning.
+// of 8192 columns at its beginning.  (64 x 6144 x 8192: 28 us; weights and
+// scales straight into registers 34.)
 // A weight row's 16 bytes of a lane half hold four dwords of 8 columns; swapped
 // with the other half's they are the four steps of 16, in dwords 0 2 1 3.
 __device__ __forceinline__ constexpr int at_step(int e) { return e == 1 ? 2 : e == 2 ? 1 : e; }
@@ -532,8 +545,10 @@ __global__ void __launch_bounds__(WT * WN * WK * 64, 2) int4_tile_kernel(Int4Arg
 // Many tokens: one wave to the whole inner dimension of its TT x NT matrix
 // tiles, WT x WN waves along tokens and weight rows.  Of a stage of 64 columns
 // the activations come to LDS asynchronously, a stage ahead, and are put in
-// order as they are read: two waves fit a SIMD, and what counts is
-// what instructions cost.
+// order as they are read; weights come two stages at a time, scales four.  Two
+// waves of two workgroups fit a SIMD, and what counts is what instructions cost.
+// (2048 x 6144 x 8192: 128 x 192 tiles 290 us, 128 x 128 350; weights and scales
+// straight into registers 325; one wave per SIMD 732.)
 template <int GROUP, int TT, int NT, int WT, int WN, int PER_SIMD>
 __global__ void __launch_bounds__(WT * WN * 64, PER_SIMD) int4_many_kernel(Int4Args a) {
     constexpr int kWaves = WT * WN, kTokens = WT * TT * 32, kChunks = 8;  // 16-byte chunks of a row of a stage
