@@ -329,7 +329,7 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
             return p >= 0 ? as_global<int32_t>(my_pages)[p] : -1;
         };
         // The loads that the others hang on come first: page numbers, then the
-        // queries, whose many rows take a while to ask for.
+        // queries.
         int off, page = page_of(t_first, off), off_next;
         const int page_next = page_of(t_first + 1, off_next);
         __builtin_amdgcn_sched_barrier(0);
@@ -337,18 +337,35 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
         const bool row_ok = row < count * a.heads;
         const int token = row_ok ? row / a.heads : 0, head = row_ok ? row % a.heads : 0;
         const long long mask = a.tree && row_ok ? a.tree[first + token] : 0;
-        bf16x8 qf[kSteps];
+        // The workgroup's queries go to LDS by lines, behind the first tile's
+        // buffer, and from there to the waves' registers: straight from memory
+        // every wave's loads would touch 32 lines each (decode of 1013 rows 20.4
+        // us).  Chunk c (16 bytes) of row r lies at place c ^ (r & 15), of its
+        // position part at c ^ (r / 2 & 7).
+        constexpr int kQueryRow = RANK * 2, kQueryRows = 1024 / kQueryRow, kQueryLoads = ROWS / kQueryRows / kWaves;
+        static_assert(ROWS * (kQueryRow + kRopeWidth * 2) <= (kBuffers - 1) * kTileBytes, "queries");
+        const unsigned query0 = lds0 + kTileBytes, query_rope0 = query0 + ROWS * kQueryRow;
         {
-            const uint16_t* p = a.q + (first + token) * a.q_stride_t + head * a.q_stride_h;
+            // lane r has the address of row r
+            const int row = block * ROWS + lane, at_row = row < count * a.heads ? row : 0;
+            const auto from = (unsigned long long)(a.q + (first + at_row / a.heads) * a.q_stride_t + at_row % a.heads * a.q_stride_h);
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int at_inner = k >= kLat ? RANK + inner * 32 + (k - kLat) * 16 + half * 8
-                                     : NARROW  ? inner * (RANK / 2) + (k >> 1) * 32 + half * 16 + (k & 1) * 8
-                                               : inner * (RANK / 2) + k * 16 + half * 8;
-                qf[k] = __builtin_bit_cast(bf16x8, *as_global<u32x4>(p + at_inner));
+            for (int i = 0; i < kQueryLoads; ++i) {
+                const int r0 = (i * kWaves + wave) * kQueryRows, r = r0 + lane / (kQueryRow / 16);
+                const unsigned in_row = ((lane % (kQueryRow / 16)) ^ (r & 15)) * 16;
+                if constexpr (kQueryRows == 1) {
+                    const unsigned lo = __builtin_amdgcn_readlane((unsigned)from, r0),
+                                   hi = __builtin_amdgcn_readlane((unsigned)(from >> 32), r0);
+                    load_to_lds16_lane((unsigned long long)hi << 32 | lo, in_row, query0 + r0 * kQueryRow);
+                } else {
+                    load_to_lds16(reinterpret_cast<const uint8_t*>(__shfl(from, r)) + in_row, query0 + r0 * kQueryRow);
+                }
             }
+            const int r = wave * 8 + (lane >> 3);
+            load_to_lds16(reinterpret_cast<const uint8_t*>(__shfl(from, r)) + kQueryRow + (((lane & 7) ^ (r >> 1)) & 7) * 16,
+                          query_rope0 + wave * 8 * kRopeWidth * 2);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        wait_vmem<0>();  // all of these, as the page numbers are waited for in any case
         // Its address; a row past the end or on a page that is not in the
         // pool reads as zero and is masked.
         auto address = [&](int page, int off) {
@@ -429,10 +446,21 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
             for (int i = 0; i < kLoads; ++i) issue(i, 0, addr, lane);
             issue_powers(0, page, off);
         }
-        // the queries have landed, and the first tile: the compiler must not
-        // wait for them inside the loop, where other loads are on their way
+        lds_barrier();  // the queries of all waves have landed
+        bf16x8 qf[kSteps];
+        {
+            const int r = rg * 32 + col;
+            const unsigned lat_at = query0 + r * kQueryRow + inner * RANK + ((half << NARROW) ^ (r & 15)) * 16;
+            const unsigned rope_from = query_rope0 + r * (kRopeWidth * 2) + (((inner * 4 + half) ^ (r >> 1)) & 7) * 16;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) asm volatile("" : "+v"(qf[k]));
+            for (int k = 0; k < kSteps; ++k) {
+                const int mixed = NARROW ? (k >> 1 & 3) * 64 + (k & 1) * 16 : (k & 7) * 32;
+                qf[k] = lds_chunk(k < kLat ? (lat_at ^ mixed) + (k >> 3) * 256 : rope_from ^ (k - kLat) * 32);
+            }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) asm volatile("" : "+v"(qf[k]));
+        }
+        lds_barrier();  // their place may be loaded over
         page = page_next;
         off = off_next;
         // The tile after the next has its page numbers brought to LDS by one
