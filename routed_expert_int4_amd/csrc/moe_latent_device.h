@@ -24,9 +24,9 @@
 //
 // Measured, rank 512, 64 heads: 32 sequences of 16384 rows, one token each,
 // 132 us (4.6 TB/s), four tokens 357 us (0.82 PFLOP/s); trees of four tokens
-// over ragged rows, 10400 on average, 213 to 229 us.  One sequence, one token:
-// 1013 rows 21 us, 16384 rows 34 us, 65536 rows 41 us.  Rank 256: 81, 241, and
-// 16, 29 and 31 us.  A tile takes a workgroup 2.6 us, of which matrix
+// over ragged rows, 10400 on average, 208 us.  One sequence, one token: 1013 rows
+// 17.5 us, 16384 rows 32 us, 65536 rows 39 us.  Rank 256: 80, 240, and
+// 16, 27 and 30 us.  A tile takes a workgroup 2.6 us, of which matrix
 // instructions are 1.0; the loads stall the waves that issue them for about 0.5
 // (issued all at once: 4 % slower; some of them after the scores, so that they
 // arrive late: 3 to 9 %).
@@ -340,7 +340,7 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
         // The workgroup's queries go to LDS by lines, behind the first tile's
         // buffer, and from there to the waves' registers: straight from memory
         // every wave's loads would touch 32 lines each (decode of 1013 rows 20.4
-        // us).  Chunk c (16 bytes) of row r lies at place c ^ (r & 15), of its
+        // us, now 17.5).  Chunk c (16 bytes) of row r lies at place c ^ (r & 15), of its
         // position part at c ^ (r / 2 & 7).
         constexpr int kQueryRow = RANK * 2, kQueryRows = 1024 / kQueryRow, kQueryLoads = ROWS / kQueryRows / kWaves;
         static_assert(ROWS * (kQueryRow + kRopeWidth * 2) <= (kBuffers - 1) * kTileBytes, "queries");

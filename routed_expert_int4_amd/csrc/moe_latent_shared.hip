@@ -8,15 +8,15 @@
 // in runs of equal length each.  Either list leaves fp32 sums, maxima and
 // totals; a second launch joins them, a row's own first.
 //
-// Bound by what a tile of 64 keys costs 64 rows (2.5 us, the matrix cores 29 %
+// Bound by what a tile of 64 keys costs 64 rows (2.5 us, the matrix cores 31 %
 // busy), as in the form without prefixes; the cache's bytes do not count any
 // more.  Measured, rank 512, 64 heads: 32 tokens on a prefix of 16384 rows, up to
-// 500 own ones, 111 us (0.67 PFLOP/s, bf16; join 12); trees of 4 tokens of 16
-// sequences on prefixes of 8192 and 6554 rows, 8 bits, 128 us (0.53); 2 tokens
-// on 517 rows 25 us, a chain of latencies.  Where a token's heads fill 64 rows
+// 500 own ones, 103 us (0.72 PFLOP/s, bf16; join 12); trees of 4 tokens of 16
+// sequences on prefixes of 8192 and 6554 rows, 8 bits, 113 us (0.61); 2 tokens
+// on 517 rows 22.6 us, a chain of latencies.  Where a token's heads fill 64 rows
 // and the last-level cache holds the prefix, each sequence by itself over the
-// same pages takes as long (111); with fewer heads the rows of several tokens
-// share a tile (16 heads: 54 against 93).  (128 rows to a workgroup, whole rows in a wave: 272 accumulators, which
+// same pages takes as long; with fewer heads the rows of several tokens share a
+// tile (16 heads: 53 against 94).  (128 rows to a workgroup, whole rows in a wave: 272 accumulators, which
 // the compiler spills.)
 #include "moe_latent_device.h"
 
