@@ -421,8 +421,8 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                 const int r0 = i * kWaves + wave;
                 const unsigned lo = __builtin_amdgcn_readlane((unsigned)addr, r0),
                                hi = __builtin_amdgcn_readlane((unsigned)(addr >> 32), r0);
-                load_to_lds16((const void*)((unsigned long long)hi << 32 | lo), (unsigned)(chunk ^ place_mix(r0)) * 16,
-                              lds0 + buf * kTileBytes + r0 * kLatRow);
+                load_to_lds16_lane((unsigned long long)hi << 32 | lo, (unsigned)(chunk ^ place_mix(r0)) * 16,
+                                   lds0 + buf * kTileBytes + r0 * kLatRow);
             } else {
                 issue_from(i, buf, __shfl(addr, row_of(i, chunk)), chunk);
             }
