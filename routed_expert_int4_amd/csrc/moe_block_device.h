@@ -102,21 +102,20 @@ __device__ __forceinline__ void load_to_lds16(const void* src, unsigned dst) {
                  "s"(__builtin_amdgcn_readfirstlane(dst))
                  : "memory");
 }
-// The same from a wave-uniform base plus a byte offset per lane.
-__device__ __forceinline__ void load_to_lds16(const void* base, unsigned offset, unsigned dst) {
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)p), hi = __builtin_amdgcn_readfirstlane((unsigned)(p >> 32));
-    base = reinterpret_cast<const void*>((uint64_t)hi << 32 | lo);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base),
-                 "s"(__builtin_amdgcn_readfirstlane(dst))
-                 : "memory");
-}
-// The same from a base that lane reads have just made: a vector memory
-// instruction may read such a register five wait states later.
+// The same from a base in scalar registers plus a byte offset per lane.  A lane
+// read may just have made the base, here or in the caller, and a vector memory
+// instruction may read such a register five wait states later: s_mov and s_nop
+// are those, since the compiler adds none in front of inline assembly.
 __device__ __forceinline__ void load_to_lds16_lane(unsigned long long base, unsigned offset, unsigned dst) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base),
                  "s"(__builtin_amdgcn_readfirstlane(dst))
                  : "memory");
+}
+// The same from a wave-uniform base, wherever the compiler keeps it.
+__device__ __forceinline__ void load_to_lds16(const void* base, unsigned offset, unsigned dst) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)p), hi = __builtin_amdgcn_readfirstlane((unsigned)(p >> 32));
+    load_to_lds16_lane((uint64_t)hi << 32 | lo, offset, dst);
 }
 // Four bytes per lane into LDS: lane l's bytes land at dst + 4 l.
 __device__ __forceinline__ void load_to_lds4(const void* src, unsigned dst) {
