@@ -534,8 +534,9 @@ moe_status_t moe_latent_append(const uint16_t* d_kv, int64_t kv_stride, const vo
  * given, receives the rows in bf16 before their rounding to codes).  rank a
  * multiple of 16.
  * moe_latent_read_fp8: rows d_slots[t] as bf16, d_out [T][rank + rope]; a slot
- * outside [0, n_slots) reads as zeros.  What a prompt's key and value
- * expansion takes for tokens that are cached already. */
+ * outside [0, n_slots) reads as zeros.  A scale is read by its exponent alone, as
+ * in moe_latent_attention_shared.  What a prompt's key and value expansion takes
+ * for tokens that are cached already. */
 moe_status_t moe_latent_append_fp8(const uint16_t* d_kv, int64_t kv_stride, const void* d_weight, int weight_type,
                                    float eps, int rank, int rope, const float* d_table, int n_positions,
                                    const int32_t* d_positions, const int64_t* d_slots, int T, uint8_t* d_cache,
@@ -584,8 +585,10 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
  * tokens on them.
  * d_cache_scale NULL: d_cache is the bf16 cache.  Else it is the 8-bit one
  * above, page_stride counts its bytes, and d_cache_scale [n_pages][page_size]
- * holds the rows' powers of two (contiguous; anything else is read as the power
- * of two with its exponent).
+ * holds the rows' powers of two (contiguous).  Anything else is read as the power
+ * of two with its exponent, its sign and its other bits having no part: 0 and
+ * subnormal numbers count as 2^-127 at most, and a row with an infinity or NaN
+ * is NaN to the tokens that see it.
  * n_prefixes > 0: prefix i has d_prefix_lens[i] rows on pages d_prefix_pages[i *
  * prefix_pages_stride + j], j < pages_per_prefix, of the same pool, and belongs
  * to sequences d_groups[i] .. d_groups[i + 1] (int32 [n_prefixes + 1], not

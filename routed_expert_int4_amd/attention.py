@@ -375,7 +375,8 @@ def _narrow_rows(cache, cache_scale, row: int, on: int) -> int:
 def latent_read(cache, cache_scale, slots, rope: int = 64, out=None, stream=None) -> torch.Tensor:
     """Rows slots (int64 [T]) of a cache of 8 bits (uint8 [pages, page_size,
     rank + 2 rope] with cache_scale) as bf16 [T, rank + rope], which holds
-    their values exactly; a slot outside the cache reads as zeros."""
+    their values exactly; a slot outside the cache reads as zeros.  Scales are
+    read as powers of two, by their exponents alone, here and in attention."""
     on = cache.get_device()
     if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, latent_read, cache, cache_scale, slots, rope, out)
@@ -414,7 +415,8 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     moe_latent_attention_workspace() bytes (allocated per call if None).
 
     cache_scale (fp32 [pages, page_size], contiguous): the cache holds 8 bits,
-    as latent_append leaves it.  prefix: rows that sequences share, seen by
+    as latent_append leaves it (a scale that is no power of two counts as the
+    one with its exponent).  prefix: rows that sequences share, seen by
     their tokens before all of these (pages, lens, max_len and trees are of
     each sequence's own rows then); they are read once for all tokens on them
     (workspace: moe_latent_attention_shared_workspace() bytes)."""

@@ -255,6 +255,7 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
     // slot, reads those of wave ^ 1, and then owns what it has read.
     __shared__ u32x4 slots[kWaves][2][64];
     __shared__ float powers[kBuffers][NARROW ? kTile : 1];  // of the tiles' rows
+    __shared__ __attribute__((aligned(16))) unsigned value_powers[NARROW ? kTile : 1];  // of this tile's, as the weights take them
     __shared__ int pages_ahead[2][NARROW ? kTile : 1];       // of the tile after those
     const int lane = threadIdx.x & 63, wave = wave_in_block(), half = lane >> 5, col = lane & 31;
     const int rg = wave >> 2, quarter = wave & 3, side = quarter >> 1, inner = quarter & 1, other = wave ^ 1;
@@ -538,7 +539,8 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                     // chunk of the position part
                     constexpr int kPairs = kLat / 2, kItems = kPairs + kRope, kAhead = 4, kFirst = 1;
                     u32x4 x[kAhead];
-                    const float power = powers[buf][side * 32 + (col ^ inner * 16)];
+                    const int key = side * 32 + (col ^ inner * 16);
+                    const float power = powers[buf][key];
                     auto item = [&](int k) {
                         return __builtin_bit_cast(u32x4, lds_chunk(k < kPairs ? (key_at + tile) ^ k * 32 : rope_base[k - kPairs]));
                     };
@@ -554,7 +556,17 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                             mfma(sum, __builtin_bit_cast(bf16x8, u), qf[kLat + k - kPairs]);
                         }
                         if (k + kAhead < kItems) x[k % kAhead] = item(k + kAhead);
-                        if (k == kFirst) look_ahead();
+                        if (k == kFirst) {
+                            // The conversion goes by the scale's exponent, and so do
+                            // the weights.  One that is not finite counts as 2^127
+                            // there, for keys whose weight is zero; a row that sees
+                            // such a key has it in its score.  (All waves leave the
+                            // same values; masked by each wave for its own keys: 1 to
+                            // 2 % slower.)
+                            const unsigned exponent = __builtin_bit_cast(unsigned, power) & 0x7F800000u;
+                            value_powers[key] = exponent < 0x7F000000u ? exponent : 0x7F000000u;
+                            look_ahead();
+                        }
                         if (k > kFirst) {
                             constexpr int kFor = kItems - 1 - kFirst;
                             const int j = k - 1 - kFirst;
@@ -652,17 +664,12 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                     return values_transposed(lo[k] + at_key, hi[k] + at_key);
             };
             // The powers of two of the wave's keys, in the order of its
-            // scores: what a code stands for enters through the weights.  One
-            // that is not finite counts as another here, for keys whose weight
-            // is zero; a row that sees such a key has it in its score.
-            float power_of[NARROW ? 8 : 1];
+            // scores: what a code stands for enters through the weights.
+            f32x4 power_of[NARROW ? 2 : 1];
             if constexpr (NARROW) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const f32x4 u = *reinterpret_cast<const f32x4*>(&powers[buf][quarter * 16 + half * 4 + i * 2]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) power_of[i + j] = __builtin_amdgcn_fmed3f(u[j], 0.0f, 0x1p127f);
-                }
+                for (int i = 0; i < 2; ++i)
+                    power_of[i] = *reinterpret_cast<const f32x4*>(&value_powers[quarter * 16 + half * 4 + i * 8]);
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) x[j] = value_chunk(j);
@@ -682,7 +689,7 @@ __device__ __forceinline__ void attend(const LatentArgs& a, int total, int runs,
                     const float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
                     sum += e;
                     if constexpr (NARROW)
-                        p[i] = (__bf16)(e * power_of[i]);
+                        p[i] = (__bf16)(e * power_of[i / 4][i % 4]);
                     else
                         p[i] = (__bf16)e;
                 }
