@@ -219,14 +219,14 @@ def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -
 def quantize_weight_int4(w, group: int = 32):
     """A weight [N, K] in 4 bits with one fp16 scale per `group` (32, 64 or
     128) columns of a row, as int4_linear reads it: (codes uint8 [N, K / 2],
-    scales [N, K / group]).  The largest magnitude of a group gets code 7 or
-    -7.  Done once when a model is loaded, in torch."""
+    scales [N, K / group]), both contiguous.  The largest magnitude of a group gets
+    code 7 or -7.  Done once when a model is loaded, in torch."""
     N, K = w.shape
     _need(group in _GROUPS and K % group == 0, f"groups of {group} columns (32, 64 or 128) in rows of {K}")
     blocks = w.float().view(N, K // group, group)
-    scale = (blocks.abs().amax(2) / 7).clamp_(2.0 ** -24, 65504.0).half()  # finite, and not zero
+    scale = (blocks.abs().amax(2) / 7).clamp_(2.0 ** -24, 65504.0).half().contiguous()  # finite, and not zero
     q = (blocks / scale.float()[:, :, None]).round_().clamp_(-8, 7).view(N, K).to(torch.int32)
-    return ((q[:, 0::2] & 15) | (q[:, 1::2] & 15) << 4).to(torch.uint8), scale
+    return ((q[:, 0::2] & 15) | (q[:, 1::2] & 15) << 4).to(torch.uint8).contiguous(), scale
 
 
 def int4_linear(x, codes, scale, out_dtype=_BF16, out=None, stream=None) -> torch.Tensor:
