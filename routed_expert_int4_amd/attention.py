@@ -219,8 +219,10 @@ def fp8_linear(a, a_scale, w, w_scale, out_dtype=_BF16, out=None, stream=None) -
 def quantize_weight_int4(w, group: int = 32):
     """A weight [N, K] in 4 bits with one fp16 scale per `group` (32, 64 or
     128) columns of a row, as int4_linear reads it: (codes uint8 [N, K / 2],
-    scales [N, K / group]), both contiguous.  The largest magnitude of a group gets
-    code 7 or -7.  Done once when a model is loaded, in torch."""
+    scales [N, K / group]), both contiguous.  The largest magnitude of a group
+    gets code 7 or -7 where a seventh of it is a normal fp16 number; below, the
+    scale is a multiple of 2^-24, and weights over 7 x 65504 are cut.  Done once
+    when a model is loaded, in torch."""
     N, K = w.shape
     _need(group in _GROUPS and K % group == 0, f"groups of {group} columns (32, 64 or 128) in rows of {K}")
     blocks = w.float().view(N, K // group, group)
