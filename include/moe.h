@@ -600,7 +600,9 @@ moe_status_t moe_latent_attention(const uint16_t* d_q, int64_t q_stride_t, int64
  * right all the same).  Prefixes with d_groups that decrease or overlap are
  * unseen.  Fewer than 2^26 rows (tokens times heads) in all.
  * moe_latent_attention_shared_workspace: device bytes needed, as above; with
- * prefixes they hold fp32 sums of all T x heads rows twice. */
+ * prefixes they hold fp32 sums of all T x heads rows twice, 8 (rank + 2) bytes
+ * a row: 263 KB a token at rank 512 and 64 heads, so that long prompts behind a
+ * prefix go in chunks. */
 size_t moe_latent_attention_shared_workspace(int B, int T, int max_q, int heads, int rank, int max_len, int n_prefixes,
                                              int max_prefix_len);
 moe_status_t moe_latent_attention_shared(const uint16_t* d_q, int64_t q_stride_t, int64_t q_stride_h, int T, int heads,

@@ -421,7 +421,8 @@ def latent_attention(q, cache, pages, lens, scale: float, max_len: int | None = 
     one with its exponent).  prefix: rows that sequences share, seen by
     their tokens before all of these (pages, lens, max_len and trees are of
     each sequence's own rows then); they are read once for all tokens on them
-    (workspace: moe_latent_attention_shared_workspace() bytes)."""
+    (workspace: moe_latent_attention_shared_workspace() bytes, which grow with
+    the tokens: 8 heads (rank + 2) each)."""
     on = q.get_device()
     if stream is not None or on < 0 or on != _device():
         return _elsewhere(stream, latent_attention, q, cache, pages, lens, scale, max_len, cu_q, max_q, tree, out,

@@ -207,7 +207,11 @@ class LatentCache:
     def share(self, b: int) -> None:
         """Makes the rows of sequence b the prefix of all sequences: they are
         before each one's own rows from now on, b's own being none.  All other
-        sequences have to be empty, and b without undecided drafts."""
+        sequences have to be empty, and b without undecided drafts.  It is held
+        once.  Steps on a long one take less time than with its pages in every
+        sequence's own list where a token has fewer than 64 heads (32 sequences
+        on 16384 rows, 16 heads: 51 against 93 us); with 64, or after a few
+        thousand rows, as much or up to a fifth more."""
         if self.prefix is not None:
             raise ValueError("there is a prefix already: drop_prefix() first")
         others = [n for i, n in enumerate(self.host_lens) if i != b]
@@ -302,7 +306,9 @@ class DecoderBlock:
     def prompt(self, delta, residual, cache: LatentCache, counts):
         """Prompts of counts[b] tokens, one after another in delta and
         residual [T, hidden], for sequences that have no rows yet and no
-        prefix (decode() takes a whole prompt as one chunk after either)."""
+        prefix (decode() takes a whole prompt as one chunk after either; behind
+        a prefix each of its tokens takes 8 heads (rank + 2) bytes of workspace,
+        540 MB for 2048 at 64 heads and rank 512, so long ones go in several)."""
         cfg = self.cfg
         if cache.prefix is not None or any(n and have for n, have in zip(counts, cache.host_lens)):
             raise ValueError("prompt() starts sequences; decode() continues them")

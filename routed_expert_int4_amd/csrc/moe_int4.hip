@@ -16,10 +16,13 @@
 //
 // Few tokens are bound by reading the weights, and a load by the lines that it
 // touches, some two cycles each: 32 bytes of 32 rows cost four times what 128
-// bytes of eight do.  Many are bound by what the vector unit does beside the
-// matrix cores, and the two overlap only in part: 64 columns of a wave's 64 x 96
-// results are 32 matrix instructions and 370 others, 192 of them the scaling of
-// the groups' sums (for every result and group, whatever the tile).
+// bytes of eight do.  Many are bound by no one thing: 64 columns of a wave's 64 x
+// 96 results are 32 matrix instructions and 370 others, 192 of them the scaling
+// of the groups' sums (for every result and group, whatever the tile).  Counted,
+// the matrix cores are busy for 40 % of the time and the others take 59 % of the
+// SIMDs' cycles; the two overlap in part, and the waves wait for a third of their
+// time.  The scaling does not hold it: at group 128 there are 272 others, 43 % of
+// the cycles, of which there are as many, and 4 to 8 % less time among other calls.
 //
 // Measured, 6144 x 8192, group 32 (25 MB of codes, 3 of scales): 1 token 9.6 us
 // (3.0 TB/s, a quarter of it launch and first latency; 49152 rows 51 us, 4.4
@@ -573,10 +576,12 @@ __global__ void __launch_bounds__(WT * WN * 64, PER_SIMD) int4_many_kernel(Int4A
     const unsigned lds0 = lds_address(lds);
     // Addresses are a base for the tile and the stage and an offset that a lane
     // keeps; rows past the last one repeat it.  Chunk c of row r of the
-    // activations lies at place c ^ (r & 7), of the weights at c ^ (r / 4 & 3):
-    // the rows of an operand read cover all banks.  (What bounds loads is the
-    // number of lines that they touch: weights straight into operand order
-    // would be 32 lines to a load of 1 KB.)
+    // activations lies at place c ^ (r & 7), of the weights at c ^ (r / 4 & 3).
+    // The weights' operand reads cover all banks; rows of activations that are
+    // eight apart share theirs, and at group 32 scales of rows sixteen apart
+    // (conflicts are counted for 11 % of a compute unit's cycles at group 32, 5 %
+    // at 128).  (What bounds loads is the number of lines that they touch: weights
+    // straight into operand order would be 32 lines to a load of 1 KB.)
     unsigned x_off[kLoads], w_off[kChunkLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -784,6 +789,10 @@ int best_shape(const Int4Args& a) {
     return best;
 }
 
+// Dot products or a matrix tile, us on one card: one token 2048 x 6144 7.0 and
+// 7.1, 6144 x 8192 10.2 and 12.3 (group 128 9.7 and 11.3), 12288 x 2048 7.1 and 7.4,
+// 49152 x 8192 49.5 and 61.1; two tokens 6.5 and 7.0, 12.4 and 12.3 (11.8 and 11.3),
+// 7.4 and 7.3, 61.0 and 61.3.
 template <int GROUP>
 void launch_group(const Int4Args& a, hipStream_t s) {
     if (a.M == 1) return launch_few<GROUP, 1>(a, s);

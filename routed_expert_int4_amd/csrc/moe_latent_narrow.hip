@@ -10,7 +10,7 @@
 // costs its workgroup, 2.47 us, about equally: 32 sequences of 16384 rows 111 us
 // (3.1 TB/s; 103 without the loads), the bf16 cache 132 to 141.  Several tokens are
 // bound by instructions: a wave has 34 matrix instructions to a tile, 128
-// conversions and some 180 other vector instructions, which the matrix cores do
+// conversions and some 175 other vector instructions, which the matrix cores do
 // not hide: 11 x 5 tokens (trees) over 9001 ragged rows 76 us (0.56 PFLOP/s), of
 // which the join takes 9 and the runs' beginnings and ends some 12.  Loads moved
 // between the scores, the exchange and the values: no difference; the two groups

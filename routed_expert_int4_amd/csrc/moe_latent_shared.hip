@@ -13,10 +13,12 @@
 // more.  Measured, rank 512, 64 heads: 32 tokens on a prefix of 16384 rows, up to
 // 500 own ones, 103 us (0.72 PFLOP/s, bf16; join 12); trees of 4 tokens of 16
 // sequences on prefixes of 8192 and 6554 rows, 8 bits, 113 us (0.61); 2 tokens
-// on 517 rows 22.6 us, a chain of latencies.  Where a token's heads fill 64 rows
-// and the last-level cache holds the prefix, each sequence by itself over the
-// same pages takes as long; with fewer heads the rows of several tokens share a
-// tile (16 heads: 53 against 94).  (128 rows to a workgroup, whole rows in a wave: 272 accumulators, which
+// on 517 rows 22.6 us, a chain of latencies.  Where a token's heads fill 64 rows,
+// each sequence by itself over the same pages takes as long, a few per cent less
+// (8 prefixes of 32768 rows, 302 MB, 4 tokens on each: 202 against 219) and up to
+// a fifth less where there is little to do (8 tokens on 4096 rows: 34 against
+// 39); with fewer heads the rows of several tokens share a tile (16 heads: 51
+// against 93).  (128 rows to a workgroup, whole rows in a wave: 272 accumulators, which
 // the compiler spills.)
 #include "moe_latent_device.h"
 

@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendArgs a) {
         if (row8) {
             // One power of two for the row, from its largest finite value, so
             // that a code times it is exact in bf16 and a code is off by 2^-4
-            // of its value; what is not finite becomes NaN.  (8192 tokens with
+            // of its value, or 2^-10 of the power of two where that is more
+            // (below 2^-17 of the row's largest); what is not finite becomes NaN.  (8192 tokens with
             // the queries of 64 heads: 34.7 us, 4.3 TB/s.)
             unsigned top = 0;
 #pragma unroll
